@@ -23,7 +23,7 @@ __all__ = [
     "aq_embedding", "aq_qmv", "aq_qmm",
     "aq_quantized_matmul", "aq_gather_qmv", "aq_gather_qmm", "aq_gather_quantized_matmul",
     "aq_quantize_fp", "aq_dequantize_fp", "aq_qmv_fp", "aq_matmul_fp", "aq_gather_matmul_fp", "aq_qmv_fp_describe",
-    "FP_MODES",
+    "FP_MODES", "aq_kv_append", "aq_kv_read", "aq_paged_attention", "aq_paged_attention_workspace",
 ]
 
 AQ_OK = 0
@@ -42,6 +42,15 @@ class AQError(RuntimeError):
         msg = _lib.aq_status_string(status).decode() if _lib is not None else str(status)
         super().__init__(f"{fn}: {msg} (status {status})")
         self.status = status
+
+
+class _KVCache(ctypes.Structure):
+    """aq_kv_cache of include/aq.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "k_biases",
+                                                "v_codes", "v_scales", "v_biases")]
+                + [("num_pages", ctypes.c_int64)]
+                + [(n, ctypes.c_int32) for n in ("page_size", "kv_heads", "head_dim", "group_size",
+                                                 "bits", "dtype")])
 
 
 _lib = None
@@ -85,6 +94,11 @@ def load_library():
         "aq_gather_matmul_fp": ([vp, i32, i64, vp, vp, i64, i64, i64, vp, i32, i32, i32, vp, vp],
                                 i32),
         "aq_qmv_fp_describe": ([i64, i64, i32, i32, ctypes.c_char_p, i32], i32),
+        "aq_kv_append": ([vp, vp, i32, i64, i64, i64, vp, vp, vp], i32),
+        "aq_kv_read": ([vp, i64, vp, vp, vp, i32, vp], i32),
+        "aq_paged_attention": ([vp, i32, i64, i32, i32, i64, vp, vp, i64, vp, ctypes.c_float, vp,
+                                vp, i64, vp], i32),
+        "aq_paged_attention_workspace": ([i64, i32, i32, i32, i32], i64),
         "aq_bench_stream_read": ([vp, i64, i32, i32, vp, vp], i32),
         "aq_bench_read_oneshot": ([vp, i64, i32, i32, vp, vp], i32),
         "aq_bench_mfma_clock": ([i32, i32, vp, vp], i32),
@@ -459,3 +473,157 @@ def aq_qmv_fp_describe(N: int, K: int, mode: str, x_dtype="f16") -> str:
     if n < 0:
         raise AQError(-1, "aq_qmv_fp_describe")
     return buf.value.decode()
+
+
+# ---- key-value cache and attention ------------------------------------------------------
+# A cache is three arrays for K and three for V: codes int32 [pages, kv_heads, page_size,
+# head_dim*bits/32], scales and biases fp16 [pages, kv_heads, page_size, head_dim/group_size];
+# with bits = 16 the codes are the values, fp16 or bf16 [pages, kv_heads, page_size, head_dim],
+# and scales and biases are None.
+def _rows(t, name):
+    """Device address of [tokens, heads, head_dim] rows, heads and head_dim contiguous, and the
+    tokens' distance in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    stride, inner, last = t.stride()
+    _, h, d = t.shape
+    if last != 1 or (h > 1 and inner != d):
+        raise ValueError(f"{name}: heads and head_dim must be contiguous")
+    return t.data_ptr(), (stride if t.shape[0] > 1 else h * d)
+
+
+def _cache_array(t, dtype, shape, name):
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, {dtype} expected")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} expected")
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous device tensor")
+    return t.data_ptr()
+
+
+def _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits):
+    torch = _torch()
+    pages, heads, page, words = shape = k_codes.shape
+    if bits == 16:
+        dim, kind, code = words, k_codes.dtype, _dtype_code(k_codes)
+        if code == AQ_F32:
+            raise TypeError("a 16-bit cache holds float16 or bfloat16")
+        scales = (None, None, None, None)
+        group_size = 0
+    else:
+        if bits not in (4, 8):
+            raise AQError(-2 if 2 <= bits <= 8 else -1, "aq_kv_cache")
+        dim, kind, code = words * 32 // bits, torch.int32, 0
+        if group_size < 1 or dim % group_size:
+            raise AQError(-1, "aq_kv_cache")
+        groups = (pages, heads, page, dim // group_size)
+        half = torch.float16
+        scales = (_cache_array(k_scales, half, groups, "k_scales"),
+                  _cache_array(k_biases, half, groups, "k_biases"),
+                  _cache_array(v_scales, half, groups, "v_scales"),
+                  _cache_array(v_biases, half, groups, "v_biases"))
+    return _KVCache(_cache_array(k_codes, kind, shape, "k_codes"), scales[0], scales[1],
+                    _cache_array(v_codes, kind, shape, "v_codes"), scales[2], scales[3],
+                    pages, page, heads, dim, group_size, bits, code)
+
+
+def _index(t, dtype, name):
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, {dtype} expected")
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous device tensor")
+    return t.data_ptr()
+
+
+def aq_kv_append(k, v, slots, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases,
+                 group_size: int, bits: int, stream=None):
+    """Quantize k, v [T, kv_heads, head_dim] (fp16/bf16; tokens may be strided) into the cache at
+    slots int64 [T] = page * page_size + place (outside the cache: not written)."""
+    cache = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
+    T = slots.numel()
+    shape = (T, cache.kv_heads, cache.head_dim)
+    if tuple(k.shape) != shape or tuple(v.shape) != shape or k.dtype != v.dtype:
+        raise ValueError(f"aq_kv_append: k and v must be {shape} of one dtype")
+    kp, ks = _rows(k, "k")
+    vp, vs = _rows(v, "v")
+    st = load_library().aq_kv_append(kp, vp, _dtype_code(k), T, ks, vs,
+                                     _index(slots, _torch().int64, "slots"), ctypes.byref(cache),
+                                     _stream(stream))
+    _check(st, "aq_kv_append")
+
+
+def aq_kv_read(slots, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size: int,
+               bits: int, out_dtype=None, k=None, v=None, stream=None):
+    """Rows of the cache at slots int64 [T] -> (k, v) [T, kv_heads, head_dim] in out_dtype
+    (default fp16); a slot outside the cache gives zeros."""
+    torch = _torch()
+    cache = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
+    T = slots.numel()
+    shape = (T, cache.kv_heads, cache.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=out_dtype or torch.float16, device=slots.device)
+    if v is None:
+        v = torch.empty(shape, dtype=k.dtype, device=slots.device)
+    if tuple(k.shape) != shape or tuple(v.shape) != shape or k.dtype != v.dtype:
+        raise ValueError(f"aq_kv_read: k and v must be {shape} of one dtype")
+    st = load_library().aq_kv_read(_index(slots, torch.int64, "slots"), T, ctypes.byref(cache),
+                                   _dev(k, "k"), _dev(v, "v"), _dtype_code(k), _stream(stream))
+    _check(st, "aq_kv_read")
+    return k, v
+
+
+def aq_paged_attention_workspace(B: int, L: int, q_heads: int, kv_heads: int,
+                                 head_dim: int) -> int:
+    """Bytes of workspace aq_paged_attention needs for this shape."""
+    n = int(load_library().aq_paged_attention_workspace(B, L, q_heads, kv_heads, head_dim))
+    if n < 0:
+        raise AQError(-1, "aq_paged_attention_workspace")
+    return n
+
+
+def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, page_table,
+                       lengths, group_size: int, bits: int, scale: float | None = None, out=None,
+                       workspace=None, stream=None):
+    """Attention of the newest L tokens of every sequence over the paged cache: q [B, L, q_heads,
+    head_dim] or [B, q_heads, head_dim] (L = 1; tokens may be strided), page_table int32 [B,
+    max_pages], lengths int32 [B] (cached tokens, the L new ones included) -> out of q's shape.
+    scale: default head_dim ** -0.5.  workspace: a device buffer zeroed once (see
+    aq_paged_attention_workspace); without one each call makes and clears its own."""
+    torch = _torch()
+    lib = load_library()
+    cache = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
+    dim = cache.head_dim
+    if q.dim() == 3:
+        B, Hq, D = q.shape
+        L, rows = 1, q
+    else:
+        B, L, Hq, D = q.shape
+        if L == 1:
+            rows = q[:, 0]
+        elif B == 1 or q.stride(0) == L * q.stride(1):
+            rows = q.as_strided((B * L, Hq, D), (q.stride(1), q.stride(2), q.stride(3)))
+        else:
+            raise ValueError("q: all tokens must lie at one distance")
+    if D != dim:
+        raise ValueError(f"q: head_dim {D}, the cache has {dim}")
+    if page_table.dim() != 2 or page_table.shape[0] != B or lengths.numel() != B:
+        raise ValueError(f"page_table must be [{B}, max_pages] and lengths [{B}]")
+    qp, qs = _rows(rows, "q")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    if workspace is None:
+        need = lib.aq_paged_attention_workspace(B, L, Hq, cache.kv_heads, dim)
+        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
+    st = lib.aq_paged_attention(qp, _dtype_code(q), B, L, Hq, qs, ctypes.byref(cache),
+                                _index(page_table, torch.int32, "page_table"),
+                                page_table.shape[1], _index(lengths, torch.int32, "lengths"),
+                                dim ** -0.5 if scale is None else scale, _dev(out, "out"),
+                                _dev(workspace, "workspace"),
+                                workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "aq_paged_attention")
+    return out

@@ -61,6 +61,49 @@ aq_status check_matmul(const void *x, int x_dtype, int64_t M, const uint32_t *co
   return AQ_OK;
 }
 
+// shape of a cache; the arrays follow in check_cache_arrays
+aq_status check_cache(const aq_kv_cache *c) {
+  if (!c) return AQ_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->head_dim < 1)
+    return AQ_ERR_INVALID_ARG;
+  if (c->bits != 4 && c->bits != 8 && c->bits != 16)
+    return c->bits >= 2 && c->bits <= 8 ? AQ_ERR_UNSUPPORTED : AQ_ERR_INVALID_ARG;
+  if (c->bits == 16) {
+    if (!valid_act_dtype(c->dtype)) return AQ_ERR_INVALID_ARG;
+  } else if ((c->group_size != 32 && c->group_size != 64 && c->group_size != 128) ||
+             c->head_dim % c->group_size != 0) {
+    return AQ_ERR_INVALID_ARG;
+  }
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return AQ_ERR_UNSUPPORTED;
+  if (c->page_size % 16 != 0 || c->num_pages > 0x7FFFFFFF) return AQ_ERR_UNSUPPORTED;
+  if (c->kv_heads > (1 << 28) || (int64_t)c->kv_heads * c->head_dim > (1 << 28) / c->page_size)
+    return AQ_ERR_UNSUPPORTED;
+  return AQ_OK;
+}
+
+// the consumers take null bias arrays as every bias +0; the writer needs them
+aq_status check_cache_arrays(const aq_kv_cache *c, bool need_biases) {
+  if (!c->k_codes || !c->v_codes) return AQ_ERR_INVALID_ARG;
+  if (!aligned16(c->k_codes) || !aligned16(c->v_codes)) return AQ_ERR_ALIGNMENT;
+  if (c->bits == 16) return AQ_OK;
+  if (!c->k_scales || !c->v_scales || (need_biases && (!c->k_biases || !c->v_biases)))
+    return AQ_ERR_INVALID_ARG;
+  if (!aligned16(c->k_scales) || !aligned16(c->v_scales) || !aligned16(c->k_biases) ||
+      !aligned16(c->v_biases))
+    return AQ_ERR_ALIGNMENT;
+  return AQ_OK;
+}
+
+aq_status check_attention_shape(int64_t B, int L, int q_heads, int kv_heads, int head_dim) {
+  if (B < 1 || L < 1 || L > 8 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0)
+    return AQ_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return AQ_ERR_UNSUPPORTED;
+  if (B >= (1 << 24) || q_heads >= (1 << 24) || B * L >= (1 << 24) ||
+      B * L * q_heads >= (1 << 24))
+    return AQ_ERR_UNSUPPORTED;
+  return AQ_OK;
+}
+
 }  // namespace
 
 namespace aq {
@@ -400,6 +443,76 @@ int aq_qmv_fp_describe(int64_t N, int64_t K, aq_fp_mode mode, aq_dtype x_dtype, 
   if (cpl == 0) return snprintf(buf, (size_t)len, "qmv1_fp_lds_kernel<%s, %s, W=%d>", mt, xt, w);
   return snprintf(buf, (size_t)len, "qmv1_fp_kernel<%s, %s, CPL=%d, UD=%d, W=%d>", mt, xt, cpl, ud,
                   w);
+}
+
+aq_status aq_kv_append(const void *k, const void *v, aq_dtype x_dtype, int64_t T, int64_t k_stride,
+                       int64_t v_stride, const int64_t *slots, const aq_kv_cache *cache,
+                       void *stream) {
+  aq_status st = check_cache(cache);
+  if (st != AQ_OK) return st;
+  if (!valid_act_dtype(x_dtype) || T < 0) return AQ_ERR_INVALID_ARG;
+  if (cache->bits == 16 && (int)x_dtype != cache->dtype) return AQ_ERR_INVALID_ARG;
+  const int64_t width = (int64_t)cache->kv_heads * cache->head_dim;
+  if (k_stride < width || v_stride < width || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return AQ_ERR_INVALID_ARG;
+  st = check_cache_arrays(cache, true);
+  if (st != AQ_OK || T == 0) return st;
+  if (!k || !v || !slots) return AQ_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(slots)) return AQ_ERR_ALIGNMENT;
+  if (T > ((int64_t)0x7FFFFFFF * 256) / (width / 8)) return AQ_ERR_UNSUPPORTED;
+  if (k_stride > ((int64_t)1 << 62) / T || v_stride > ((int64_t)1 << 62) / T)
+    return AQ_ERR_UNSUPPORTED;
+  return from_hip(aq::launch_kv_append(k, v, (int)x_dtype, T, k_stride, v_stride, slots, *cache,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+aq_status aq_kv_read(const int64_t *slots, int64_t T, const aq_kv_cache *cache, void *k, void *v,
+                     aq_dtype out_dtype, void *stream) {
+  aq_status st = check_cache(cache);
+  if (st != AQ_OK) return st;
+  if (T < 0 || (out_dtype != AQ_F32 && out_dtype != AQ_F16 && out_dtype != AQ_BF16))
+    return AQ_ERR_INVALID_ARG;
+  st = check_cache_arrays(cache, false);
+  if (st != AQ_OK || T == 0) return st;
+  if (!k || !v || !slots) return AQ_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(slots)) return AQ_ERR_ALIGNMENT;
+  if (T > ((int64_t)0x7FFFFFFF * 256) / ((int64_t)cache->kv_heads * cache->head_dim / 8))
+    return AQ_ERR_UNSUPPORTED;
+  return from_hip(aq::launch_kv_read(slots, T, *cache, k, v, (int)out_dtype,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+int64_t aq_paged_attention_workspace(int64_t B, int L, int q_heads, int kv_heads, int head_dim) {
+  if (check_attention_shape(B, L, q_heads, kv_heads, head_dim) != AQ_OK) return -1;
+  return aq::attn_workspace_bytes(B, L, q_heads, kv_heads, head_dim);
+}
+
+aq_status aq_paged_attention(const void *q, aq_dtype x_dtype, int64_t B, int L, int q_heads,
+                             int64_t q_stride, const aq_kv_cache *cache, const int32_t *page_table,
+                             int64_t max_pages, const int32_t *lengths, float scale, void *out,
+                             void *workspace, int64_t workspace_bytes, void *stream) {
+  aq_status st = check_cache(cache);
+  if (st != AQ_OK) return st;
+  if (!valid_act_dtype(x_dtype) || max_pages < 1) return AQ_ERR_INVALID_ARG;
+  if (cache->bits == 16 && (int)x_dtype != cache->dtype) return AQ_ERR_INVALID_ARG;
+  st = check_attention_shape(B, L, q_heads, cache->kv_heads, cache->head_dim);
+  if (st != AQ_OK) return st;
+  if (q_stride < (int64_t)q_heads * cache->head_dim || q_stride % 8 != 0)
+    return AQ_ERR_INVALID_ARG;
+  if (q_stride > ((int64_t)1 << 62) / (B * L)) return AQ_ERR_UNSUPPORTED;
+  if (max_pages > 0x7FFFFFFF / cache->page_size) return AQ_ERR_UNSUPPORTED;
+  st = check_cache_arrays(cache, false);
+  if (st != AQ_OK) return st;
+  if (!q || !page_table || !lengths || !out || !workspace) return AQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(page_table) || !aligned16(lengths) || !aligned16(out) ||
+      !aligned16(workspace))
+    return AQ_ERR_ALIGNMENT;
+  if (workspace_bytes <
+      aq::attn_workspace_bytes(B, L, q_heads, cache->kv_heads, cache->head_dim))
+    return AQ_ERR_INVALID_ARG;
+  const aq::AttnArgs a = {q,     q_stride,     page_table, lengths, out,    workspace,
+                          max_pages, scale, (int)x_dtype, (int)B,     L,       q_heads};
+  return from_hip(aq::launch_paged_attention(a, *cache, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -149,4 +149,25 @@ __device__ __forceinline__ void load32(const void *__restrict__ base, int64_t e,
   for (int j = 0; j < 4; ++j) load8<WDT>(base, e + 8 * j, v + 8 * j);
 }
 
+// ---- stores: 8 consecutive values at element e, rounded to nearest even -------------
+
+template <int ODT>
+__device__ __forceinline__ void store8(void *__restrict__ base, int64_t e, const float *v) {
+  if constexpr (ODT == X_F32) {
+    float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(base) + e);
+    p[0] = make_float4(v[0], v[1], v[2], v[3]);
+    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (ODT == X_F16)
+        u[i] = __builtin_bit_cast(uint32_t, half2v{(_Float16)v[2 * i], (_Float16)v[2 * i + 1]});
+      else
+        u[i] = __builtin_bit_cast(uint32_t, bf16x2v{(__bf16)v[2 * i], (__bf16)v[2 * i + 1]});
+    }
+    *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(base) + e) = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+}
+
 }  // namespace aq

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "aq.h"
+
 namespace aq {
 
 enum XType { X_F32 = 0, X_F16 = 1, X_BF16 = 2 };
@@ -102,5 +104,28 @@ hipError_t launch_gather_mm_fp(const void *x, int x_dtype, int64_t Tk, const uin
                                const uint8_t *scales, int64_t E, int64_t N, int64_t K,
                                const int32_t *ids, int topk, int mode, int T, void *y,
                                hipStream_t s);
+
+// the paged key-value cache: rows quantized as they are written, read back,
+// and the attention of each sequence's newest tokens over it
+using KvCache = aq_kv_cache;
+hipError_t launch_kv_append(const void *k, const void *v, int x_dtype, int64_t T, int64_t k_stride,
+                            int64_t v_stride, const int64_t *slots, const KvCache &c,
+                            hipStream_t s);
+hipError_t launch_kv_read(const int64_t *slots, int64_t T, const KvCache &c, void *k, void *v,
+                          int out_dtype, hipStream_t s);
+struct AttnArgs {
+  const void *q;
+  int64_t q_stride;
+  const int32_t *page_table;
+  const int32_t *lengths;
+  void *out;
+  void *workspace;
+  int64_t max_pages;
+  float scale;
+  int x_dtype;
+  int B, L, q_heads;
+};
+int64_t attn_workspace_bytes(int64_t B, int L, int q_heads, int kv_heads, int head_dim);
+hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream_t s);
 
 }  // namespace aq

@@ -367,6 +367,105 @@ aq_status aq_gather_matmul_fp(const void *x, aq_dtype x_dtype, int64_t T, const 
 int aq_qmv_fp_describe(int64_t N, int64_t K, aq_fp_mode mode, aq_dtype x_dtype, char *buf,
                        int len);
 
+/* ---- key-value cache and attention ---------------------------------------
+ *
+ * A paged cache of attention keys and values in the format above, one packed
+ * row per token and head: the head_dim values of a token's key (or value) in
+ * one head are cut into groups of group_size along head_dim, each group
+ * stored as `bits`-bit codes, one fp16 scale and one fp16 bias, w = q*s + b.
+ * Page p holds page_size consecutive tokens of one sequence, all heads:
+ *
+ *   codes   uint32 [num_pages, kv_heads, page_size, head_dim*bits/32]
+ *   scales  uint16 [num_pages, kv_heads, page_size, head_dim/group_size]
+ *   biases  uint16, the same shape
+ *
+ * for K and for V.  With bits = 16 the code arrays hold the values themselves,
+ * [num_pages, kv_heads, page_size, head_dim] in `dtype` (AQ_F16 or AQ_BF16);
+ * scales and biases are then not looked at (may be NULL) and neither is
+ * group_size.  A token's slot is page * page_size + its place in the page.
+ *
+ * Supported: bits 4, 8, 16; head_dim 64, 128, 256; group_size 32, 64, 128
+ * dividing head_dim; page_size a multiple of 16; kv_heads * page_size *
+ * head_dim <= 2^28 (a page is addressed with 32-bit offsets); the cache
+ * itself may be of any size.  AQ_ERR_INVALID_ARG / AQ_ERR_UNSUPPORTED
+ * otherwise.  All arrays are device memory, 16-byte aligned. */
+typedef struct aq_kv_cache {
+  void *k_codes;
+  uint16_t *k_scales;
+  uint16_t *k_biases;
+  void *v_codes;
+  uint16_t *v_scales;
+  uint16_t *v_biases;
+  int64_t num_pages;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t group_size;
+  int32_t bits;
+  int32_t dtype; /* aq_dtype of the pages when bits = 16, not looked at otherwise */
+} aq_kv_cache;
+
+/* Quantize keys and values into the cache as they are written: token t's rows
+ * k[t, h, :] and v[t, h, :] go to slots[t], each group by the rule of
+ * aq_quantize (the codes, scales and biases are those aq_quantize gives for
+ * the row).  k, v: device, x_dtype AQ_F16 or AQ_BF16, heads and head_dim
+ * contiguous, tokens k_stride and v_stride elements apart (multiples of 8, at
+ * least kv_heads * head_dim), so both may be parts of one projection's rows.
+ * slots: device int64 [T]; a slot outside [0, num_pages * page_size) writes
+ * nothing; two equal slots in one call leave either token's rows, group by
+ * group.  Values are clamped to fp16's finite range first; a group that holds
+ * a NaN gets scale 0, bias NaN and codes 0, so all of it reads back as NaN.
+ * bits = 16: x_dtype must be the cache's dtype, rows are copied as they are.
+ * T = 0 does nothing.  Scales and biases are required unless bits = 16. */
+aq_status aq_kv_append(const void *k, const void *v, aq_dtype x_dtype, int64_t T, int64_t k_stride,
+                       int64_t v_stride, const int64_t *slots, const aq_kv_cache *cache,
+                       void *stream);
+
+/* Read rows of the cache back: k[t, h, :] and v[t, h, :] = the rows of
+ * slots[t], q*s + b as aq_dequantize rounds it into out_dtype (AQ_F32, AQ_F16
+ * or AQ_BF16).  k, v: device [T, kv_heads, head_dim].  A slot outside the
+ * cache reads nothing and gives zero rows.  NULL bias arrays: every bias +0.
+ * T = 0 does nothing. */
+aq_status aq_kv_read(const int64_t *slots, int64_t T, const aq_kv_cache *cache, void *k, void *v,
+                     aq_dtype out_dtype, void *stream);
+
+/* Attention of the newest tokens of each sequence over the paged cache.  For
+ * sequence b of B, its last L (1..8) tokens, query head h and j = h / (q_heads
+ * / kv_heads):
+ *
+ *   out[b, i, h, :] = sum_t p_t v[t, j, :],   p = softmax_t(scale * q[b, i, h, :] . k[t, j, :])
+ *
+ * over the cached tokens t <= len - L + i, len = lengths[b] clamped to
+ * [0, max_pages * page_size], which counts the L tokens themselves (append
+ * them first).  Token t of the sequence is at place t % page_size of page
+ * page_table[b, t / page_size]; the tokens of a page id outside
+ * [0, num_pages) are left out, and nothing past len is looked at, whatever
+ * it holds.  A row that sees no token is zero.
+ *
+ * q: device, x_dtype AQ_F16 or AQ_BF16 (bits = 16: the cache's dtype), rows
+ * [q_heads, head_dim] contiguous, token b*L + i at q + (b*L + i) * q_stride
+ * elements (a multiple of 8, at least q_heads * head_dim).  out: device [B, L,
+ * q_heads, head_dim] in x_dtype.  page_table: device int32 [B, max_pages].
+ * lengths: device int32 [B].  q_heads a multiple of kv_heads.  Scores and
+ * softmax statistics are held in binary32.  NULL bias arrays: every bias +0.
+ *
+ * workspace: device memory of aq_paged_attention_workspace bytes, 16-byte
+ * aligned, cleared (zeroed) once before its first use; every call leaves it
+ * fit for the next one, of any shape it is large enough for.  Calls that may
+ * run at the same time need workspaces of their own.  The launch does not
+ * depend on the lengths, so a captured graph follows them as they grow.
+ * AQ_ERR_INVALID_ARG when workspace_bytes is too small, B < 1, L outside
+ * 1..8; AQ_ERR_UNSUPPORTED for max_pages * page_size >= 2^31 or B * L *
+ * q_heads >= 2^24. */
+aq_status aq_paged_attention(const void *q, aq_dtype x_dtype, int64_t B, int L, int q_heads,
+                             int64_t q_stride, const aq_kv_cache *cache, const int32_t *page_table,
+                             int64_t max_pages, const int32_t *lengths, float scale, void *out,
+                             void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace aq_paged_attention needs for this shape (at most 64 MiB);
+ * -1 on bad arguments.  May query the current device's compute-unit count. */
+int64_t aq_paged_attention_workspace(int64_t B, int L, int q_heads, int kv_heads, int head_dim);
+
 #ifdef __cplusplus
 }
 #endif

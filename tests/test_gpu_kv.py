@@ -1,0 +1,492 @@
+"""The key-value cache and its attention on the GPU: rows quantized into the
+cache are bit for bit what the oracle's quantizer gives, rows read back what
+its dequantizer gives, and attention is held to the binary64 formula within
+the bound that kv_ref.attention derives."""
+import numpy as np
+import pytest
+
+import kv_ref
+import oracle
+from gpu_util import out_bits, out_to_f64, torch_dtype
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def aq():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import group_wise_affine_aq_amd as mod
+    mod.load_library()
+    return mod
+
+
+def _rows(rng, shape):
+    """Values with loud channels, constant groups, zeros and negative zeros."""
+    x = rng.standard_normal(shape)
+    x[..., ::29] *= 6
+    x[0] = 0.25
+    if shape[0] > 1:
+        x[1] = np.where(rng.random(shape[1:]) < 0.5, -0.0, 0.0)
+    return x
+
+
+def _dev16(bits, dtype):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).cuda().view(torch_dtype(dtype))
+
+
+def _cache_bits(t):
+    import torch
+    return t.view(torch.int16).cpu().numpy().view(np.uint16) if t.dtype != torch.int32 else \
+        t.cpu().numpy().view(np.uint32)
+
+
+SHAPES = [  # tokens, heads, dim, group, page
+    (1, 1, 64, 32, 16), (3, 5, 64, 64, 48), (37, 8, 128, 64, 16), (130, 2, 128, 128, 32),
+    (65, 3, 128, 32, 64), (9, 1, 256, 64, 16), (33, 4, 256, 128, 16), (17, 2, 256, 32, 96)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("bits", [4, 8, 16])
+@pytest.mark.parametrize("T,H,D,G,page", SHAPES)
+def test_append_and_read(aq, T, H, D, G, page, bits, dtype):
+    import torch
+    rng = np.random.default_rng(T * 1000 + D + bits)
+    pages = T // page + 4
+    want = kv_ref.Cache(pages, H, page, D, G, bits, dtype)
+    got = want.device()
+    slots = rng.permutation(pages * page)[:T].astype(np.int64)
+    drop = rng.random(T) < 0.15  # tokens that are not to be written
+    slots[drop] = rng.choice([-1, pages * page, -(1 << 40), 1 << 40], drop.sum())
+    kb, kx = kv_ref.to_bits(_rows(rng, (T, H, D)), dtype)
+    vb, vx = kv_ref.to_bits(_rows(rng, (T, H, D)), dtype)
+    # tokens strided, as parts of a wider projection; V at another distance
+    wide = torch.zeros((T, 3 * H * D + 8), dtype=torch_dtype(dtype), device="cuda")
+    k = wide[:, H * D:2 * H * D].unflatten(1, (H, D)).copy_(_dev16(kb, dtype))
+    v = _dev16(vb, dtype)
+    aq.aq_kv_append(k, v, torch.from_numpy(slots).cuda(), *got, G, bits)
+    for t in range(T):
+        if not drop[t]:
+            want.put("k", slots[t], kb[t], kx[t])
+            want.put("v", slots[t], vb[t], vx[t])
+    for i, (n, part) in enumerate((n, p) for n in "kv" for p in range(3)):
+        if got[i] is not None:
+            assert np.array_equal(_cache_bits(got[i]), want.parts[n][part]), (n, part)
+    # reading back, in every type; slots outside the cache give zeros
+    for out in ("f32", "f16", "bf16"):
+        rk, rv = aq.aq_kv_read(torch.from_numpy(slots).cuda(), *got, G, bits,
+                               out_dtype=torch_dtype(out))
+        for n, r in (("k", rk), ("v", rv)):
+            r = out_bits(r)
+            for t in range(T):
+                if drop[t]:
+                    assert not r[t].any()
+                    continue
+                pg, at = slots[t] // page, slots[t] % page
+                parts = [None if x is None else np.ascontiguousarray(x[pg, :, at]) for x in want.parts[n]]
+                if bits == 16:
+                    ref = out_bits(_dev16(parts[0], dtype).to(torch_dtype(out)))
+                else:
+                    ref = oracle.dequantize(*parts, D, G, bits, {"f32": 0, "f16": 1, "bf16": 2}[out])
+                    ref = np.ascontiguousarray(ref).view(r.dtype)
+                assert np.array_equal(r[t], ref), (n, t, out)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_append_out_of_range_and_nan(aq, bits):
+    """bf16 values past fp16's range are clamped, infinities with them; a group
+    that holds a NaN reads back as NaN, its neighbours as they are."""
+    import torch
+    H, D, G = 1, 128, 32
+    x = np.random.default_rng(1).standard_normal((4, H, D))
+    x[0, 0, 3], x[0, 0, 40] = 1e30, -1e30
+    x[1, 0, 70], x[1, 0, 71] = np.inf, -np.inf
+    x[2, 0, 33] = np.nan
+    x[3, 0, 100] = -np.inf
+    xb, xv = kv_ref.to_bits(x, "bf16")
+    c = kv_ref.Cache(1, H, 16, D, G, bits)
+    got = c.device()
+    slots = torch.arange(4, device="cuda")
+    aq.aq_kv_append(_dev16(xb, "bf16"), _dev16(xb, "bf16"), slots, *got, G, bits)
+    k, v = (out_to_f64(t) for t in aq.aq_kv_read(slots, *got, G, bits, out_dtype=torch.float32))
+    ref = np.clip(np.nan_to_num(xv, nan=0.0, posinf=65504, neginf=-65504), -65504, 65504)
+    rc, rs, rb = oracle.quantize(ref[:, 0].astype(np.float32), G, bits)
+    ref = oracle.dequantize_exact(rc, rs, rb, D, G, bits).astype(np.float32)
+    for r in (k, v):
+        assert np.isnan(r[2, 0, 32:64]).all()
+        fine = np.ones((4, D), bool)
+        fine[2, 32:64] = False
+        assert np.array_equal(r[:, 0][fine], ref[fine].astype(np.float64))
+
+
+# B lengths, q heads per head, kv heads, dim, G, bits, page, L, q dtype
+CASES = [
+    ([1], 4, 2, 128, 64, 8, 16, 1, "f16"),
+    ([0, 1, 15, 16, 17, 31, 32, 33, 64, 65], 4, 2, 128, 64, 8, 16, 1, "bf16"),
+    ([300, 0, 77], 1, 3, 64, 32, 4, 48, 1, "f16"),
+    ([1023, 513], 8, 1, 128, 128, 4, 64, 1, "bf16"),
+    ([250, 3, 129], 7, 2, 64, 64, 8, 16, 1, "f16"),
+    ([600, 41], 16, 1, 256, 64, 8, 32, 1, "f16"),
+    ([190, 5], 2, 2, 256, 128, 4, 16, 3, "bf16"),
+    ([333, 2, 0, 8], 8, 2, 128, 32, 8, 16, 5, "bf16"),   # 40 rows a head; lengths under L
+    ([100, 7], 5, 1, 128, 32, 4, 16, 8, "f16"),          # 40 rows a head
+    ([411], 33, 1, 64, 32, 8, 16, 2, "f16"),             # 66 rows a head
+    ([290, 3], 3, 2, 256, 32, 8, 16, 7, "f16"),
+    ([257, 0, 12], 4, 2, 128, 0, 16, 16, 1, "f16"),
+    ([257, 40], 8, 1, 64, 0, 16, 48, 4, "bf16"),
+    ([130], 20, 1, 256, 0, 16, 32, 2, "bf16"),
+    ([5000, 1, 2600], 4, 1, 128, 64, 4, 16, 1, "f16"),   # split over many workgroups
+    ([70] * 40, 2, 3, 64, 64, 4, 16, 1, "bf16"),
+]
+
+
+def _build(lengths, heads, dim, G, bits, page, dtype, seed, poison=True, holes=False):
+    rng = np.random.default_rng(seed)
+    need = [-(-max(0, n) // page) for n in lengths]
+    pages = sum(need) + 3
+    cache = kv_ref.Cache(pages, heads, page, dim, G or 32, bits, dtype)
+    if poison:
+        cache.poison()
+    order = rng.permutation(pages)
+    table = np.full((len(lengths), max(need + [1]) + 2), -1, np.int32)
+    at = 0
+    for b, n in enumerate(lengths):
+        table[b, :need[b]] = order[at:at + need[b]]
+        at += need[b]
+        if n <= 0:
+            continue
+        for name in "kv":
+            x = rng.standard_normal((n, heads, dim))
+            if name == "k":
+                x[..., ::29] *= 4
+            xb, xv = kv_ref.to_bits(x, dtype)
+            slots = table[b, np.arange(n) // page].astype(np.int64) * page + np.arange(n) % page
+            if bits == 16:
+                cache.parts[name][0][slots // page, :, slots % page] = xb
+            else:
+                for part, got in zip(cache.parts[name], oracle.quantize(
+                        xv.reshape(n * heads, dim).astype(np.float32), G, bits)):
+                    part[slots // page, :, slots % page] = got.reshape(n, heads, -1)
+    if holes:  # page ids outside the cache inside the sequences
+        table[rng.random(table.shape) < 0.3] = -7
+        table[rng.random(table.shape) < 0.1] = pages
+    return cache, table
+
+
+def _attend(aq, cache, table, lengths, q_bits, dtype, G, null_biases=False, **more):
+    import torch
+    return aq.aq_paged_attention(
+        _dev16(q_bits, dtype), *cache.device(null_biases), torch.from_numpy(table).cuda(),
+        torch.tensor(lengths, dtype=torch.int32, device="cuda"), G, cache.bits, **more)
+
+
+def _close(out, ref, bound, dtype):
+    got = out_to_f64(out)
+    assert np.isfinite(got).all()
+    off = np.abs(got - ref)
+    most = kv_ref.rounding(dtype) * np.abs(ref) + bound + 2.0 ** -24
+    assert (off <= most).all(), f"worst error/bound {(off / most).max():.3f}"
+
+
+@pytest.mark.parametrize("lengths,per,heads,dim,G,bits,page,L,dtype", CASES)
+def test_attention(aq, lengths, per, heads, dim, G, bits, page, L, dtype):
+    cache, table = _build(lengths, heads, dim, G, bits, page, dtype, seed=len(lengths) + dim)
+    rng = np.random.default_rng(5)
+    qb, q = kv_ref.to_bits(rng.standard_normal((len(lengths), L, per * heads, dim)), dtype)
+    out = _attend(aq, cache, table, lengths, qb, dtype, G)
+    ref, bound = kv_ref.attention(q, cache, table, lengths, dim ** -0.5)
+    _close(out, ref, bound, dtype)
+    for b, n in enumerate(lengths):  # rows that see no token
+        for i in range(L):
+            if n - L + i < 0:
+                assert not out[b, i].any()
+
+
+@pytest.mark.parametrize("bits,dtype", [(4, "f16"), (8, "bf16"), (16, "f16")])
+def test_attention_pages_outside_the_cache(aq, bits, dtype):
+    """Page ids outside the cache are left out, whole sequences of them too;
+    lengths past the table or below zero are clamped."""
+    written = [208, 0, 90, 33, 64]
+    cache, table = _build(written, 2, 64, 32, bits, 16, dtype, seed=3, holes=True)
+    table[0, 13:] = -1
+    table[3] = -1
+    lengths = [10 ** 6, -5, 90, 33, 64]
+    qb, q = kv_ref.to_bits(np.random.default_rng(6).standard_normal((5, 2, 6, 64)), dtype)
+    out = _attend(aq, cache, table, lengths, qb, dtype, 32)
+    ref, bound = kv_ref.attention(q, cache, table, lengths, 64 ** -0.5)
+    _close(out, ref, bound, dtype)
+    assert not out[1].any() and not out[3].any()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_attention_null_biases(aq, bits):
+    import torch
+    lengths = [150, 31]
+    cache, table = _build(lengths, 2, 128, 64, bits, 16, "f16", seed=8, poison=False)
+    for n in "kv":
+        cache.parts[n][2][:] = 0
+    qb, _ = kv_ref.to_bits(np.random.default_rng(9).standard_normal((2, 1, 8, 128)), "f16")
+    a = _attend(aq, cache, table, lengths, qb, "f16", 64)
+    b = _attend(aq, cache, table, lengths, qb, "f16", 64, null_biases=True)
+    assert torch.equal(a, b)
+    slots = torch.arange(40, device="cuda")
+    for x, y in zip(aq.aq_kv_read(slots, *cache.device(), 64, bits),
+                    aq.aq_kv_read(slots, *cache.device(True), 64, bits)):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("size", [1e-4, 1.0, 300.0])
+def test_attention_peaked_and_flat_scores(aq, dtype, size):
+    """Queries from nearly nothing (all tokens alike) to far past exp's range
+    (one token takes all)."""
+    lengths = [700, 90]
+    cache, table = _build(lengths, 2, 128, 64, 8, 32, dtype, seed=11)
+    qb, q = kv_ref.to_bits(size * np.random.default_rng(12).standard_normal((2, 2, 8, 128)), dtype)
+    out = _attend(aq, cache, table, lengths, qb, dtype, 64)
+    ref, bound = kv_ref.attention(q, cache, table, lengths, 128 ** -0.5)
+    _close(out, ref, bound, dtype)
+
+
+def test_attention_small_and_large_values(aq):
+    """Values near fp16's smallest scales and near its largest."""
+    for size in (1e-4, 2e4):
+        lengths = [400]
+        cache, table = _build(lengths, 1, 64, 32, 8, 16, "f16", seed=13)
+        rng = np.random.default_rng(14)
+        _, x = kv_ref.to_bits(np.clip(size * rng.standard_normal((400, 64)), -6e4, 6e4), "f16")
+        slots = table[0, np.arange(400) // 16].astype(np.int64) * 16 + np.arange(400) % 16
+        for part, got in zip(cache.parts["v"], oracle.quantize(x.astype(np.float32), 32, 8)):
+            part[slots // 16, 0, slots % 16] = got
+        qb, q = kv_ref.to_bits(rng.standard_normal((1, 1, 4, 64)), "f16")
+        out = _attend(aq, cache, table, lengths, qb, "f16", 32)
+        ref, bound = kv_ref.attention(q, cache, table, lengths, 64 ** -0.5)
+        _close(out, ref, bound, "f16")
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+def test_attention_nan_reaches_its_rows_only(aq, bits):
+    import torch
+    lengths = [100, 60]
+    cache, table = _build(lengths, 2, 64, 64, bits, 16, "f16", seed=15)
+    page, at = table[0, 2], 5
+    part = 0 if bits == 16 else 2
+    cache.parts["v"][part][page, 1, at] = 0x7E00
+    qb, q = kv_ref.to_bits(np.random.default_rng(16).standard_normal((2, 1, 4, 64)), "f16")
+    out = out_to_f64(_attend(aq, cache, table, lengths, qb, "f16", 64))
+    assert np.isnan(out[0, 0, 2:]).all()
+    cache.parts["v"][part][page, 1, at] = 0
+    ref, bound = kv_ref.attention(q, cache, table, lengths, 64 ** -0.5)
+    fine = np.ones(ref.shape, bool)
+    fine[0, 0, 2:] = False
+    assert (np.abs(out - ref)[fine] <= (2.0 ** -11 * np.abs(ref) + bound + 2.0 ** -24)[fine]).all()
+
+
+def test_attention_strided_queries_and_given_buffers(aq):
+    import torch
+    lengths = [130, 70]
+    cache, table = _build(lengths, 2, 128, 64, 8, 16, "bf16", seed=17)
+    qb, _ = kv_ref.to_bits(np.random.default_rng(18).standard_normal((2, 3, 8, 128)), "bf16")
+    a = _attend(aq, cache, table, lengths, qb, "bf16", 64)
+    wide = torch.zeros((2, 3, 12 * 128), dtype=torch.bfloat16, device="cuda")
+    wide[..., 256:256 + 1024] = _dev16(qb, "bf16").flatten(2)
+    q = wide[..., 256:256 + 1024].unflatten(2, (8, 128))
+    out = torch.full_like(a, 7.0)
+    need = aq.aq_paged_attention_workspace(2, 3, 8, 2, 128)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    args = (*cache.device(), torch.from_numpy(table).cuda(),
+            torch.tensor(lengths, dtype=torch.int32, device="cuda"), 64, 8)
+    for _ in range(3):  # the workspace serves call after call
+        out.fill_(7.0)
+        assert aq.aq_paged_attention(q, *args, out=out, workspace=ws) is out
+        assert torch.equal(out, a)
+    # one token: [B, heads, dim] is [B, 1, heads, dim]
+    one = aq.aq_paged_attention(q[:, 2], *args, workspace=ws)
+    assert torch.equal(one, aq.aq_paged_attention(q[:, 2:3], *args, workspace=ws)[:, 0])
+
+
+def test_one_workspace_serves_every_shape(aq):
+    import torch
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    for rep in range(2):
+        for lengths, per, heads, dim, G, bits, page, L, dtype in CASES[:8] + CASES[-2:]:
+            cache, table = _build(lengths, heads, dim, G, bits, page, dtype, seed=21)
+            qb, _ = kv_ref.to_bits(np.random.default_rng(22).standard_normal(
+                (len(lengths), L, per * heads, dim)), dtype)
+            a = _attend(aq, cache, table, lengths, qb, dtype, G, workspace=ws)
+            assert torch.equal(a, _attend(aq, cache, table, lengths, qb, dtype, G))
+
+
+def test_cache_past_four_gib(aq):
+    """Slots and pages whose byte offsets pass 32 bits."""
+    import torch
+    H, D, G, bits, page = 8, 128, 64, 8, 64
+    pages = 72000  # 4.7 GB of codes each
+    shape = (pages, H, page)
+    got = []
+    for _ in "kv":
+        got.append(torch.empty(shape + (D * bits // 32,), dtype=torch.int32, device="cuda"))
+        got += [torch.empty(shape + (D // G,), dtype=torch.float16, device="cuda") for _ in range(2)]
+    n = 150
+    ids = np.array([pages - 1, 3, pages - 2], np.int64)
+    small = kv_ref.Cache(3, H, page, D, G, bits)
+    rng = np.random.default_rng(23)
+    kb, kx = kv_ref.to_bits(rng.standard_normal((n, H, D)), "f16")
+    vb, vx = kv_ref.to_bits(rng.standard_normal((n, H, D)), "f16")
+    for t in range(n):
+        small.put("k", t, kb[t], kx[t])
+        small.put("v", t, vb[t], vx[t])
+    slots = torch.from_numpy(ids[np.arange(n) // page] * page + np.arange(n) % page).cuda()
+    aq.aq_kv_append(_dev16(kb, "f16"), _dev16(vb, "f16"), slots, *got, G, bits)
+    k, _ = aq.aq_kv_read(slots, *got, G, bits, out_dtype=torch.float32)
+    for h in range(H):
+        ref = np.concatenate([small.row("k", p, h, page)[0] for p in range(3)])[:n]
+        assert np.array_equal(out_to_f64(k)[:, h], ref.astype(np.float32).astype(np.float64))
+    qb, q = kv_ref.to_bits(rng.standard_normal((1, 1, 32, D)), "f16")
+    out = aq.aq_paged_attention(_dev16(qb, "f16"), *got,
+                                torch.tensor([ids.tolist()], dtype=torch.int32, device="cuda"),
+                                torch.tensor([n], dtype=torch.int32, device="cuda"), G, bits)
+    ref, bound = kv_ref.attention(q, small, np.array([[0, 1, 2]], np.int32), [n], D ** -0.5)
+    _close(out, ref, bound, "f16")
+
+
+def test_on_another_stream(aq):
+    """Inputs made, cache written, attended to and read back on a side stream."""
+    import torch
+    lengths = [96, 50]
+    cache, table = _build(lengths, 2, 128, 64, 8, 16, "f16", seed=25)
+    qb, _ = kv_ref.to_bits(np.random.default_rng(26).standard_normal((2, 1, 8, 128)), "f16")
+    a = _attend(aq, cache, table, lengths, qb, "f16", 64)
+    args = (*cache.device(), torch.from_numpy(table).cuda(),
+            torch.tensor(lengths, dtype=torch.int32, device="cuda"), 64, 8)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        junk = torch.randn((4096, 4096), device="cuda")
+        junk = junk @ junk  # the stream is busy when the call is made
+        q = _dev16(qb, "f16") + 0 * junk[0, 0].half().nan_to_num(0, 0, 0)
+        b = aq.aq_paged_attention(q, *args)
+    c = aq.aq_paged_attention(_dev16(qb, "f16"), *args, stream=s)
+    s.synchronize()
+    assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_graph_follows_growing_lengths(aq):
+    """A captured step of append and attention, replayed while the sequences
+    grow, gives what the eager calls give."""
+    import torch
+    H, D, G, bits, page, B, per = 2, 128, 64, 4, 16, 3, 4
+    steps, start = 5, [0, 14, 500]
+    mp = 34
+    table = torch.arange(B * mp, dtype=torch.int32, device="cuda").view(B, mp)
+    rng = np.random.default_rng(27)
+
+    def fresh():
+        c = kv_ref.Cache(B * mp, H, page, D, G, bits)
+        got = c.device()
+        for b, n in enumerate(start):
+            if n:
+                xb, _ = kv_ref.to_bits(np.random.default_rng(b).standard_normal((n, H, D)), "f16")
+                t = torch.arange(n, device="cuda")
+                slots = table[b, t // page].long() * page + t % page
+                aq.aq_kv_append(_dev16(xb, "f16"), _dev16(xb, "f16"), slots, *got, G, bits)
+        return got
+
+    new = [[_dev16(kv_ref.to_bits(rng.standard_normal((B, H * (per if n == "q" else 1), D)), "f16")[0],
+                   "f16") for n in "kvq"] for _ in range(steps)]
+    k, v, q = (x.clone() for x in new[0])
+    slots = torch.zeros(B, dtype=torch.int64, device="cuda")
+    lengths = torch.zeros(B, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(q)
+
+    def step(cache):
+        aq.aq_kv_append(k, v, slots, *cache, G, bits)
+        aq.aq_paged_attention(q, *cache, table, lengths, G, bits, out=out, workspace=ws)
+
+    def load(i):
+        for dst, src in zip((k, v, q), new[i]):
+            dst.copy_(src)
+        at = torch.tensor([n + i for n in start], device="cuda")
+        lengths.copy_(at + 1)
+        slots.copy_(table[torch.arange(B, device="cuda"), at // page].long() * page + at % page)
+
+    eager, cache = [], fresh()
+    for i in range(steps):
+        load(i)
+        step(cache)
+        eager.append(out.clone())
+    cache = fresh()
+    load(0)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        step(cache)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            step(cache)
+    torch.cuda.synchronize()
+    for i in range(steps):
+        load(i)
+        out.fill_(3.0)
+        torch.randn(1 << 18, device="cuda").sort()  # the program's own work between
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager[i]), i
+
+
+@pytest.mark.parametrize("op", ["read", "append"])
+def test_no_tokens(aq, op):
+    import torch
+    c = kv_ref.Cache(2, 2, 16, 64, 32, 8).device()
+    none = torch.empty(0, dtype=torch.int64, device="cuda")
+    if op == "read":
+        k, v = aq.aq_kv_read(none, *c, 32, 8)
+        assert k.shape == v.shape == (0, 2, 64)
+    else:
+        x = torch.empty((0, 2, 64), dtype=torch.float16, device="cuda")
+        aq.aq_kv_append(x, x, none, *c, 32, 8)
+
+
+def test_binding_refusals(aq):
+    """What the binding checks before the library does."""
+    import torch
+    c = kv_ref.Cache(2, 2, 16, 64, 32, 8).device()
+    x = torch.zeros((3, 2, 64), dtype=torch.float16, device="cuda")
+    slots = torch.zeros(3, dtype=torch.int64, device="cuda")
+    q = torch.zeros((1, 4, 64), dtype=torch.float16, device="cuda")
+    table = torch.zeros((1, 2), dtype=torch.int32, device="cuda")
+    n = torch.ones(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(TypeError):
+        aq.aq_kv_append(x, x, slots.int(), *c, 32, 8)
+    with pytest.raises(ValueError):
+        aq.aq_kv_append(x[:2], x[:2], slots, *c, 32, 8)
+    with pytest.raises(ValueError):
+        aq.aq_kv_append(x.transpose(1, 2).contiguous().transpose(1, 2), x, slots, *c, 32, 8)
+    with pytest.raises(ValueError):
+        aq.aq_kv_append(x.cpu(), x, slots, *c, 32, 8)
+    with pytest.raises(ValueError):  # scales of another group size
+        aq.aq_kv_append(x, x, slots, *c, 64, 8)
+    with pytest.raises(aq.AQError):
+        aq.aq_kv_append(x, x, slots, *c, 32, 5)
+    with pytest.raises(aq.AQError):  # a cache cannot be written without biases
+        aq.aq_kv_append(x, x, slots, c[0], c[1], None, c[3], c[4], None, 32, 8)
+    with pytest.raises(TypeError):
+        aq.aq_paged_attention(q, *c, table.long(), n, 32, 8)
+    with pytest.raises(TypeError):
+        aq.aq_paged_attention(q.double(), *c, table, n, 32, 8)
+    with pytest.raises(aq.AQError):
+        aq.aq_paged_attention(q[:, :3], *c, table, n, 32, 8)
+    with pytest.raises(aq.AQError):
+        aq.aq_paged_attention(q[:, None].expand(1, 9, 4, 64).contiguous(), *c, table, n, 32, 8)
+    with pytest.raises(ValueError):
+        aq.aq_paged_attention(q, *c, table, torch.ones(2, dtype=torch.int32, device="cuda"), 32, 8)
+    with pytest.raises(aq.AQError):  # workspace too small
+        aq.aq_paged_attention(q, *c, table, n, 32, 8,
+                              workspace=torch.zeros(8, dtype=torch.uint8, device="cuda"))
+    half = torch.zeros((2, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(aq.AQError):  # a 16-bit cache of another type
+        aq.aq_paged_attention(q, half, None, None, half, None, None, table, n, 0, 16)
