@@ -500,7 +500,7 @@ aq_status aq_paged_attention(const void *q, aq_dtype x_dtype, int64_t B, int L, 
   if (q_stride < (int64_t)q_heads * cache->head_dim || q_stride % 8 != 0)
     return AQ_ERR_INVALID_ARG;
   if (q_stride > ((int64_t)1 << 62) / (B * L)) return AQ_ERR_UNSUPPORTED;
-  if (max_pages > 0x7FFFFFFF / cache->page_size) return AQ_ERR_UNSUPPORTED;
+  if (max_pages > 0x7FFFFF00 / cache->page_size) return AQ_ERR_UNSUPPORTED;
   st = check_cache_arrays(cache, false);
   if (st != AQ_OK) return st;
   if (!q || !page_table || !lengths || !out || !workspace) return AQ_ERR_INVALID_ARG;

@@ -455,7 +455,7 @@ aq_status aq_kv_read(const int64_t *slots, int64_t T, const aq_kv_cache *cache, 
  * run at the same time need workspaces of their own.  The launch does not
  * depend on the lengths, so a captured graph follows them as they grow.
  * AQ_ERR_INVALID_ARG when workspace_bytes is too small, B < 1, L outside
- * 1..8; AQ_ERR_UNSUPPORTED for max_pages * page_size >= 2^31 or B * L *
+ * 1..8; AQ_ERR_UNSUPPORTED for max_pages * page_size > 2^31 - 256 or B * L *
  * q_heads >= 2^24. */
 aq_status aq_paged_attention(const void *q, aq_dtype x_dtype, int64_t B, int L, int q_heads,
                              int64_t q_stride, const aq_kv_cache *cache, const int32_t *page_table,
