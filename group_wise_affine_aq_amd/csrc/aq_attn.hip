@@ -68,8 +68,8 @@ typedef float f32x4v __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
 
-constexpr int kBlock = 128;       // tokens per block: 4 waves of 32
-constexpr int kMaxGrid = 1024;    // arrival counters in the workspace
+constexpr int kTile = 32;         // tokens a wave takes at a time
+constexpr int NW = 4;             // waves of a workgroup
 constexpr float kNegInf = -__builtin_inff();
 
 // `bytes` bytes at a uniform address; reads past them give zeros, without a
@@ -198,11 +198,11 @@ struct Params {
   const void *kc, *ks, *kb, *vc, *vs, *vb;
   const int32_t *table, *lengths;
   void *out;
-  float *parts;       // two pieces per workgroup
-  uint32_t *arrived;  // one counter per workgroup, zero between calls
+  float *parts;  // two pieces per workgroup
   int64_t max_pages, num_pages;
   uint32_t page_subs, page_magic;  // page_size / 16 and floor(2^32 / that) + 1
   int kv_heads, group, L, B, slices, x_dtype;
+  uint32_t chunk;  // tokens of the work line's chunks, at least
   float scale;
 };
 
@@ -219,6 +219,76 @@ __device__ __forceinline__ int clamped_length(const Params &p, int b) {
   const int n = p.lengths[b];
   return n < 0 ? 0 : (n > cap ? (int)cap : n);
 }
+
+// one piece in the workspace: the results of 16 NT columns, D floats each, then
+// the columns' m and l
+constexpr int piece_floats(int D, int NT) { return NT * (16 * D + 32); }
+
+// ---- the work line ------------------------------------------------------------------
+// All tiles of all units -- a unit is one sequence, key head and slice of query
+// rows -- in one line, sequences first, cut evenly.  It is counted in chunks:
+// single tiles, or, where one pass of the waves takes all there is, four
+// tiles, so that a workgroup's waves all have one and no unit is cut without
+// need.
+
+// inclusive sum over the lanes, a row of 16 and then the rows
+__device__ __forceinline__ uint32_t lanes_prefix(uint32_t v) {
+  v += __builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);  // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);  // row_bcast:31
+  return v;
+}
+
+struct Line {
+  uint32_t rows;      // units per sequence
+  uint32_t chunk;     // tokens
+  uint32_t grid, share, longer;  // workgroup w has share chunks, one more if w < longer
+  int per;            // sequences per lane
+  uint32_t mine, upto;  // chunks (of one unit) of this lane's sequences, and up to them
+  bool idle;          // this lane has a sequence without tokens
+
+  __device__ __forceinline__ uint32_t chunks(uint32_t len) const { return (len + chunk - 1) / chunk; }
+
+  __device__ __forceinline__ uint32_t count(const Params &p, int lane) {
+    const int lo = lane * per < p.B ? lane * per : p.B, hi = lo + per < p.B ? lo + per : p.B;
+    mine = 0;
+    idle = false;
+    for (int b = lo; b < hi; ++b) {
+      const int len = clamped_length(p, b);
+      mine += chunks(len);
+      idle |= len == 0;
+    }
+    upto = lanes_prefix(mine);
+    return (uint32_t)uniform(__builtin_amdgcn_readlane(upto, 63)) * rows;
+  }
+
+  // `most`: workgroups there are
+  __device__ __forceinline__ Line(const Params &p, uint32_t most, int lane) {
+    rows = p.kv_heads * p.slices;
+    per = (p.B + 63) / 64;
+    chunk = p.chunk;
+    uint32_t total = count(p, lane);
+    if (chunk == kTile && total <= most * NW) {
+      chunk = NW * kTile;
+      total = count(p, lane);
+    }
+    grid = total < most ? total : most;
+    share = grid ? total / grid : 0;
+    longer = total - share * grid;
+  }
+
+  __device__ __forceinline__ uint32_t begin(uint32_t w) const {
+    return w * share + (w < longer ? w : longer);
+  }
+  // the workgroup that has chunk `at`
+  __device__ __forceinline__ uint32_t owner(uint32_t at) const {
+    const uint32_t first = longer * (share + 1);
+    return at < first ? at / (share + 1) : longer + (at - first) / share;
+  }
+};
 
 // ---- one wave's state over a segment of tokens -------------------------------------
 // BITS 4, 8 or 16; BF: operands are bf16 (bits = 16 with a bf16 cache); G is
@@ -335,10 +405,12 @@ struct Wave {
     return a;
   }
 
-  // queries of rows slice*16*NT .. of (b, head): columns of this lane
-  __device__ __forceinline__ void start(const Params &p, int b, int head, int slice, int len) {
-    const int lane = lane_here(), h = lane >> 4;
-    const int cols = p.L * p.group;
+  // queries of rows slice*16*NT .. of (b, head), the columns of this lane:
+  // fetched first, made into operands when the keys are on their way
+  struct Queries { uint4 raw[NT][KS]; };
+  __device__ __forceinline__ void load_queries(Queries &qs, const Params &p, int b, int head,
+                                               int slice, int len, int lane) {
+    const int h = lane >> 4, cols = p.L * p.group;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = (slice * NT + nt) * 16 + (lane & 15);
@@ -348,7 +420,6 @@ struct Wave {
       const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) +
                             ((int64_t)b * p.L + i) * p.q_stride +
                             (int64_t)(head * p.group + j) * D;
-      uint4 raw[KS];
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         // where the keys' 8 values of this product lie along the row
@@ -359,9 +430,17 @@ struct Wave {
         } else {
           d = s * 32 + h * 8;
         }
-        raw[s] = *reinterpret_cast<const uint4 *>(src + d);
-        if (!on) raw[s] = make_uint4(0, 0, 0, 0);
+        qs.raw[nt][s] = *reinterpret_cast<const uint4 *>(src + d);
       }
+    }
+  }
+  __device__ __forceinline__ void start(const Queries &qs, const Params &p, int slice, int lane) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool on = (slice * NT + nt) * 16 + (lane & 15) < p.L * p.group;
+      uint4 raw[KS];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) raw[s] = on ? qs.raw[nt][s] : make_uint4(0, 0, 0, 0);
       if constexpr (QUANT) {
         float x[KS][8], top = 0.f;
 #pragma unroll
@@ -405,7 +484,6 @@ struct Wave {
         for (int s = 0; s < KS; ++s) q[nt][s] = u32x4v{raw[s].x, raw[s].y, raw[s].z, raw[s].w};
       }
     }
-    clear();
   }
 
   __device__ __forceinline__ void clear() {
@@ -553,8 +631,9 @@ struct Wave {
 
   // The values of tokens a column does not see must not reach it, not even as
   // 0 * NaN.  Quantized values: the codes are finite, so this is a matter of
-  // the lane's scales and biases: those of tokens past the lane's columns, and
-  // any that are not finite, become 0; a NaN goes to the columns that see it.
+  // the lane's scales and biases.  Those of tokens past its column become 0;
+  // where a lane has two columns, those of tokens past both do, and any that
+  // are not finite, whose NaN goes to the columns that see it.
   __device__ __forceinline__ void edge_values(Values &v, int token, const bool *on, int h) {
 #pragma unroll
     for (int x = 0; x < 2 * SW; ++x) {
@@ -563,15 +642,20 @@ struct Wave {
 #pragma unroll
       for (int e = 2 * w; e < 2 * w + 2; ++e) {
         const int g = e % NG, at = token + 16 * sub + 4 * h + e / NG;
-        const float zero = half_at(v.g.s[sub][w], e & 1) * 0.f + half_at(v.g.b[sub][w], e & 1) * 0.f;
-        bool seen = false;
+        const uint32_t half = e & 1 ? 0xFFFF0000u : 0x0000FFFFu;
+        if constexpr (NT == 1) {
+          if (on[sub] && at < vis[0]) keep |= half;
+        } else {
+          const float zero = half_at(v.g.s[sub][w], e & 1) * 0.f + half_at(v.g.b[sub][w], e & 1) * 0.f;
+          bool seen = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const bool here = on[sub] && at < vis[nt];
-          seen |= here;
-          bacc[nt][g] += here ? zero : 0.f;
+          for (int nt = 0; nt < NT; ++nt) {
+            const bool here = on[sub] && at < vis[nt];
+            seen |= here;
+            bacc[nt][g] += here ? zero : 0.f;
+          }
+          if (seen && zero == 0.f) keep |= half;
         }
-        if (seen && zero == 0.f) keep |= e & 1 ? 0xFFFF0000u : 0x0000FFFFu;
       }
       // (opaque, or the words of all tiles are taken apart into halves)
       asm volatile("" : "+v"(keep));
@@ -596,50 +680,57 @@ struct Wave {
     }
   }
 
-  // the 32-token tiles of one wave in blocks [blk0, blk1) of a sequence
+  // tiles first, first + NW, ... below end of a sequence: one wave's part
   __device__ __forceinline__ void run(const Params &p, int b, int head, int slice, int len,
-                                      int blk0, int blk1) {
-    const int lane = lane_here(), wave = uniform(threadIdx.x >> 6);
+                                      int tile0, int end) {
+    const int lane = lane_here();
     const int least = len - p.L + 1 + (slice * NT * 16) / p.group;  // what every column sees
-    for (int c0 = blk0; c0 < blk1; c0 += 32) {
-      const int first = c0 * kBlock + wave * 32;
-      const int most = blk1 - c0 < 32 ? blk1 - c0 : 32;
-      // lane 2k + sub: the rows of tile k
-      uint32_t row_lo = 0, row_hi = 0x80000000u;
-      {
-        const int64_t t = (int64_t)first + (lane >> 1) * kBlock + (lane & 1) * 16;
-        if ((lane >> 1) < most && t < len) {
-          const uint32_t s = (uint32_t)(t >> 4), pg = page_of(p, s);
-          const int id = p.table[(int64_t)b * p.max_pages + pg];
-          if (id >= 0 && id < p.num_pages) {
-            const int64_t row = (((int64_t)id * p.kv_heads + head) * p.page_subs + (s - pg * p.page_subs)) * 16;
-            row_lo = (uint32_t)row;
-            row_hi = (uint32_t)(row >> 32);
-          }
+    Keys k;
+    Values v;
+    uint32_t row_lo, row_hi;  // lane 2 i + sub: the rows of the round's tile i
+    int64_t rows[2];
+    bool on[2], on_next[2];
+    int c0 = tile0, first, tiles;
+    // up to 32 tiles' pages at once
+    auto look_up = [&] {
+      first = c0 * kTile;
+      const int left = (end - c0 + NW - 1) / NW;
+      tiles = left < 32 ? left : 32;
+      row_lo = 0, row_hi = 0x80000000u;
+      const int64_t t = (int64_t)first + (lane >> 1) * (NW * kTile) + (lane & 1) * 16;
+      if ((lane >> 1) < tiles && t < len) {
+        const uint32_t s = (uint32_t)(t >> 4), pg = page_of(p, s);
+        const int id = p.table[(int64_t)b * p.max_pages + pg];
+        if (id >= 0 && id < p.num_pages) {
+          const int64_t row = (((int64_t)id * p.kv_heads + head) * p.page_subs + (s - pg * p.page_subs)) * 16;
+          row_lo = (uint32_t)row;
+          row_hi = (uint32_t)(row >> 32);
         }
       }
-      // tiles past len are at the end only
-      int tiles = (len - first + kBlock - 1) / kBlock;
-      tiles = len <= first ? 0 : (tiles < most ? tiles : most);
-      if (tiles == 0) continue;
-      Keys k;
-      Values v;
-      int64_t rows[2];
-      bool on[2], on_next[2];
-      auto locate = [&](int tile, bool *there) {
+    };
+    auto locate = [&](int tile, bool *there) {
 #pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          const uint32_t lo = __builtin_amdgcn_readlane(row_lo, 2 * tile + sub);
-          const uint32_t hi = __builtin_amdgcn_readlane(row_hi, 2 * tile + sub);
-          there[sub] = !(hi >> 31);
-          rows[sub] = (int64_t)(((uint64_t)(hi & 0x7FFFFFFFu) << 32) | lo);
-        }
-      };
+      for (int sub = 0; sub < 2; ++sub) {
+        const uint32_t lo = __builtin_amdgcn_readlane(row_lo, 2 * tile + sub);
+        const uint32_t hi = __builtin_amdgcn_readlane(row_hi, 2 * tile + sub);
+        there[sub] = !(hi >> 31);
+        rows[sub] = (int64_t)(((uint64_t)(hi & 0x7FFFFFFFu) << 32) | lo);
+      }
+    };
+    {
+      Queries qs;
+      load_queries(qs, p, b, head, slice, len, lane);
+      look_up();
+      start(qs, p, slice, lane);
+      __builtin_amdgcn_sched_barrier(0);
       locate(0, on);
       load_keys(k, p, rows, on, lane);
       load_values(v, p, rows, on, lane);
+      clear();
+    }
+    for (;;) {
       for (int tile = 0; tile < tiles; ++tile) {
-        const int token = first + tile * kBlock;
+        const int token = first + tile * (NW * kTile);
         const bool last = tile + 1 == tiles;
         float t[NT][8];
         const bool edge = token + 32 > least || !on[0] || !on[1];
@@ -679,343 +770,223 @@ struct Wave {
         on[0] = on_next[0];
         on[1] = on_next[1];
       }
+      c0 += 32 * NW;
+      if (c0 >= end) break;
+      look_up();
+      locate(0, on);
+      load_keys(k, p, rows, on, lane);
+      load_values(v, p, rows, on, lane);
     }
   }
 
-  // (m, l, o) with the biases' part folded in and every lane holding its
-  // column's whole sums
-  __device__ __forceinline__ void fold(float (&r)[NR]) {
+  // The wave's (m, l, o), the biases' part folded in, to its place in LDS: rows
+  // of D results per column, then the columns' m and l.
+  static constexpr int PF = piece_floats(D, NT);
+  static constexpr int ROW = D + 4;  // columns on different banks
+  static constexpr int SHARE = NT * 16 * ROW;
+  __device__ __forceinline__ void give(float *o_at, float *ml_at, int used) {
+    const int lane = lane_here(), c = lane & 15, h = lane >> 4;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      l[nt] = quarters_sum(l[nt]);
+      const float sum = quarters_sum(l[nt]);
+      if (lane < 16) {
+        ml_at[nt * 32 + lane] = m[nt];
+        ml_at[nt * 32 + 16 + lane] = sum;
+      }
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const float add = QUANT ? quarters_sum(bacc[nt][g]) : 0.f;
+        if (nt * 16 + c < used) {
+          float *at = o_at + (nt * 16 + c) * ROW + g * G + 4 * h * VN;
 #pragma unroll
-        for (int n = 0; n < VN; ++n)
+          for (int e = 0; e < 4 * VN; e += 4) {  // value e: row e / VN of product e % VN
+            f32x4v y;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            r[((nt * NG + g) * VN + n) * 4 + i] =
-                QUANT ? __builtin_fmaf(o[nt][g][n][i], BITS == 4 && (n & 1) ? 0x1p20f : 0x1p24f, add)
-                      : o[nt][g][n][i];
+            for (int x = 0; x < 4; ++x) {
+              const int n = (e + x) % VN;
+              const float r = o[nt][g][n][(e + x) / VN];
+              y[x] = QUANT ? __builtin_fmaf(r, BITS == 4 && (n & 1) ? 0x1p20f : 0x1p24f, add) : r;
+            }
+            *reinterpret_cast<f32x4v *>(at + e) = y;
+          }
+        }
       }
     }
   }
 };
 
-// m, l and r of the four waves -> wave 0
-template <int NT, int NR>
-__device__ __forceinline__ void join_waves(float (&m)[NT], float (&l)[NT], float (&r)[NR],
-                                           float *ml, float *buf) {
-  const int lane = lane_here(), wave = threadIdx.x >> 6;
-  __syncthreads();  // the buffers' last readers are done
-  if (lane < 16)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      ml[(wave * NT + nt) * 32 + lane] = m[nt];
-      ml[(wave * NT + nt) * 32 + 16 + lane] = l[nt];
-    }
-  __syncthreads();
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float top = kNegInf, total = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) top = __builtin_fmaxf(top, ml[(w * NT + nt) * 32 + (lane & 15)]);
-    const float base = top == kNegInf ? 0.f : top;
-#pragma unroll
-    for (int w = 0; w < 4; ++w)
-      total += ml[(w * NT + nt) * 32 + 16 + (lane & 15)] *
-               exp2_fast(ml[(w * NT + nt) * 32 + (lane & 15)] - base);
-    const float keep = exp2_fast(m[nt] - base);
-#pragma unroll
-    for (int i = 0; i < NR / NT; ++i) r[nt * (NR / NT) + i] *= keep;
-    m[nt] = top;
-    l[nt] = total;
-  }
-  if (wave >= 2)
-#pragma unroll
-    for (int i = 0; i < NR; ++i) buf[((wave - 2) * NR + i) * 64 + lane] = r[i];
-  __syncthreads();
-  if (wave < 2)
-#pragma unroll
-    for (int i = 0; i < NR; ++i) r[i] += buf[(wave * NR + i) * 64 + lane];
-  __syncthreads();
-  if (wave == 1)
-#pragma unroll
-    for (int i = 0; i < NR; ++i) buf[i * 64 + lane] = r[i];
-  __syncthreads();
-  if (wave == 0)
-#pragma unroll
-    for (int i = 0; i < NR; ++i) r[i] += buf[i * 64 + lane];
-}
-
-// One piece in the workspace: the results of 16 NT columns, D floats each, then
-// the columns' m and l.  Pieces are read by other workgroups than wrote them,
-// on other XCDs with L2s of their own, in the same launch: stores and loads go
-// past the L2s (sc1, the cache policy of device scope), and a workgroup counts
-// as arrived when its stores are done.  (Ordinary stores with a device-wide
-// fence write back and drop whole L2s: 118 against 37 us for 16 sequences of
-// up to 4096 tokens, 8 bits.)
-constexpr int kDeviceScope = 16;
-template <int D, int NT>
-constexpr int piece_floats() { return NT * (16 * D + 32); }
-
-__device__ __forceinline__ void put_piece(Span to, int at, f32x4v v) {
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, v), to, at * 4, 0, kDeviceScope);
-}
-__device__ __forceinline__ f32x4v get_piece4(Span from, int at) {
-  return __builtin_bit_cast(f32x4v, __builtin_amdgcn_raw_buffer_load_b128(from, at * 4, 0, kDeviceScope));
-}
-__device__ __forceinline__ float get_piece(Span from, int at) {
-  const uint32_t u = __builtin_amdgcn_raw_buffer_load_b32(from, at * 4, 0, kDeviceScope);
-  return __builtin_bit_cast(float, u);
-}
-
-// Joins a unit's pieces w0 .. w1 (the first is that workgroup's second) and
-// writes the rows: m and l of each column over 16 strands of pieces, then
-// every four values of a column over one strand per wave.  The order of all
-// sums is the pieces' own.
-template <int D, int NT>
-__device__ __forceinline__ void join_pieces(const Params &p, int b, int head, int slice, int64_t w0,
-                                            int n, float *ml, float *buf) {
-  constexpr int PF = piece_floats<D, NT>(), ML = NT * 16 * D;
-  const int lane = lane_here(), wave = uniform(threadIdx.x >> 6);
-  const int cols = p.L * p.group - slice * NT * 16;
-  const Span first = span(p.parts, (2 * w0 + 1) * (PF * 4), PF * 4);
-  // piece i > 0 is at (2 i - 1) PF floats past the first
-  const float *rest = p.parts + (2 * w0 + 1) * (int64_t)PF;
-  auto piece = [&](int i) {
-    return i ? span(rest, (2 * (int64_t)i - 1) * (PF * 4), PF * 4) : first;
-  };
-  {
-    const int strand = threadIdx.x >> 4, c = threadIdx.x & 15;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float m = kNegInf, l = 0.f;
-#pragma unroll 4
-      for (int i0 = 0; i0 < n; i0 += 16) {
-        const int i = i0 + strand;
-        if (i < n) {
-          // strands of a wave read different pieces: plain addresses
-          const float *src = rest + (i ? (2 * (int64_t)i - 1) * PF : 0) + ML + nt * 32 + c;
-          const float pm = __hip_atomic_load(src, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          const float pl = __hip_atomic_load(src + 16, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          const float top = __builtin_fmaxf(m, pm), base = top == kNegInf ? 0.f : top;
-          l = l * exp2_fast(m - base) + pl * exp2_fast(pm - base);
-          m = top;
-        }
-      }
-      buf[(strand * NT + nt) * 32 + c] = m;
-      buf[(strand * NT + nt) * 32 + 16 + c] = l;
-    }
-    __syncthreads();
-    if (threadIdx.x < 16 * NT) {
-      const int nt = threadIdx.x >> 4;
-      float m = kNegInf, l = 0.f;
-      for (int w = 0; w < 16; ++w) m = __builtin_fmaxf(m, buf[(w * NT + nt) * 32 + c]);
-      const float base = m == kNegInf ? 0.f : m;
-      for (int w = 0; w < 16; ++w)
-        l += buf[(w * NT + nt) * 32 + 16 + c] * exp2_fast(buf[(w * NT + nt) * 32 + c] - base);
-      ml[nt * 32 + c] = base;
-      ml[nt * 32 + 16 + c] = l == 0.f ? 0.f : 1.f / l;
-    }
-    __syncthreads();
-  }
-  const int used = cols < 16 * NT ? cols : 16 * NT;
-  constexpr int Q = D / 4;
-  for (int i0 = 0; i0 < used * Q; i0 += 64) {
-    const int item = i0 + lane, c = item / Q;  // past the columns in use: read, not written
-    const float base = ml[(c >> 4) * 32 + (c & 15)];
-    f32x4v acc = {0.f, 0.f, 0.f, 0.f};
-    for (int i = wave; i < n; i += 32) {
-      f32x4v v[8];
-      float m[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const Span src = piece(i + 4 * x < n ? i + 4 * x : i);
-        v[x] = get_piece4(src, item * 4);
-        m[x] = get_piece(src, ML + (c >> 4) * 32 + (c & 15));
-      }
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const float w = i + 4 * x < n ? exp2_fast(m[x] - base) : 0.f;
-        if (i + 4 * x < n) acc += v[x] * w;
-      }
-    }
-    *reinterpret_cast<f32x4v *>(buf + (wave * 64 + lane) * 4) = acc;
-    __syncthreads();
-    if (wave == ((i0 >> 6) & 3) && c < used) {
-      const float inv = ml[(c >> 4) * 32 + 16 + (c & 15)];
-      f32x4v y = *reinterpret_cast<f32x4v *>(buf + lane * 4);
-      for (int w = 1; w < 4; ++w) y += *reinterpret_cast<f32x4v *>(buf + (w * 64 + lane) * 4);
-      y *= inv;
-      const int r = slice * NT * 16 + c, i = r / p.group, j = r - i * p.group;
-      uint2 *out = reinterpret_cast<uint2 *>(
-          reinterpret_cast<uint16_t *>(p.out) +
-          (((int64_t)b * p.L + i) * p.kv_heads * p.group + head * p.group + j) * D + (item % Q) * 4);
-      *out = p.x_dtype == X_F16 ? make_uint2(pack_f16(y[0], y[1]), pack_f16(y[2], y[3]))
-                                : make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
-    }
-    __syncthreads();
-  }
+// four values of a row of the result
+template <int D>
+__device__ __forceinline__ void put_result(const Params &p, int b, int head, int r, int at, f32x4v y) {
+  const int i = r / p.group, j = r - i * p.group;
+  uint2 *out = reinterpret_cast<uint2 *>(
+      reinterpret_cast<uint16_t *>(p.out) +
+      (((int64_t)b * p.L + i) * p.kv_heads * p.group + head * p.group + j) * D + at);
+  *out = p.x_dtype == X_F16 ? make_uint2(pack_f16(y[0], y[1]), pack_f16(y[2], y[3]))
+                            : make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
 }
 
 template <int BITS, bool BF, int D, int G, int NT, int WGS>
-__global__ __launch_bounds__(256, WGS) void attn_kernel(Params p) {
+__global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
   using W = Wave<BITS, BF, D, G, NT>;
-  constexpr int NR = W::NR, NG = W::NG, VN = W::VN;
-  __shared__ float buf[2 * NR * 64];
-  __shared__ float ml[4 * NT * 32];
-  __shared__ uint32_t sums[4];
-  __shared__ int found[2];
-  __shared__ uint32_t flag;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ f32x4v buf4[NW * W::SHARE / 4];
+  __shared__ float ml[NW * NT * 32];
+  float *buf = reinterpret_cast<float *>(buf4);
+  const int wave = uniform(threadIdx.x >> 6);
 
+  const Line line(p, gridDim.x, lane_here());
   // sequences without tokens: zero rows
-  const int64_t row_halves = (int64_t)p.L * p.kv_heads * p.group * D;
-  for (int64_t b = blockIdx.x; b < p.B; b += gridDim.x)
-    if (clamped_length(p, (int)b) == 0)
-      for (int64_t i = threadIdx.x; i < row_halves / 8; i += 256)
-        reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + b * row_halves)[i] =
-            make_uint4(0, 0, 0, 0);
-
-  // blocks of all sequences, and this workgroup's part of the line
-  const int per = (p.B + 255) / 256;
-  const int b_lo = threadIdx.x * per < p.B ? threadIdx.x * per : p.B;
-  const int b_hi = b_lo + per < p.B ? b_lo + per : p.B;
-  uint32_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += (uint32_t)(clamped_length(p, b) + kBlock - 1) / kBlock;
-  uint32_t upto = mine;  // inclusive sum over the threads
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t x = __shfl_up(upto, d);
-    if (lane >= d) upto += x;
+  if (__ballot(line.idle)) {
+    const int64_t row_halves = (int64_t)p.L * p.kv_heads * p.group * D;
+    for (int64_t b = blockIdx.x; b < p.B; b += gridDim.x)
+      if (clamped_length(p, (int)b) == 0)
+        for (int64_t i = threadIdx.x; i < row_halves / 8; i += 64 * NW)
+          reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + b * row_halves)[i] =
+              make_uint4(0, 0, 0, 0);
   }
-  if (lane == 63) sums[wave] = upto;
-  __syncthreads();
-  uint32_t all = 0;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    if (w < wave) upto += sums[w];
-    all += sums[w];
-  }
-  const int64_t units = (int64_t)p.kv_heads * p.slices;  // per sequence
-  const int64_t total = all * units;
-  const int64_t grid = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
-  if (blockIdx.x >= grid) return;
-  int64_t pos = blockIdx.x * total / grid;
-  const int64_t end = (blockIdx.x + 1) * total / grid;
-  if ((int64_t)(upto - mine) * units <= pos && pos < (int64_t)upto * units) {
-    uint32_t before = upto - mine;
-    int b = b_lo;
-    for (;; ++b) {
-      const uint32_t n = (uint32_t)(clamped_length(p, b) + kBlock - 1) / kBlock;
-      if (pos < (int64_t)(before + n) * units) break;
-      before += n;
-    }
-    found[0] = b;
-    found[1] = (int)before;
-  }
-  __syncthreads();
-  int b = uniform(found[0]);
-  uint32_t before = (uint32_t)uniform(found[1]);
+  if (blockIdx.x >= line.grid) return;
+  uint32_t pos = line.begin(blockIdx.x);
+  const uint32_t end = line.begin(blockIdx.x + 1);
+  const int at = __builtin_ctzll(__ballot(pos < line.upto * line.rows));
+  int b = at * line.per;
+  uint32_t before = (uint32_t)__builtin_amdgcn_readlane(line.upto - line.mine, at);
 
   W st;
   while (pos < end) {
     int len = uniform(clamped_length(p, b));
-    int blocks = (int)((uint32_t)(len + kBlock - 1) / kBlock);
-    while (pos >= (int64_t)(before + blocks) * units) {
-      before += blocks;
+    uint32_t chunks = line.chunks(len);
+    while (pos >= (before + chunks) * line.rows) {
+      before += chunks;
       ++b;
       len = uniform(clamped_length(p, b));
-      blocks = (int)((uint32_t)(len + kBlock - 1) / kBlock);
+      chunks = line.chunks(len);
     }
-    const int64_t in_seq = pos - (int64_t)before * units;
-    const int unit = uniform((int)(in_seq / blocks));
-    const int blk0 = (int)(in_seq - (int64_t)unit * blocks);
+    const uint32_t in_seq = pos - before * line.rows;
+    const int unit = uniform(in_seq / chunks);
+    const uint32_t c0 = in_seq - unit * chunks;
     const int head = uniform(unit / p.slices), slice = unit - head * p.slices;
-    const int64_t left = end - pos;
-    const int blk1 = left < blocks - blk0 ? blk0 + (int)left : blocks;
-    const int64_t unit_pos = pos - blk0;
-    pos += blk1 - blk0;
+    const uint32_t c1 = end - pos < chunks - c0 ? c0 + (end - pos) : chunks;
+    pos += c1 - c0;
 
-    st.start(p, b, head, slice, len);
-    st.run(p, b, head, slice, len, blk0, blk1);
-    float r[NR];
-    st.fold(r);
-    join_waves<NT, NR>(st.m, st.l, r, ml, buf);
-
-    if (blk0 != 0 || blk1 != blocks) {
-      // a piece: to the workspace, and join if it is the unit's last to arrive
-      const int lane = lane_here();
-      constexpr int PF = piece_floats<D, NT>();
-      const int64_t w0 = ((unit_pos + 1) * grid - 1) / total;
-      const int n = uniform((int)(((unit_pos + blocks) * grid - 1) / total - w0) + 1);
-      if (wave == 0) {
-        const Span to = span(p.parts, (2 * (int64_t)blockIdx.x + (blk0 == 0)) * (PF * 4), PF * 4);
-        const int c = lane & 15, h = lane >> 4;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int e = 0; e < 4 * VN; e += 4) {
-              f32x4v y;
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                y[x] = r[((nt * NG + g) * VN + (e + x) % VN) * 4 + (e + x) / VN];
-              put_piece(to, (nt * 16 + c) * D + g * G + 4 * h * VN + e, y);
-            }
-          if (h < 2) {
-            const float x = h ? st.l[nt] : st.m[nt];
-            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), to,
-                                                  (NT * 16 * D + nt * 32 + lane) * 4, 0, kDeviceScope);
-          }
-        }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        if (lane == 0)
-          flag = __hip_atomic_fetch_add(p.arrived + w0, 1u, __ATOMIC_RELAXED,
-                                        __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(n - 1);
-      }
-      __syncthreads();
-      const bool last = uniform((int)flag) != 0;
-      __syncthreads();
-      if (last) {
-        asm volatile("" ::: "memory");
-        if (threadIdx.x == 0)
-          __hip_atomic_store(p.arrived + w0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        join_pieces<D, NT>(p, b, head, slice, w0, n, ml, buf);
-      }
-      continue;
+    const int tiles = (len + kTile - 1) / kTile, tile0 = (int)(c0 * (line.chunk / kTile));
+    int tile1 = (int)(c1 * (line.chunk / kTile));
+    tile1 = tile1 < tiles ? tile1 : tiles;
+    const int busy = tile1 - tile0 < NW ? tile1 - tile0 : NW;
+    const int cols = p.L * p.group - slice * NT * 16, used = cols < NT * 16 ? cols : NT * 16;
+    __syncthreads();  // the last round's readers of LDS are done
+    if (wave < busy) {
+      st.run(p, b, head, slice, len, tile0 + wave, tile1);
+      st.give(buf + wave * W::SHARE, ml + wave * NT * 32, used);
     }
-    if (wave == 0) {
-      // a lane's results of a group are G/4 neighbouring values: 4 rows of VN
-      const int lane = lane_here(), cols = p.L * p.group, h = lane >> 4;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int c = (slice * NT + nt) * 16 + (lane & 15);
-        if (c >= cols) continue;
-        const int i = c / p.group, j = c - i * p.group;
-        uint16_t *out = reinterpret_cast<uint16_t *>(p.out) +
-                        (((int64_t)b * p.L + i) * p.kv_heads * p.group + head * p.group + j) * D;
-        const float inv = st.l[nt] == 0.f ? 0.f : 1.f / st.l[nt];
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int e = 0; e < 4 * VN; e += 8) {
-            float y[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              y[x] = r[((nt * NG + g) * VN + (e + x) % VN) * 4 + (e + x) / VN] * inv;
-            const int64_t at = g * G + 4 * h * VN + e;
-            if (p.x_dtype == X_F16)
-              store8<X_F16>(out, at, y);
-            else
-              store8<X_BF16>(out, at, y);
-          }
+    __syncthreads();
+
+    // every four values of the rows, over the waves' shares: to the output, or,
+    // where this is only a piece of the unit, to the workspace (a workgroup's
+    // second place is for the piece that starts its unit)
+    const bool whole = c0 == 0 && c1 == chunks;
+    float *to = p.parts + (2 * (int64_t)blockIdx.x + (c0 == 0)) * W::PF;
+    constexpr int Q = D / 4;
+    for (int item = threadIdx.x; item < used * Q; item += 64 * NW) {
+      const int c = item / Q, at = (item % Q) * 4;
+      const float *mc = ml + (c >> 4) * 32 + (c & 15);
+      float top = kNegInf, l = 0.f;
+      for (int w = 0; w < busy; ++w) top = __builtin_fmaxf(top, mc[w * NT * 32]);
+      const float base = top == kNegInf ? 0.f : top;
+      f32x4v y = {0.f, 0.f, 0.f, 0.f};
+      for (int w = 0; w < busy; ++w) {
+        const float f = exp2_fast(mc[w * NT * 32] - base);
+        l += mc[w * NT * 32 + 16] * f;
+        y += *reinterpret_cast<const f32x4v *>(buf + w * W::SHARE + c * W::ROW + at) * f;
+      }
+      if (whole) {
+        put_result<D>(p, b, head, slice * NT * 16 + c, at, y * (l == 0.f ? 0.f : 1.f / l));
+      } else {
+        *reinterpret_cast<f32x4v *>(to + c * D + at) = y;
+        if (at == 0) {
+          to[NT * 16 * D + c] = top;
+          to[NT * 16 * D + NT * 16 + c] = l;
+        }
       }
     }
   }
+}
+
+// Joins the pieces of units that were cut: a workgroup takes 64 times four
+// values of one unit, its eight waves every eighth piece each, and adds the
+// waves' parts in order, so the result does not depend on timing.  (A second
+// launch: joined by whichever workgroup arrives last, one workgroup reads all
+// of a unit's pieces and the others of the chip are idle: 190 us for three
+// sequences of up to 20001 tokens and one key head of 256, against ## us.)
+constexpr int kJoinWaves = 8;
+template <int D>
+__global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, int nt, int workgroups) {
+  __shared__ float part[kJoinWaves][6][64];
+  const int lane = lane_here(), wave = uniform(threadIdx.x >> 6);
+  const Line line(p, workgroups, lane);
+  const uint32_t rows = line.rows;
+  const int b = blockIdx.x / rows, unit = blockIdx.x - b * rows;
+  const uint32_t chunks = line.chunks(clamped_length(p, b));
+  if (chunks < 2) return;
+  // chunks of the sequences before b: the lanes before its, and in its lane
+  const int at = b / line.per;
+  uint32_t before = (uint32_t)__builtin_amdgcn_readlane(line.upto - line.mine, at);
+  for (int x = at * line.per; x < b; ++x) before += line.chunks(clamped_length(p, x));
+  const uint32_t pos = before * rows + unit * chunks;
+  const int w0 = uniform(line.owner(pos)), n = uniform(line.owner(pos + chunks - 1)) - w0 + 1;
+  if (n < 2) return;
+
+  constexpr int Q = D / 4;
+  const int head = unit / p.slices, slice = unit - head * p.slices;
+  const int cols = p.L * p.group - slice * nt * 16, used = cols < nt * 16 ? cols : nt * 16;
+  const int item = blockIdx.y * 64 + lane;
+  const bool on = item < used * Q;
+  const int c = on ? item / Q : 0, d = on ? (item % Q) * 4 : 0;
+  const int PF = piece_floats(D, nt);
+  const float *first = p.parts + (2 * (int64_t)w0 + 1) * PF;
+  float m = kNegInf, l = 0.f;
+  f32x4v acc = {0.f, 0.f, 0.f, 0.f};
+  constexpr int U = 4;
+  for (int i = wave; i < n; i += U * kJoinWaves) {
+    f32x4v v[U];
+    float pm[U], pl[U];
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      const int k = i + x * kJoinWaves < n ? i + x * kJoinWaves : i;
+      const float *src = first + (k ? (2 * (int64_t)k - 1) * PF : 0);
+      v[x] = *reinterpret_cast<const f32x4v *>(src + c * D + d);
+      pm[x] = src[nt * 16 * D + c];
+      pl[x] = src[nt * 16 * D + nt * 16 + c];
+    }
+    float top = m;
+#pragma unroll
+    for (int x = 0; x < U; ++x) top = __builtin_fmaxf(top, pm[x]);
+    const float base = top == kNegInf ? 0.f : top, keep = exp2_fast(m - base);
+    m = top;
+    l *= keep;
+    acc *= keep;
+#pragma unroll
+    for (int x = 0; x < U; ++x)
+      if (i + x * kJoinWaves < n) {
+        const float f = exp2_fast(pm[x] - base);
+        l += pl[x] * f;
+        acc += v[x] * f;
+      }
+  }
+  part[wave][0][lane] = m;
+  part[wave][1][lane] = l;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) part[wave][2 + x][lane] = acc[x];
+  __syncthreads();
+  if (wave != 0 || !on) return;
+  for (int w = 1; w < kJoinWaves && w < n; ++w) {
+    const float pm = part[w][0][lane], top = __builtin_fmaxf(m, pm), base = top == kNegInf ? 0.f : top;
+    const float f = exp2_fast(m - base), g = exp2_fast(pm - base);
+    m = top;
+    l = l * f + part[w][1][lane] * g;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) acc[x] = acc[x] * f + part[w][2 + x][lane] * g;
+  }
+  put_result<D>(p, b, head, slice * nt * 16 + c, d, acc * (l == 0.f ? 0.f : 1.f / l));
 }
 
 // query rows per slice: two tiles of 16 where there are more than 16
@@ -1027,17 +998,12 @@ constexpr int wgs_per_cu(int D, int NG, int NT) {
   return D * NT <= 128 && NG <= 2 ? 3 : (D * NT <= 128 || (D * NT <= 256 && NG <= 2) ? 2 : 1);
 }
 
-int grid_for(int D, int ng, int nt) {
-  const int n = device_cus() * wgs_per_cu(D, ng, nt);
-  return n < kMaxGrid ? n : kMaxGrid;
-}
-
 }  // namespace
 
 int64_t attn_workspace_bytes(int64_t, int L, int q_heads, int kv_heads, int head_dim) {
   const int nt = tiles_for((int64_t)L * (q_heads / kv_heads));
-  const int64_t piece = (int64_t)nt * head_dim * 16 + nt * 32;
-  return kMaxGrid * 4 + 2 * (int64_t)grid_for(head_dim, 1, nt) * piece * 4;
+  const int wgs = device_cus() * wgs_per_cu(head_dim, 1, nt);
+  return (int64_t)wgs * 2 * piece_floats(head_dim, nt) * 4;
 }
 
 hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream_t s) {
@@ -1053,8 +1019,7 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
   p.table = a.page_table;
   p.lengths = a.lengths;
   p.out = a.out;
-  p.arrived = reinterpret_cast<uint32_t *>(a.workspace);
-  p.parts = reinterpret_cast<float *>(a.workspace) + kMaxGrid;
+  p.parts = reinterpret_cast<float *>(a.workspace);
   p.max_pages = a.max_pages;
   p.num_pages = c.num_pages;
   p.page_subs = (uint32_t)c.page_size / 16;
@@ -1068,31 +1033,42 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
   const int64_t cols = (int64_t)a.L * p.group;
   const int nt = tiles_for(cols);
   p.slices = (int)((cols + 16 * nt - 1) / (16 * nt));
-  // no more workgroups than blocks the table can hold
-  const int64_t blocks = (a.max_pages * c.page_size + kBlock - 1) / kBlock;
-  int64_t grid = grid_for(c.head_dim, c.bits == 16 ? 1 : c.head_dim / c.group_size, nt);
-  if (blocks * a.B < grid && blocks * a.B * c.kv_heads * p.slices < grid)
-    grid = blocks * a.B * c.kv_heads * p.slices;
-#define AQ_K(B, F, D, G)                                                                      \
-  do {                                                                                        \
-    if (nt == 1)                                                                              \
-      hipLaunchKernelGGL((attn_kernel<B, F, D, G, 1, wgs_per_cu(D, D / G, 1)>), dim3((unsigned)grid), \
-                         dim3(256), 0, s, p);                                                 \
-    else                                                                                      \
-      hipLaunchKernelGGL((attn_kernel<B, F, D, G, 2, wgs_per_cu(D, D / G, 2)>), dim3((unsigned)grid), \
-                         dim3(256), 0, s, p);                                                 \
-    return hipGetLastError();                                                                 \
+  // The line's chunks are counted in 32 bits: where the table could hold more
+  // tiles than that they are longer.  A table that holds no more than one tile
+  // per wave leaves units whole.
+  const int64_t cap = a.max_pages * c.page_size, per_tile = (int64_t)a.B * c.kv_heads * p.slices;
+  int64_t chunk = cap <= NW * kTile ? NW * kTile : kTile;
+  while ((cap + chunk - 1) / chunk * per_tile > 0x7FFFFFFF) chunk *= 2;
+  p.chunk = (uint32_t)chunk;
+  // no more workgroups than chunks the table can hold
+  const int64_t most = (cap + chunk - 1) / chunk * per_tile;
+  int64_t grid = (int64_t)device_cus() *
+                 wgs_per_cu(c.head_dim, c.bits == 16 ? 1 : c.head_dim / c.group_size, nt);
+  if (most < grid) grid = most;
+  hipError_t err = hipErrorInvalidValue;
+#define AQ_KT(B, F, D, G, T)                                                           \
+  hipLaunchKernelGGL((attn_kernel<B, F, D, G, T, wgs_per_cu(D, D / G, T)>),            \
+                     dim3((unsigned)grid), dim3(64 * NW), 0, s, p)
+#define AQ_K(B, F, D, G)                                                               \
+  do {                                                                                 \
+    if (nt == 1)                                                                       \
+      AQ_KT(B, F, D, G, 1);                                                            \
+    else                                                                               \
+      AQ_KT(B, F, D, G, 2);                                                            \
+    err = hipGetLastError();                                                           \
   } while (0)
 #define AQ_G(B, D)                                     \
   if (c.head_dim == D) {                               \
     if (c.group_size == 32) AQ_K(B, false, D, 32);     \
     if (c.group_size == 64) AQ_K(B, false, D, 64);     \
-    if constexpr (D >= 128) AQ_K(B, false, D, 128);    \
+    if constexpr (D >= 128) {                          \
+      if (c.group_size == 128) AQ_K(B, false, D, 128); \
+    }                                                  \
   }
 #define AQ_H(D)                                        \
   if (c.head_dim == D) {                               \
     if (c.dtype == X_BF16) AQ_K(16, true, D, D);       \
-    AQ_K(16, false, D, D);                             \
+    else AQ_K(16, false, D, D);                        \
   }
   if (c.bits == 4) { AQ_G(4, 64) AQ_G(4, 128) AQ_G(4, 256) }
   if (c.bits == 8) { AQ_G(8, 64) AQ_G(8, 128) AQ_G(8, 256) }
@@ -1100,7 +1076,18 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
 #undef AQ_H
 #undef AQ_G
 #undef AQ_K
-  return hipErrorInvalidValue;
+#undef AQ_KT
+  // (a chunk that holds the whole table: no unit is cut)
+  if (err != hipSuccess || cap <= chunk) return err;
+  const int items = (int)(cols < 16 * nt ? cols : 16 * nt) * c.head_dim / 4;
+  const dim3 join((unsigned)per_tile, (unsigned)((items + 63) / 64));
+#define AQ_J(D) \
+  hipLaunchKernelGGL((attn_join_kernel<D>), join, dim3(64 * kJoinWaves), 0, s, p, nt, (int)grid)
+  if (c.head_dim == 64) AQ_J(64);
+  else if (c.head_dim == 128) AQ_J(128);
+  else AQ_J(256);
+#undef AQ_J
+  return hipGetLastError();
 }
 
 }  // namespace aq
