@@ -590,8 +590,8 @@ def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_bias
     """Attention of the newest L tokens of every sequence over the paged cache: q [B, L, q_heads,
     head_dim] or [B, q_heads, head_dim] (L = 1; tokens may be strided), page_table int32 [B,
     max_pages], lengths int32 [B] (cached tokens, the L new ones included) -> out of q's shape.
-    scale: default head_dim ** -0.5.  workspace: a device buffer zeroed once (see
-    aq_paged_attention_workspace); without one each call makes and clears its own."""
+    scale: default head_dim ** -0.5.  workspace: a device buffer of
+    aq_paged_attention_workspace bytes; without one each call allocates its own."""
     torch = _torch()
     lib = load_library()
     cache = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
@@ -618,7 +618,7 @@ def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_bias
         raise ValueError("out must have q's shape and dtype")
     if workspace is None:
         need = lib.aq_paged_attention_workspace(B, L, Hq, cache.kv_heads, dim)
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     st = lib.aq_paged_attention(qp, _dtype_code(q), B, L, Hq, qs, ctypes.byref(cache),
                                 _index(page_table, torch.int32, "page_table"),
                                 page_table.shape[1], _index(lengths, torch.int32, "lengths"),

@@ -199,6 +199,8 @@ struct Params {
   const int32_t *table, *lengths;
   void *out;
   float *parts;  // two pieces per workgroup
+  int4 *cuts;    // per workgroup: pieces, sequence, key head and slice of the unit that starts in
+                 // its last piece, 0 pieces where none does
   int64_t max_pages, num_pages;
   uint32_t page_subs, page_magic;  // page_size / 16 and floor(2^32 / that) + 1
   int kv_heads, group, L, B, slices, x_dtype;
@@ -283,7 +285,7 @@ struct Line {
   __device__ __forceinline__ uint32_t begin(uint32_t w) const {
     return w * share + (w < longer ? w : longer);
   }
-  // the workgroup that has chunk `at`
+  // the workgroup that takes chunk `at`
   __device__ __forceinline__ uint32_t owner(uint32_t at) const {
     const uint32_t first = longer * (share + 1);
     return at < first ? at / (share + 1) : longer + (at - first) / share;
@@ -844,7 +846,11 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
           reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + b * row_halves)[i] =
               make_uint4(0, 0, 0, 0);
   }
-  if (blockIdx.x >= line.grid) return;
+  if (blockIdx.x >= line.grid) {
+    if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  int4 cut = make_int4(0, 0, 0, 0);
   uint32_t pos = line.begin(blockIdx.x);
   const uint32_t end = line.begin(blockIdx.x + 1);
   const int at = __builtin_ctzll(__ballot(pos < line.upto * line.rows));
@@ -866,6 +872,7 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
     const uint32_t c0 = in_seq - unit * chunks;
     const int head = uniform(unit / p.slices), slice = unit - head * p.slices;
     const uint32_t c1 = end - pos < chunks - c0 ? c0 + (end - pos) : chunks;
+    const uint32_t unit_end = pos - c0 + chunks;
     pos += c1 - c0;
 
     const int tiles = (len + kTile - 1) / kTile, tile0 = (int)(c0 * (line.chunk / kTile));
@@ -884,6 +891,8 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
     // where this is only a piece of the unit, to the workspace (a workgroup's
     // second place is for the piece that starts its unit)
     const bool whole = c0 == 0 && c1 == chunks;
+    if (c0 == 0 && !whole)
+      cut = make_int4((int)(line.owner(unit_end - 1) - blockIdx.x) + 1, b, head, slice);
     float *to = p.parts + (2 * (int64_t)blockIdx.x + (c0 == 0)) * W::PF;
     constexpr int Q = D / 4;
     for (int item = threadIdx.x; item < used * Q; item += 64 * NW) {
@@ -909,6 +918,7 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
       }
     }
   }
+  if (threadIdx.x == 0) p.cuts[blockIdx.x] = cut;
 }
 
 // Joins the pieces of units that were cut: a workgroup takes 64 times four
@@ -916,27 +926,17 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
 // waves' parts in order, so the result does not depend on timing.  (A second
 // launch: joined by whichever workgroup arrives last, one workgroup reads all
 // of a unit's pieces and the others of the chip are idle: 190 us for three
-// sequences of up to 20001 tokens and one key head of 256, against ## us.)
+// sequences of up to 20001 tokens and one key head of 256, against 22 us.)
 constexpr int kJoinWaves = 8;
 template <int D>
-__global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, int nt, int workgroups) {
+__global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, int nt) {
   __shared__ float part[kJoinWaves][6][64];
+  const int w0 = blockIdx.x;
+  const int4 cut = p.cuts[w0];
+  const int n = uniform(cut.x), b = uniform(cut.y), head = uniform(cut.z), slice = uniform(cut.w);
+  if (n == 0) return;
   const int lane = lane_here(), wave = uniform(threadIdx.x >> 6);
-  const Line line(p, workgroups, lane);
-  const uint32_t rows = line.rows;
-  const int b = blockIdx.x / rows, unit = blockIdx.x - b * rows;
-  const uint32_t chunks = line.chunks(clamped_length(p, b));
-  if (chunks < 2) return;
-  // chunks of the sequences before b: the lanes before its, and in its lane
-  const int at = b / line.per;
-  uint32_t before = (uint32_t)__builtin_amdgcn_readlane(line.upto - line.mine, at);
-  for (int x = at * line.per; x < b; ++x) before += line.chunks(clamped_length(p, x));
-  const uint32_t pos = before * rows + unit * chunks;
-  const int w0 = uniform(line.owner(pos)), n = uniform(line.owner(pos + chunks - 1)) - w0 + 1;
-  if (n < 2) return;
-
   constexpr int Q = D / 4;
-  const int head = unit / p.slices, slice = unit - head * p.slices;
   const int cols = p.L * p.group - slice * nt * 16, used = cols < nt * 16 ? cols : nt * 16;
   const int item = blockIdx.y * 64 + lane;
   const bool on = item < used * Q;
@@ -1003,7 +1003,7 @@ constexpr int wgs_per_cu(int D, int NG, int NT) {
 int64_t attn_workspace_bytes(int64_t, int L, int q_heads, int kv_heads, int head_dim) {
   const int nt = tiles_for((int64_t)L * (q_heads / kv_heads));
   const int wgs = device_cus() * wgs_per_cu(head_dim, 1, nt);
-  return (int64_t)wgs * 2 * piece_floats(head_dim, nt) * 4;
+  return (int64_t)wgs * (16 + 2 * piece_floats(head_dim, nt) * 4);
 }
 
 hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream_t s) {
@@ -1019,7 +1019,6 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
   p.table = a.page_table;
   p.lengths = a.lengths;
   p.out = a.out;
-  p.parts = reinterpret_cast<float *>(a.workspace);
   p.max_pages = a.max_pages;
   p.num_pages = c.num_pages;
   p.page_subs = (uint32_t)c.page_size / 16;
@@ -1045,6 +1044,8 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
   int64_t grid = (int64_t)device_cus() *
                  wgs_per_cu(c.head_dim, c.bits == 16 ? 1 : c.head_dim / c.group_size, nt);
   if (most < grid) grid = most;
+  p.cuts = reinterpret_cast<int4 *>(a.workspace);
+  p.parts = reinterpret_cast<float *>(p.cuts + grid);
   hipError_t err = hipErrorInvalidValue;
 #define AQ_KT(B, F, D, G, T)                                                           \
   hipLaunchKernelGGL((attn_kernel<B, F, D, G, T, wgs_per_cu(D, D / G, T)>),            \
@@ -1080,9 +1081,9 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
   // (a chunk that holds the whole table: no unit is cut)
   if (err != hipSuccess || cap <= chunk) return err;
   const int items = (int)(cols < 16 * nt ? cols : 16 * nt) * c.head_dim / 4;
-  const dim3 join((unsigned)per_tile, (unsigned)((items + 63) / 64));
+  const dim3 join((unsigned)grid, (unsigned)((items + 63) / 64));
 #define AQ_J(D) \
-  hipLaunchKernelGGL((attn_join_kernel<D>), join, dim3(64 * kJoinWaves), 0, s, p, nt, (int)grid)
+  hipLaunchKernelGGL((attn_join_kernel<D>), join, dim3(64 * kJoinWaves), 0, s, p, nt)
   if (c.head_dim == 64) AQ_J(64);
   else if (c.head_dim == 128) AQ_J(128);
   else AQ_J(256);
