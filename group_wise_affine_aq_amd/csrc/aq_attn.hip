@@ -228,10 +228,11 @@ constexpr int piece_floats(int D, int NT) { return NT * (16 * D + 32); }
 
 // ---- the work line ------------------------------------------------------------------
 // All tiles of all units -- a unit is one sequence, key head and slice of query
-// rows -- in one line, sequences first, cut evenly.  It is counted in chunks:
-// single tiles, or, where one pass of the waves takes all there is, four
-// tiles, so that a workgroup's waves all have one and no unit is cut without
-// need.
+// rows -- in one line, sequences first, cut evenly.  A workgroup whose part
+// begins in one unit and ends in another waits twice for first loads (about
+// 7 us), so the line is counted in chunks that do not cross units, as many as
+// there are workgroups at most, as long as they need not be more than 20 tiles
+// (the work of 7 us) larger than an even cut in single tiles.
 
 // inclusive sum over the lanes, a row of 16 and then the rows
 __device__ __forceinline__ uint32_t lanes_prefix(uint32_t v) {
@@ -254,15 +255,12 @@ struct Line {
 
   __device__ __forceinline__ uint32_t chunks(uint32_t len) const { return (len + chunk - 1) / chunk; }
 
+  int len;            // its first sequence's length
+
   __device__ __forceinline__ uint32_t count(const Params &p, int lane) {
     const int lo = lane * per < p.B ? lane * per : p.B, hi = lo + per < p.B ? lo + per : p.B;
-    mine = 0;
-    idle = false;
-    for (int b = lo; b < hi; ++b) {
-      const int len = clamped_length(p, b);
-      mine += chunks(len);
-      idle |= len == 0;
-    }
+    mine = lo < hi ? chunks(len) : 0;
+    for (int b = lo + 1; b < hi; ++b) mine += chunks(clamped_length(p, b));
     upto = lanes_prefix(mine);
     return (uint32_t)uniform(__builtin_amdgcn_readlane(upto, 63)) * rows;
   }
@@ -271,11 +269,23 @@ struct Line {
   __device__ __forceinline__ Line(const Params &p, uint32_t most, int lane) {
     rows = p.kv_heads * p.slices;
     per = (p.B + 63) / 64;
+    const int lo = lane * per < p.B ? lane * per : p.B, hi = lo + per < p.B ? lo + per : p.B;
+    len = lo < hi ? clamped_length(p, lo) : 1;
+    idle = len == 0;
+    for (int b = lo + 1; b < hi; ++b) idle |= clamped_length(p, b) == 0;
     chunk = p.chunk;
     uint32_t total = count(p, lane);
-    if (chunk == kTile && total <= most * NW) {
-      chunk = NW * kTile;
-      total = count(p, lane);
+    if (chunk == kTile && rows * p.B <= most) {
+      const uint32_t even = (total + NW * most - 1) / (NW * most) * NW;
+      for (uint32_t more = 0; more <= 20 && chunk == kTile; more += NW) {
+        chunk = (even + more) * kTile;
+        const uint32_t n = count(p, lane);
+        if (n <= most)
+          total = n;
+        else
+          chunk = kTile;
+      }
+      if (chunk == kTile) total = count(p, lane);
     }
     grid = total < most ? total : most;
     share = grid ? total / grid : 0;
@@ -858,8 +868,8 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
   uint32_t before = (uint32_t)__builtin_amdgcn_readlane(line.upto - line.mine, at);
 
   W st;
+  int len = uniform(__builtin_amdgcn_readlane(line.len, at));
   while (pos < end) {
-    int len = uniform(clamped_length(p, b));
     uint32_t chunks = line.chunks(len);
     while (pos >= (before + chunks) * line.rows) {
       before += chunks;
