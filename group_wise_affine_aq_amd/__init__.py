@@ -129,17 +129,25 @@ def aq_qweight_bytes(N: int, K: int, group_size: int, bits: int) -> int:
 
 
 # ---- marshalling -----------------------------------------------------------------------
+_torch_module = None
+_dtype_codes = {}
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _dtype_codes.update({torch.float32: AQ_F32, torch.float16: AQ_F16, torch.bfloat16: AQ_BF16})
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
-    torch = _torch()
-    m = {torch.float32: AQ_F32, torch.float16: AQ_F16, torch.bfloat16: AQ_BF16}
-    if t.dtype not in m:
+    _torch()
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return code
 
 
 def _torch_dtype(code: int):
@@ -479,25 +487,37 @@ def aq_qmv_fp_describe(N: int, K: int, mode: str, x_dtype="f16") -> str:
 # A cache is three arrays for K and three for V: codes int32 [pages, kv_heads, page_size,
 # head_dim*bits/32], scales and biases fp16 [pages, kv_heads, page_size, head_dim/group_size];
 # with bits = 16 the codes are the values, fp16 or bf16 [pages, kv_heads, page_size, head_dim],
-# and scales and biases are None.
+# and scales and biases are None.  A decode step makes one such call per layer, so what runs
+# before the launch is kept short.
+def _queue(stream, t):
+    """The stream's handle; without one, that of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    try:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    except AttributeError:  # (a torch without the short way)
+        return torch.cuda.current_stream(t.device).cuda_stream
+
+
 def _rows(t, name):
     """Device address of [tokens, heads, head_dim] rows, heads and head_dim contiguous, and the
     tokens' distance in elements."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     stride, inner, last = t.stride()
-    _, h, d = t.shape
+    n, h, d = t.shape
     if last != 1 or (h > 1 and inner != d):
         raise ValueError(f"{name}: heads and head_dim must be contiguous")
-    return t.data_ptr(), (stride if t.shape[0] > 1 else h * d)
+    return t.data_ptr(), (stride if n > 1 else h * d)
 
 
-def _cache_array(t, dtype, shape, name):
+def _array(t, dtype, shape, name):
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, {dtype} expected")
-    if t.shape != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} expected")
     if not (t.is_cuda and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous device tensor")
@@ -506,52 +526,46 @@ def _cache_array(t, dtype, shape, name):
 
 def _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits):
     torch = _torch()
-    pages, heads, page, words = shape = k_codes.shape
+    shape = k_codes.shape
+    pages, heads, page, words = shape
     if bits == 16:
-        dim, kind, code = words, k_codes.dtype, _dtype_code(k_codes)
+        code = _dtype_code(k_codes)
         if code == AQ_F32:
             raise TypeError("a 16-bit cache holds float16 or bfloat16")
-        scales = (None, None, None, None)
-        group_size = 0
-    else:
-        if bits not in (4, 8):
-            raise AQError(-2 if 2 <= bits <= 8 else -1, "aq_kv_cache")
-        dim, kind, code = words * 32 // bits, torch.int32, 0
-        if group_size < 1 or dim % group_size:
-            raise AQError(-1, "aq_kv_cache")
-        groups = (pages, heads, page, dim // group_size)
-        half = torch.float16
-        scales = (_cache_array(k_scales, half, groups, "k_scales"),
-                  _cache_array(k_biases, half, groups, "k_biases"),
-                  _cache_array(v_scales, half, groups, "v_scales"),
-                  _cache_array(v_biases, half, groups, "v_biases"))
-    return _KVCache(_cache_array(k_codes, kind, shape, "k_codes"), scales[0], scales[1],
-                    _cache_array(v_codes, kind, shape, "v_codes"), scales[2], scales[3],
-                    pages, page, heads, dim, group_size, bits, code)
-
-
-def _index(t, dtype, name):
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, {dtype} expected")
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous device tensor")
-    return t.data_ptr()
+        kind = k_codes.dtype
+        return _KVCache(_array(k_codes, kind, shape, "k_codes"), None, None,
+                        _array(v_codes, kind, shape, "v_codes"), None, None,
+                        pages, page, heads, words, 0, 16, code)
+    if bits != 4 and bits != 8:
+        raise AQError(-2 if 2 <= bits <= 8 else -1, "aq_kv_cache")
+    dim = words * 32 // bits
+    if group_size < 1 or dim % group_size:
+        raise AQError(-1, "aq_kv_cache")
+    groups, half, word = (pages, heads, page, dim // group_size), torch.float16, torch.int32
+    return _KVCache(_array(k_codes, word, shape, "k_codes"),
+                    _array(k_scales, half, groups, "k_scales"),
+                    _array(k_biases, half, groups, "k_biases"),
+                    _array(v_codes, word, shape, "v_codes"),
+                    _array(v_scales, half, groups, "v_scales"),
+                    _array(v_biases, half, groups, "v_biases"),
+                    pages, page, heads, dim, group_size, bits, 0)
 
 
 def aq_kv_append(k, v, slots, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases,
                  group_size: int, bits: int, stream=None):
     """Quantize k, v [T, kv_heads, head_dim] (fp16/bf16; tokens may be strided) into the cache at
     slots int64 [T] = page * page_size + place (outside the cache: not written)."""
+    lib = load_library()
     cache = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
     T = slots.numel()
     shape = (T, cache.kv_heads, cache.head_dim)
-    if tuple(k.shape) != shape or tuple(v.shape) != shape or k.dtype != v.dtype:
+    if k.shape != shape or v.shape != shape or k.dtype is not v.dtype:
         raise ValueError(f"aq_kv_append: k and v must be {shape} of one dtype")
     kp, ks = _rows(k, "k")
     vp, vs = _rows(v, "v")
-    st = load_library().aq_kv_append(kp, vp, _dtype_code(k), T, ks, vs,
-                                     _index(slots, _torch().int64, "slots"), ctypes.byref(cache),
-                                     _stream(stream))
+    st = lib.aq_kv_append(kp, vp, _dtype_code(k), T, ks, vs,
+                          _array(slots, _torch().int64, None, "slots"), ctypes.byref(cache),
+                          _queue(stream, slots))
     _check(st, "aq_kv_append")
 
 
@@ -560,17 +574,20 @@ def aq_kv_read(slots, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, 
     """Rows of the cache at slots int64 [T] -> (k, v) [T, kv_heads, head_dim] in out_dtype
     (default fp16); a slot outside the cache gives zeros."""
     torch = _torch()
+    lib = load_library()
     cache = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
     T = slots.numel()
     shape = (T, cache.kv_heads, cache.head_dim)
-    if k is None:
-        k = torch.empty(shape, dtype=out_dtype or torch.float16, device=slots.device)
-    if v is None:
+    if k is None and v is None:
+        k, v = torch.empty((2,) + shape, dtype=out_dtype or torch.float16, device=slots.device)
+    elif k is None:
+        k = torch.empty(shape, dtype=v.dtype, device=slots.device)
+    elif v is None:
         v = torch.empty(shape, dtype=k.dtype, device=slots.device)
-    if tuple(k.shape) != shape or tuple(v.shape) != shape or k.dtype != v.dtype:
-        raise ValueError(f"aq_kv_read: k and v must be {shape} of one dtype")
-    st = load_library().aq_kv_read(_index(slots, torch.int64, "slots"), T, ctypes.byref(cache),
-                                   _dev(k, "k"), _dev(v, "v"), _dtype_code(k), _stream(stream))
+    kind = k.dtype
+    st = lib.aq_kv_read(_array(slots, torch.int64, None, "slots"), T, ctypes.byref(cache),
+                        _array(k, kind, shape, "k"), _array(v, kind, shape, "v"), _dtype_code(k),
+                        _queue(stream, slots))
     _check(st, "aq_kv_read")
     return k, v
 
@@ -598,32 +615,34 @@ def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_bias
     dim = cache.head_dim
     if q.dim() == 3:
         B, Hq, D = q.shape
-        L, rows = 1, q
+        L = 1
+        step, inner, last = q.stride()
     else:
         B, L, Hq, D = q.shape
+        outer, step, inner, last = q.stride()
         if L == 1:
-            rows = q[:, 0]
-        elif B == 1 or q.stride(0) == L * q.stride(1):
-            rows = q.as_strided((B * L, Hq, D), (q.stride(1), q.stride(2), q.stride(3)))
-        else:
+            step = outer
+        elif B > 1 and outer != L * step:
             raise ValueError("q: all tokens must lie at one distance")
     if D != dim:
         raise ValueError(f"q: head_dim {D}, the cache has {dim}")
+    if last != 1 or (Hq > 1 and inner != D) or not q.is_cuda:
+        raise ValueError("q: a device tensor, heads and head_dim contiguous")
+    if B * L == 1:
+        step = Hq * D
     if page_table.dim() != 2 or page_table.shape[0] != B or lengths.numel() != B:
         raise ValueError(f"page_table must be [{B}, max_pages] and lengths [{B}]")
-    qp, qs = _rows(rows, "q")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must have q's shape and dtype")
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if workspace is None:
         need = lib.aq_paged_attention_workspace(B, L, Hq, cache.kv_heads, dim)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    st = lib.aq_paged_attention(qp, _dtype_code(q), B, L, Hq, qs, ctypes.byref(cache),
-                                _index(page_table, torch.int32, "page_table"),
-                                page_table.shape[1], _index(lengths, torch.int32, "lengths"),
-                                dim ** -0.5 if scale is None else scale, _dev(out, "out"),
-                                _dev(workspace, "workspace"),
-                                workspace.numel() * workspace.element_size(), _stream(stream))
+    st = lib.aq_paged_attention(q.data_ptr(), _dtype_code(q), B, L, Hq, step, ctypes.byref(cache),
+                                _array(page_table, torch.int32, None, "page_table"),
+                                page_table.shape[1], _array(lengths, torch.int32, None, "lengths"),
+                                dim ** -0.5 if scale is None else scale,
+                                _array(out, q.dtype, q.shape, "out"),
+                                _array(workspace, workspace.dtype, None, "workspace"),
+                                workspace.numel() * workspace.element_size(), _queue(stream, q))
     _check(st, "aq_paged_attention")
     return out
