@@ -459,7 +459,8 @@ aq_status aq_kv_append(const void *k, const void *v, aq_dtype x_dtype, int64_t T
   if (st != AQ_OK || T == 0) return st;
   if (!k || !v || !slots) return AQ_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v) || !aligned16(slots)) return AQ_ERR_ALIGNMENT;
-  if (T > ((int64_t)0x7FFFFFFF * 256) / (width / 8)) return AQ_ERR_UNSUPPORTED;
+  // the grid: at least 8 tokens of one head per workgroup
+  if (T > (int64_t)0x7FFFFFF0 / cache->kv_heads * 8) return AQ_ERR_UNSUPPORTED;
   if (k_stride > ((int64_t)1 << 62) / T || v_stride > ((int64_t)1 << 62) / T)
     return AQ_ERR_UNSUPPORTED;
   return from_hip(aq::launch_kv_append(k, v, (int)x_dtype, T, k_stride, v_stride, slots, *cache,
@@ -476,8 +477,7 @@ aq_status aq_kv_read(const int64_t *slots, int64_t T, const aq_kv_cache *cache, 
   if (st != AQ_OK || T == 0) return st;
   if (!k || !v || !slots) return AQ_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v) || !aligned16(slots)) return AQ_ERR_ALIGNMENT;
-  if (T > ((int64_t)0x7FFFFFFF * 256) / ((int64_t)cache->kv_heads * cache->head_dim / 8))
-    return AQ_ERR_UNSUPPORTED;
+  if (T > (int64_t)0x7FFFFFF0 / cache->kv_heads * 8) return AQ_ERR_UNSUPPORTED;
   return from_hip(aq::launch_kv_read(slots, T, *cache, k, v, (int)out_dtype,
                                      static_cast<hipStream_t>(stream)));
 }

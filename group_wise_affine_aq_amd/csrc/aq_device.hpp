@@ -150,23 +150,34 @@ __device__ __forceinline__ void load32(const void *__restrict__ base, int64_t e,
 }
 
 // ---- stores: 8 consecutive values at element e, rounded to nearest even -------------
+// STREAM: nontemporal, for results too large to be found in a cache later
 
-template <int ODT>
+typedef uint32_t store16v __attribute__((ext_vector_type(4)));
+template <bool STREAM>
+__device__ __forceinline__ void store16(void *p, store16v v) {
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(v, reinterpret_cast<store16v *>(p));
+  else
+    *reinterpret_cast<store16v *>(p) = v;
+}
+
+template <int ODT, bool STREAM = false>
 __device__ __forceinline__ void store8(void *__restrict__ base, int64_t e, const float *v) {
+  store16v u[2];
   if constexpr (ODT == X_F32) {
-    float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(base) + e);
-    p[0] = make_float4(v[0], v[1], v[2], v[3]);
-    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i >> 2][i & 3] = __builtin_bit_cast(uint32_t, v[i]);
+    store16<STREAM>(reinterpret_cast<float *>(base) + e, u[0]);
+    store16<STREAM>(reinterpret_cast<float *>(base) + e + 4, u[1]);
   } else {
-    uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (ODT == X_F16)
-        u[i] = __builtin_bit_cast(uint32_t, half2v{(_Float16)v[2 * i], (_Float16)v[2 * i + 1]});
+        u[0][i] = __builtin_bit_cast(uint32_t, half2v{(_Float16)v[2 * i], (_Float16)v[2 * i + 1]});
       else
-        u[i] = __builtin_bit_cast(uint32_t, bf16x2v{(__bf16)v[2 * i], (__bf16)v[2 * i + 1]});
+        u[0][i] = __builtin_bit_cast(uint32_t, bf16x2v{(__bf16)v[2 * i], (__bf16)v[2 * i + 1]});
     }
-    *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(base) + e) = make_uint4(u[0], u[1], u[2], u[3]);
+    store16<STREAM>(reinterpret_cast<uint16_t *>(base) + e, u[0]);
   }
 }
 
