@@ -302,6 +302,11 @@ struct Line {
   }
 };
 
+// N words moved as one, whatever they are otherwise accessed as
+template <int N>
+struct __attribute__((may_alias, aligned(N >= 4 ? 16 : 4 * N))) words { uint32_t w[N]; };
+typedef uint16_t __attribute__((may_alias)) u16_any;
+
 // ---- one wave's state over a segment of tokens -------------------------------------
 // BITS 4, 8 or 16; BF: operands are bf16 (bits = 16 with a bf16 cache); G is
 // head_dim for 16 bits.
@@ -327,9 +332,18 @@ struct Wave {
   static constexpr float CENTRE = BITS == 8 ? 128.f : 8.f;
   static constexpr float UP = BITS == 8 ? 6.f : (BITS == 4 ? 2.f : 0.f);
 
+  struct Keys { uint32_t c[2][KW]; };
+  struct Values { uint32_t c[8][NG][VW]; };
+  // Scales and biases of a tile are fetched once: lane 16 a + t has array a
+  // (K scales, K biases, V scales, V biases), token t of each 16.  Through a
+  // strip of LDS of the wave's own every lane then gets those of its four
+  // tokens.  (Every lane fetching its own: 32 registers for the time that
+  // loads are under way instead of 2, and twice the codes' bytes through the
+  // load path.)
+  static constexpr int TB = NG * 2;            // bytes per token and array
+  static constexpr int RW = TB < 4 ? 1 : TB / 4;
+  struct Raw { uint32_t w[2][RW]; };
   struct Scales { uint32_t s[2][SW], b[2][SW]; };
-  struct Keys { uint32_t c[2][KW]; Scales g; };
-  struct Values { uint32_t c[8][NG][VW]; Scales g; };
 
   u32x4v q[NT][KS];
   float qsum[NT][NG], C[NT];
@@ -337,16 +351,8 @@ struct Wave {
   float m[NT], l[NT], bacc[NT][NG];
   f32x4v o[NT][NG][VN];
 
-  // The 16 tokens at rows[sub]; there[sub]: whether their page is (if not,
-  // zeros, and nothing is read)
-  static __device__ __forceinline__ void load_scales(Scales &g, const void *s, const void *b,
-                                                     int sub, int64_t row, bool there, int h) {
-    const int bytes = there ? 16 * NG * 2 : 0;
-    fetch<NG * 8>(g.s[sub], span(s, row * (NG * 2), bytes), h * (NG * 8));
-    // without bias arrays every bias is +0
-    fetch<NG * 8>(g.b[sub], span(b ? b : s, row * (NG * 2), b ? bytes : 0), h * (NG * 8));
-  }
-
+  // The 16 tokens at rows[sub]; there[sub]: whether their page is (if not, zero
+  // codes and the first row's scales, which edge tiles do not use)
   static __device__ __forceinline__ void load_keys(Keys &k, const Params &p, const int64_t *rows,
                                                    const bool *there, int lane) {
     const int t = lane & 15, h = lane >> 4;
@@ -357,7 +363,6 @@ struct Wave {
 #pragma unroll
       for (int i = 0; i < PIECES; ++i)  // a piece every 4 lanes' worth along the row
         fetch<PIECE>(k.c[sub] + i * (PIECE / 4), codes, t * RB + h * PIECE + i * 4 * PIECE);
-      if constexpr (QUANT) load_scales(k.g, p.ks, p.kb, sub, rows[sub], there[sub], h);
     }
   }
 
@@ -373,7 +378,53 @@ struct Wave {
 #pragma unroll
         for (int g = 0; g < NG; ++g)
           fetch<VB>(v.c[4 * sub + i][g], codes, 4 * h * RB + t * VB + i * RB + g * (G * BITS / 8));
-      if constexpr (QUANT) load_scales(v.g, p.vs, p.vb, sub, rows[sub], there[sub], h);
+    }
+  }
+
+  // the lane's array, from its token on; without bias arrays every bias is +0
+  // (something is fetched all the same)
+  static __device__ __forceinline__ const char *scales_of(const Params &p, int lane, bool &none) {
+    const int a = lane >> 4;
+    const void *s = a & 2 ? p.vs : p.ks, *b = a & 2 ? p.vb : p.kb;
+    none = (a & 1) && !b;
+    return reinterpret_cast<const char *>((a & 1) && b ? b : s) + (lane & 15) * TB;
+  }
+  static __device__ __forceinline__ void load_scales(Raw &r, const char *from, const int64_t *rows) {
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      const char *at = from + rows[sub] * TB;
+      if constexpr (TB == 2) {
+        r.w[sub][0] = *reinterpret_cast<const uint16_t *>(at);
+      } else {
+        const words<RW> x = *reinterpret_cast<const words<RW> *>(at);
+#pragma unroll
+        for (int i = 0; i < RW; ++i) r.w[sub][i] = x.w[i];
+      }
+    }
+  }
+  static __device__ __forceinline__ void share_scales(const Raw &r, char *strip, int lane, bool none) {
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      char *at = strip + (sub * 64 + lane) * TB;
+      if constexpr (TB == 2) {
+        *reinterpret_cast<u16_any *>(at) = none ? 0 : (uint16_t)r.w[sub][0];
+      } else {
+        words<RW> x;
+#pragma unroll
+        for (int i = 0; i < RW; ++i) x.w[i] = none ? 0u : r.w[sub][i];
+        *reinterpret_cast<words<RW> *>(at) = x;
+      }
+    }
+  }
+  // arrays a and a + 1 for the lane's four tokens of each 16
+  static __device__ __forceinline__ void take_scales(Scales &g, const char *strip, int a, int lane) {
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      const char *at = strip + ((sub * 4 + a) * 16 + 4 * (lane >> 4)) * TB;
+      const words<SW> s = *reinterpret_cast<const words<SW> *>(at);
+      const words<SW> b = *reinterpret_cast<const words<SW> *>(at + 16 * TB);
+#pragma unroll
+      for (int i = 0; i < SW; ++i) g.s[sub][i] = s.w[i], g.b[sub][i] = b.w[i];
     }
   }
 
@@ -513,7 +564,7 @@ struct Wave {
   }
 
   // scores of the tile's 32 tokens, in powers of two: t[nt][4*sub + i]
-  __device__ __forceinline__ void scores(const Keys &k, float (&t)[NT][8]) const {
+  __device__ __forceinline__ void scores(const Keys &k, const Scales &ks, float (&t)[NT][8]) const {
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
       f32x4v acc[NT][NG];
@@ -535,8 +586,8 @@ struct Wave {
             x = 0.f;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-              x = __builtin_fmaf(scale_at(k.g.s[sub], i, g), acc[nt][g][i], x);
-              x = __builtin_fmaf(scale_at(k.g.b[sub], i, g), qsum[nt][g], x);
+              x = __builtin_fmaf(scale_at(ks.s[sub], i, g), acc[nt][g][i], x);
+              x = __builtin_fmaf(scale_at(ks.b[sub], i, g), qsum[nt][g], x);
             }
           } else {
             x = acc[nt][0][i];
@@ -577,26 +628,26 @@ struct Wave {
   }
 
   // o += weights x values
-  __device__ __forceinline__ void gather(const Values &v, const float (&p)[NT][8]) {
+  __device__ __forceinline__ void gather(const Values &v, const Scales &vs, const float (&p)[NT][8]) {
     u32x4v w[NT][NG], w2[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if constexpr (QUANT) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          uint32_t words[8];
+          uint32_t scale[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) words[j] = v.g.s[j >> 2][((j & 3) * NG + g) >> 1];
+          for (int j = 0; j < 8; ++j) scale[j] = vs.s[j >> 2][((j & 3) * NG + g) >> 1];
           if constexpr (NG == 1)
-            w[nt][g] = scaled_weights<0, 1>(p[nt], words);
+            w[nt][g] = scaled_weights<0, 1>(p[nt], scale);
           else if (g & 1)
-            w[nt][g] = scaled_weights<1, 1>(p[nt], words);
+            w[nt][g] = scaled_weights<1, 1>(p[nt], scale);
           else
-            w[nt][g] = scaled_weights<0, 0>(p[nt], words);
+            w[nt][g] = scaled_weights<0, 0>(p[nt], scale);
           float add = 0.f;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float s = scale_at(v.g.s[j >> 2], j & 3, g), b = scale_at(v.g.b[j >> 2], j & 3, g);
+            const float s = scale_at(vs.s[j >> 2], j & 3, g), b = scale_at(vs.b[j >> 2], j & 3, g);
             add = __builtin_fmaf(p[nt][j], __builtin_fmaf(CENTRE, s, b), add);
             add = __builtin_fmaf(half_at(w[nt][g][j >> 1], j & 1), -CENTRE, add);
           }
@@ -646,7 +697,7 @@ struct Wave {
   // the lane's scales and biases.  Those of tokens past its column become 0;
   // where a lane has two columns, those of tokens past both do, and any that
   // are not finite, whose NaN goes to the columns that see it.
-  __device__ __forceinline__ void edge_values(Values &v, int token, const bool *on, int h) {
+  __device__ __forceinline__ void edge_values(Scales &vs, int token, const bool *on, int h) {
 #pragma unroll
     for (int x = 0; x < 2 * SW; ++x) {
       const int sub = x / SW, w = x % SW;
@@ -658,7 +709,7 @@ struct Wave {
         if constexpr (NT == 1) {
           if (on[sub] && at < vis[0]) keep |= half;
         } else {
-          const float zero = half_at(v.g.s[sub][w], e & 1) * 0.f + half_at(v.g.b[sub][w], e & 1) * 0.f;
+          const float zero = half_at(vs.s[sub][w], e & 1) * 0.f + half_at(vs.b[sub][w], e & 1) * 0.f;
           bool seen = false;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -671,8 +722,8 @@ struct Wave {
       }
       // (opaque, or the words of all tiles are taken apart into halves)
       asm volatile("" : "+v"(keep));
-      v.g.s[sub][w] &= keep;
-      v.g.b[sub][w] &= keep;
+      vs.s[sub][w] &= keep;
+      vs.b[sub][w] &= keep;
     }
   }
 
@@ -694,11 +745,14 @@ struct Wave {
 
   // tiles first, first + NW, ... below end of a sequence: one wave's part
   __device__ __forceinline__ void run(const Params &p, int b, int head, int slice, int len,
-                                      int tile0, int end) {
+                                      int tile0, int end, char *strip) {
     const int lane = lane_here();
     const int least = len - p.L + 1 + (slice * NT * 16) / p.group;  // what every column sees
     Keys k;
     Values v;
+    Raw raw;
+    bool none;
+    const char *from = scales_of(p, lane, none);
     uint32_t row_lo, row_hi;  // lane 2 i + sub: the rows of the round's tile i
     int64_t rows[2];
     bool on[2], on_next[2];
@@ -736,6 +790,7 @@ struct Wave {
       start(qs, p, slice, lane);
       __builtin_amdgcn_sched_barrier(0);
       locate(0, on);
+      if constexpr (QUANT) load_scales(raw, from, rows);
       load_keys(k, p, rows, on, lane);
       load_values(v, p, rows, on, lane);
       clear();
@@ -746,18 +801,25 @@ struct Wave {
         const bool last = tile + 1 == tiles;
         float t[NT][8];
         const bool edge = token + 32 > least || !on[0] || !on[1];
-        scores(k, t);
+        Scales g;
+        if constexpr (QUANT) {
+          share_scales(raw, strip, lane, none);
+          take_scales(g, strip, 0, lane);
+        }
+        scores(k, g, t);
         // the last tile fetches itself again: loads without a branch let the
         // waits count only what they need
         locate(last ? tile : tile + 1, on_next);
         // (into the registers just used: nothing moves across)
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (QUANT) load_scales(raw, from, rows);
         load_keys(k, p, rows, on_next, lane);
         if (edge) edge_scores(t, token, on, lane >> 4);
         weigh(t);
         if constexpr (QUANT) {
-          if (edge) edge_values(v, token, on, lane >> 4);
-          gather(v, t);
+          take_scales(g, strip, 2, lane);
+          if (edge) edge_values(g, token, on, lane >> 4);
+          gather(v, g, t);
         } else {
           const int passes = edge ? p.L : 1;
           for (int i = 0; i < passes; ++i) {
@@ -773,7 +835,7 @@ struct Wave {
               }
               edge_pass(v, t, w, len - p.L + 1 + i, token, on, lane >> 4);
             }
-            gather(v, w);
+            gather(v, g, w);
           }
           if (edge) locate(last ? tile : tile + 1, on_next);
         }
@@ -786,6 +848,7 @@ struct Wave {
       if (c0 >= end) break;
       look_up();
       locate(0, on);
+      if constexpr (QUANT) load_scales(raw, from, rows);
       load_keys(k, p, rows, on, lane);
       load_values(v, p, rows, on, lane);
     }
@@ -892,7 +955,8 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
     const int cols = p.L * p.group - slice * NT * 16, used = cols < NT * 16 ? cols : NT * 16;
     __syncthreads();  // the last round's readers of LDS are done
     if (wave < busy) {
-      st.run(p, b, head, slice, len, tile0 + wave, tile1);
+      st.run(p, b, head, slice, len, tile0 + wave, tile1,
+             reinterpret_cast<char *>(buf + wave * W::SHARE));
       st.give(buf + wave * W::SHARE, ml + wave * NT * 32, used);
     }
     __syncthreads();
