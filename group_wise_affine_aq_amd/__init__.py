@@ -608,7 +608,8 @@ def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_bias
     head_dim] or [B, q_heads, head_dim] (L = 1; tokens may be strided), page_table int32 [B,
     max_pages], lengths int32 [B] (cached tokens, the L new ones included) -> out of q's shape.
     scale: default head_dim ** -0.5.  workspace: a device buffer of
-    aq_paged_attention_workspace bytes; without one each call allocates its own."""
+    aq_paged_attention_workspace bytes, zeroed once before its first use; without one each call
+    makes and clears its own."""
     torch = _torch()
     lib = load_library()
     cache = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
@@ -636,7 +637,7 @@ def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_bias
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if workspace is None:
         need = lib.aq_paged_attention_workspace(B, L, Hq, cache.kv_heads, dim)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
     st = lib.aq_paged_attention(q.data_ptr(), _dtype_code(q), B, L, Hq, step, ctypes.byref(cache),
                                 _array(page_table, torch.int32, None, "page_table"),
                                 page_table.shape[1], _array(lengths, torch.int32, None, "lengths"),

@@ -199,7 +199,10 @@ struct Params {
   const int32_t *table, *lengths;
   void *out;
   float *parts;  // two pieces per workgroup
-  int4 *cuts;    // per workgroup: pieces, sequence, key head and slice of the unit that starts in
+  uint32_t *arrived;  // per workgroup: pieces there of the unit that starts in its last piece;
+                      // zero between calls
+  int inside;    // pieces are joined by the workgroup that finishes a unit's last
+  int4 *cuts;    // (else) per workgroup: pieces, sequence, key head and slice of the unit that starts in
                  // its last piece, 0 pieces where none does
   int64_t max_pages, num_pages;
   uint32_t page_subs, page_magic;  // page_size / 16 and floor(2^32 / that) + 1
@@ -222,9 +225,30 @@ __device__ __forceinline__ int clamped_length(const Params &p, int b) {
   return n < 0 ? 0 : (n > cap ? (int)cap : n);
 }
 
-// one piece in the workspace: the results of 16 NT columns, D floats each, then
-// the columns' m and l
+// One piece in the workspace: the results of 16 NT columns, D floats each, then
+// the columns' m and l.  Where a unit's pieces are joined inside the launch
+// they are read by other workgroups than wrote them, on other XCDs with L2s of
+// their own: stores and loads go past the L2s (sc1, the cache policy of device
+// scope), and a workgroup counts as arrived when its stores are done.
+// (Ordinary stores with a device-wide fence write back and drop whole L2s: 118
+// against 37 us for 16 sequences of up to 4096 tokens, 8 bits, at that step.)
+constexpr int kDeviceScope = 16;
+constexpr int kMaxGrid = 1024;  // counters and records in the workspace
 constexpr int piece_floats(int D, int NT) { return NT * (16 * D + 32); }
+
+__device__ __forceinline__ void put_piece(Span to, int at, f32x4v v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, v), to, at * 4, 0, kDeviceScope);
+}
+__device__ __forceinline__ void put_piece1(Span to, int at, float v) {
+  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), to, at * 4, 0, kDeviceScope);
+}
+__device__ __forceinline__ f32x4v get_piece(Span from, int at) {
+  return __builtin_bit_cast(f32x4v, __builtin_amdgcn_raw_buffer_load_b128(from, at * 4, 0, kDeviceScope));
+}
+__device__ __forceinline__ float get_piece1(Span from, int at) {
+  const uint32_t u = __builtin_amdgcn_raw_buffer_load_b32(from, at * 4, 0, kDeviceScope);
+  return __builtin_bit_cast(float, u);
+}
 
 // ---- the work line ------------------------------------------------------------------
 // All tiles of all units -- a unit is one sequence, key head and slice of query
@@ -297,6 +321,7 @@ struct Line {
   }
   // the workgroup that takes chunk `at`
   __device__ __forceinline__ uint32_t owner(uint32_t at) const {
+    if (share == 1 && longer == 0) return at;
     const uint32_t first = longer * (share + 1);
     return at < first ? at / (share + 1) : longer + (at - first) / share;
   }
@@ -901,11 +926,81 @@ __device__ __forceinline__ void put_result(const Params &p, int b, int head, int
                             : make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
 }
 
+// Running (m, l, acc) of one strand of pieces
+struct Strand {
+  float m = kNegInf, l = 0.f;
+  f32x4v acc = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ void add(float pm, float pl, f32x4v v) {
+    const float top = __builtin_fmaxf(m, pm), base = top == kNegInf ? 0.f : top;
+    const float f = exp2_fast(m - base), g = exp2_fast(pm - base);
+    m = top;
+    l = l * f + pl * g;
+    acc = acc * f + v * g;
+  }
+  __device__ __forceinline__ f32x4v result() const { return acc * (l == 0.f ? 0.f : 1.f / l); }
+};
+
+// Joins, inside the launch, the n pieces of a unit from workgroup w0's second
+// on, and writes the rows.  Every four values are one thread's, or, where the
+// workgroup has more threads, several threads' with every so many-th piece
+// each, joined through LDS: the order of all sums is the pieces' own.
+template <int D, int NT>
+__device__ __forceinline__ void join_inside(const Params &p, int b, int head, int slice, int w0,
+                                            int n, int used, float *buf) {
+  constexpr int PF = piece_floats(D, NT), ML = NT * 16 * D, Q = D / 4, U = 8;
+  const int items = used * Q;
+  int strands = 64 * NW / items;
+  strands = strands < 1 ? 1 : (strands > n ? n : strands);
+  const int step = strands == 1 ? 64 * NW : items;  // items at a time
+  const float *first = p.parts + (2 * (int64_t)w0 + 1) * PF;
+  for (int i0 = 0; i0 < items; i0 += step) {
+    const int strand = strands == 1 ? 0 : (int)threadIdx.x / items;
+    const int item = i0 + (strands == 1 ? (int)threadIdx.x : (int)threadIdx.x - strand * items);
+    const bool on = strand < strands && item < items;
+    const int c = on ? item / Q : 0, at = on ? (item % Q) * 4 : 0;
+    Strand st;
+    // pieces in rounds of U strands' worth; every thread's piece of a round is
+    // `strand` past a uniform one, piece k > 0 (2 k - 1) pieces past the first
+    for (int k0 = 0; k0 < n; k0 += U * strands) {
+      f32x4v v[U];
+      float pm[U], pl[U];
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        const int k = k0 + x * strands + strand, kk = k < n ? k : n - 1;
+        const int off = kk ? (2 * kk - 1) * PF : 0;
+        const Span from = span(first, 0, 0x7FFFFFFF);
+        v[x] = get_piece(from, off + c * D + at);
+        pm[x] = get_piece1(from, off + ML + c);
+        pl[x] = get_piece1(from, off + ML + NT * 16 + c);
+      }
+#pragma unroll
+      for (int x = 0; x < U; ++x)
+        if (k0 + x * strands + strand < n) st.add(pm[x], pl[x], v[x]);
+    }
+    if (strands > 1) {
+      if (on) {
+        float *to = buf + (strand * items + item) * 6;
+        to[0] = st.m, to[1] = st.l;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) to[2 + x] = st.acc[x];
+      }
+      __syncthreads();
+      if (on && strand == 0)
+        for (int k = 1; k < strands; ++k) {
+          const float *from = buf + (k * items + item) * 6;
+          st.add(from[0], from[1], f32x4v{from[2], from[3], from[4], from[5]});
+        }
+    }
+    if (on && strand == 0) put_result<D>(p, b, head, slice * NT * 16 + c, at, st.result());
+  }
+}
+
 template <int BITS, bool BF, int D, int G, int NT, int WGS>
 __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
   using W = Wave<BITS, BF, D, G, NT>;
   __shared__ f32x4v buf4[NW * W::SHARE / 4];
   __shared__ float ml[NW * NT * 32];
+  __shared__ uint32_t last;
   float *buf = reinterpret_cast<float *>(buf4);
   const int wave = uniform(threadIdx.x >> 6);
 
@@ -920,7 +1015,7 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
               make_uint4(0, 0, 0, 0);
   }
   if (blockIdx.x >= line.grid) {
-    if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0 && !p.inside) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
   int4 cut = make_int4(0, 0, 0, 0);
@@ -945,7 +1040,7 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
     const uint32_t c0 = in_seq - unit * chunks;
     const int head = uniform(unit / p.slices), slice = unit - head * p.slices;
     const uint32_t c1 = end - pos < chunks - c0 ? c0 + (end - pos) : chunks;
-    const uint32_t unit_end = pos - c0 + chunks;
+    const uint32_t unit_begin = pos - c0;
     pos += c1 - c0;
 
     const int tiles = (len + kTile - 1) / kTile, tile0 = (int)(c0 * (line.chunk / kTile));
@@ -965,9 +1060,7 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
     // where this is only a piece of the unit, to the workspace (a workgroup's
     // second place is for the piece that starts its unit)
     const bool whole = c0 == 0 && c1 == chunks;
-    if (c0 == 0 && !whole)
-      cut = make_int4((int)(line.owner(unit_end - 1) - blockIdx.x) + 1, b, head, slice);
-    float *to = p.parts + (2 * (int64_t)blockIdx.x + (c0 == 0)) * W::PF;
+    const Span to = span(p.parts, (2 * (int64_t)blockIdx.x + (c0 == 0)) * (W::PF * 4), W::PF * 4);
     constexpr int Q = D / 4;
     for (int item = threadIdx.x; item < used * Q; item += 64 * NW) {
       const int c = item / Q, at = (item % Q) * 4;
@@ -984,23 +1077,42 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
       if (whole) {
         put_result<D>(p, b, head, slice * NT * 16 + c, at, y * (l == 0.f ? 0.f : 1.f / l));
       } else {
-        *reinterpret_cast<f32x4v *>(to + c * D + at) = y;
+        put_piece(to, c * D + at, y);
         if (at == 0) {
-          to[NT * 16 * D + c] = top;
-          to[NT * 16 * D + NT * 16 + c] = l;
+          put_piece1(to, NT * 16 * D + c, top);
+          put_piece1(to, NT * 16 * D + NT * 16 + c, l);
         }
       }
     }
+    if (whole) continue;
+
+    if (!p.inside) {
+      if (c0 == 0)
+        cut = make_int4((int)(line.owner(unit_begin + chunks - 1) - blockIdx.x) + 1, b, head, slice);
+      continue;
+    }
+    // count this piece in, and join them if it is the unit's last to arrive
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    const int w0 = uniform(line.owner(unit_begin));
+    const int n = uniform(line.owner(unit_begin + chunks - 1)) - w0 + 1;
+    if (threadIdx.x == 0) {
+      last = __hip_atomic_fetch_add(p.arrived + w0, 1u, __ATOMIC_RELAXED,
+                                    __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(n - 1);
+      if (last) __hip_atomic_store(p.arrived + w0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (uniform((int)last)) {
+      asm volatile("" ::: "memory");
+      join_inside<D, NT>(p, b, head, slice, w0, n, used, buf);
+    }
   }
-  if (threadIdx.x == 0) p.cuts[blockIdx.x] = cut;
+  if (threadIdx.x == 0 && !p.inside) p.cuts[blockIdx.x] = cut;
 }
 
-// Joins the pieces of units that were cut: a workgroup takes 64 times four
-// values of one unit, its eight waves every eighth piece each, and adds the
-// waves' parts in order, so the result does not depend on timing.  (A second
-// launch: joined by whichever workgroup arrives last, one workgroup reads all
-// of a unit's pieces and the others of the chip are idle: 190 us for three
-// sequences of up to 20001 tokens and one key head of 256, against 22 us.)
+// Joins the pieces of units that were cut, in a launch of its own: a workgroup
+// takes 64 times four values of one unit, its eight waves every eighth piece
+// each, and adds the waves' parts in order.
 constexpr int kJoinWaves = 8;
 template <int D>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, int nt) {
@@ -1017,8 +1129,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, in
   const int c = on ? item / Q : 0, d = on ? (item % Q) * 4 : 0;
   const int PF = piece_floats(D, nt);
   const float *first = p.parts + (2 * (int64_t)w0 + 1) * PF;
-  float m = kNegInf, l = 0.f;
-  f32x4v acc = {0.f, 0.f, 0.f, 0.f};
+  Strand st;
   constexpr int U = 4;
   for (int i = wave; i < n; i += U * kJoinWaves) {
     f32x4v v[U];
@@ -1031,36 +1142,20 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, in
       pm[x] = src[nt * 16 * D + c];
       pl[x] = src[nt * 16 * D + nt * 16 + c];
     }
-    float top = m;
-#pragma unroll
-    for (int x = 0; x < U; ++x) top = __builtin_fmaxf(top, pm[x]);
-    const float base = top == kNegInf ? 0.f : top, keep = exp2_fast(m - base);
-    m = top;
-    l *= keep;
-    acc *= keep;
 #pragma unroll
     for (int x = 0; x < U; ++x)
-      if (i + x * kJoinWaves < n) {
-        const float f = exp2_fast(pm[x] - base);
-        l += pl[x] * f;
-        acc += v[x] * f;
-      }
+      if (i + x * kJoinWaves < n) st.add(pm[x], pl[x], v[x]);
   }
-  part[wave][0][lane] = m;
-  part[wave][1][lane] = l;
+  part[wave][0][lane] = st.m;
+  part[wave][1][lane] = st.l;
 #pragma unroll
-  for (int x = 0; x < 4; ++x) part[wave][2 + x][lane] = acc[x];
+  for (int x = 0; x < 4; ++x) part[wave][2 + x][lane] = st.acc[x];
   __syncthreads();
   if (wave != 0 || !on) return;
-  for (int w = 1; w < kJoinWaves && w < n; ++w) {
-    const float pm = part[w][0][lane], top = __builtin_fmaxf(m, pm), base = top == kNegInf ? 0.f : top;
-    const float f = exp2_fast(m - base), g = exp2_fast(pm - base);
-    m = top;
-    l = l * f + part[w][1][lane] * g;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) acc[x] = acc[x] * f + part[w][2 + x][lane] * g;
-  }
-  put_result<D>(p, b, head, slice * nt * 16 + c, d, acc * (l == 0.f ? 0.f : 1.f / l));
+  for (int w = 1; w < kJoinWaves && w < n; ++w)
+    st.add(part[w][0][lane], part[w][1][lane],
+           f32x4v{part[w][2][lane], part[w][3][lane], part[w][4][lane], part[w][5][lane]});
+  put_result<D>(p, b, head, slice * nt * 16 + c, d, st.result());
 }
 
 // query rows per slice: two tiles of 16 where there are more than 16
@@ -1069,7 +1164,7 @@ int tiles_for(int64_t cols) { return cols > 16 ? 2 : 1; }
 // workgroups per CU the kernel is built for: what its registers allow (a
 // lane's scales and biases grow with the groups of a row)
 constexpr int wgs_per_cu(int D, int NG, int NT) {
-  return D * NT <= 128 && NG <= 2 ? 3 : (D * NT <= 128 || (D * NT <= 256 && NG <= 2) ? 2 : 1);
+  return D * NT <= 64 ? 3 : (D * NT <= 128 || (D * NT <= 256 && NG <= 2) ? 2 : 1);
 }
 
 }  // namespace
@@ -1077,7 +1172,7 @@ constexpr int wgs_per_cu(int D, int NG, int NT) {
 int64_t attn_workspace_bytes(int64_t, int L, int q_heads, int kv_heads, int head_dim) {
   const int nt = tiles_for((int64_t)L * (q_heads / kv_heads));
   const int wgs = device_cus() * wgs_per_cu(head_dim, 1, nt);
-  return (int64_t)wgs * (16 + 2 * piece_floats(head_dim, nt) * 4);
+  return kMaxGrid * 20 + (int64_t)(wgs < kMaxGrid ? wgs : kMaxGrid) * 2 * piece_floats(head_dim, nt) * 4;
 }
 
 hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream_t s) {
@@ -1117,9 +1212,19 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
   const int64_t most = (cap + chunk - 1) / chunk * per_tile;
   int64_t grid = (int64_t)device_cus() *
                  wgs_per_cu(c.head_dim, c.bits == 16 ? 1 : c.head_dim / c.group_size, nt);
+  if (grid > kMaxGrid) grid = kMaxGrid;
   if (most < grid) grid = most;
   p.cuts = reinterpret_cast<int4 *>(a.workspace);
-  p.parts = reinterpret_cast<float *>(p.cuts + grid);
+  p.arrived = reinterpret_cast<uint32_t *>(p.cuts + kMaxGrid);
+  p.parts = reinterpret_cast<float *>(p.arrived + kMaxGrid);
+  // A unit's pieces, each `items` times four values, are joined by one
+  // workgroup inside the launch, unless one sequence could have so many (a
+  // piece is four tiles at least) that a launch over the whole chip is faster:
+  // that costs 2 to 3 us wherever anything is cut, one workgroup about 1 us per
+  // thousand of pieces times items (85 pieces of 1024 items: 83 us).
+  const int items = (int)(cols < 16 * nt ? cols : 16 * nt) * c.head_dim / 4;
+  const int64_t pieces = (cap + NW * kTile - 1) / (NW * kTile);
+  p.inside = (pieces < grid ? pieces : grid) * items <= 16384;
   hipError_t err = hipErrorInvalidValue;
 #define AQ_KT(B, F, D, G, T)                                                           \
   hipLaunchKernelGGL((attn_kernel<B, F, D, G, T, wgs_per_cu(D, D / G, T)>),            \
@@ -1153,8 +1258,7 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
 #undef AQ_K
 #undef AQ_KT
   // (a chunk that holds the whole table: no unit is cut)
-  if (err != hipSuccess || cap <= chunk) return err;
-  const int items = (int)(cols < 16 * nt ? cols : 16 * nt) * c.head_dim / 4;
+  if (err != hipSuccess || cap <= chunk || p.inside) return err;
   const dim3 join((unsigned)grid, (unsigned)((items + 63) / 64));
 #define AQ_J(D) \
   hipLaunchKernelGGL((attn_join_kernel<D>), join, dim3(64 * kJoinWaves), 0, s, p, nt)

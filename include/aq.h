@@ -450,10 +450,11 @@ aq_status aq_kv_read(const int64_t *slots, int64_t T, const aq_kv_cache *cache, 
  * softmax statistics are held in binary32.  NULL bias arrays: every bias +0.
  *
  * workspace: device memory of aq_paged_attention_workspace bytes, 16-byte
- * aligned, whatever it holds; calls that may run at the same time need
- * workspaces of their own.  The launches (the attention, and joining what it
- * cut) do not depend on the lengths, so a captured graph follows them as they
- * grow; results are the same bits every time.
+ * aligned, zeroed once before its first use; every call leaves it fit for the
+ * next one, of any shape it is large enough for.  Calls that may run at the
+ * same time need workspaces of their own.  The launches do not depend on the
+ * lengths, so a captured graph follows them as they grow; results are the
+ * same bits every time.
  * AQ_ERR_INVALID_ARG when workspace_bytes is too small, B < 1, L outside
  * 1..8; AQ_ERR_UNSUPPORTED for max_pages * page_size > 2^31 - 256 or B * L *
  * q_heads >= 2^24. */
