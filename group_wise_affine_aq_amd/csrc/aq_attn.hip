@@ -28,9 +28,10 @@
 //    one byte permute (8 bits) or a mask (4 bits; the odd nibbles are masked
 //    in place, 16 times too large, and the query or the result is scaled by
 //    1/16) per pair.  2^24 goes into factors that are there anyway.
-//  * Queries are scaled by a power of two per row so that their largest value
-//    lies in [256, 512) and rounded to fp16: exact for fp16 and bf16 down to
-//    2^-18 of the row's largest value.
+//  * bf16 queries become fp16, scaled by a power of two per row so that the
+//    largest lies in [256, 512): exact down to 2^-22 of it, 2^-18 for the odd
+//    codes of 4 bits.  fp16 queries are taken as they are; below 2^-10 the odd
+//    ones' sixteenths round, by 2^-25 at most.
 //  * Weights p s are rounded to fp16 (2^-11 relative) for the second product.
 //    They are kept 2^6 (8 bits) or 2^2 (4 bits) times too large, as far as
 //    the largest possible scale of a group allows (131008 / 255, / 15), which
@@ -522,22 +523,42 @@ struct Wave {
       }
     }
   }
-  __device__ __forceinline__ void start(const Queries &qs, const Params &p, int slice, int lane) {
+  // (columns past the last hold the first row's queries: never written out)
+  __device__ __forceinline__ void start(const Queries &qs, const Params &p) {
+    const float log2s = p.scale * 1.44269504088896341f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const bool on = (slice * NT + nt) * 16 + (lane & 15) < p.L * p.group;
-      uint4 raw[KS];
+      if constexpr (!QUANT) {
+        C[nt] = log2s;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) raw[s] = on ? qs.raw[nt][s] : make_uint4(0, 0, 0, 0);
-      if constexpr (QUANT) {
+        for (int s = 0; s < KS; ++s)
+          q[nt][s] = u32x4v{qs.raw[nt][s].x, qs.raw[nt][s].y, qs.raw[nt][s].z, qs.raw[nt][s].w};
+        continue;
+      }
+      if (p.x_dtype == X_F16) {
+        C[nt] = log2s * 0x1p24f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const uint32_t u[4] = {qs.raw[nt][s].x, qs.raw[nt][s].y, qs.raw[nt][s].z, qs.raw[nt][s].w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            if constexpr (BITS == 8) {
+              q[nt][s][w] = u[w];
+            } else {  // queries w and w + 4, the odd ones / 16
+              const uint32_t x = __builtin_amdgcn_perm(u[2 + (w >> 1)], u[w >> 1], w & 1 ? 0x07060302u : 0x05040100u);
+              const half2v h = __builtin_bit_cast(half2v, x) * half2v{(_Float16)0.0625f, (_Float16)0.0625f};
+              q[nt][s][w] = w & 1 ? __builtin_bit_cast(uint32_t, h) : x;
+            }
+          }
+        }
+      } else {
         float x[KS][8], top = 0.f;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          const uint32_t u[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
+          const uint32_t u[4] = {qs.raw[nt][s].x, qs.raw[nt][s].y, qs.raw[nt][s].z, qs.raw[nt][s].w};
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const uint16_t bits = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
-            x[s][e] = p.x_dtype == X_F16 ? f16_to_f32(bits) : bf16_to_f32(bits);
+            x[s][e] = __builtin_bit_cast(float, e & 1 ? u[e >> 1] & 0xFFFF0000u : u[e >> 1] << 16);
             top = __builtin_fmaxf(top, __builtin_fabsf(x[s][e]));
           }
         }
@@ -545,16 +566,7 @@ struct Wave {
         int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
         e = e < -100 ? -100 : (e > 100 ? 100 : e);
         const float down = __builtin_ldexpf(1.f, 8 - e);
-        C[nt] = __builtin_ldexpf(p.scale * 1.44269504088896341f, 24 + e - 8);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float sum = 0.f;
-#pragma unroll
-          for (int k = 0; k < NKS; ++k)
-#pragma unroll
-            for (int i8 = 0; i8 < 8; ++i8) sum += x[g * NKS + k][i8];
-          qsum[nt][g] = quarters_sum(sum) * down * 0x1p-24f;
-        }
+        C[nt] = __builtin_ldexpf(log2s, 24 + e - 8);
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -566,10 +578,16 @@ struct Wave {
               q[nt][s][w] = pack_f16(x[s][w] * f, x[s][w + 4] * f);
             }
           }
-      } else {
-        C[nt] = p.scale * 1.44269504088896341f;
+      }
+      // a group's sum, as the score of keys whose codes are all 1
+      const u32x4v ones = BITS == 8 ? u32x4v{0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u}
+                                    : u32x4v{0x00010001u, 0x00100010u, 0x00010001u, 0x00100010u};
 #pragma unroll
-        for (int s = 0; s < KS; ++s) q[nt][s] = u32x4v{raw[s].x, raw[s].y, raw[s].z, raw[s].w};
+      for (int g = 0; g < NG; ++g) {
+        f32x4v sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < NKS; ++k) sum = mfma<BF>(ones, q[nt][g * NKS + k], sum);
+        qsum[nt][g] = sum[0];
       }
     }
   }
@@ -812,7 +830,7 @@ struct Wave {
       Queries qs;
       load_queries(qs, p, b, head, slice, len, lane);
       look_up();
-      start(qs, p, slice, lane);
+      start(qs, p);
       __builtin_amdgcn_sched_barrier(0);
       locate(0, on);
       if constexpr (QUANT) load_scales(raw, from, rows);
@@ -947,7 +965,7 @@ struct Strand {
 template <int D, int NT>
 __device__ __forceinline__ void join_inside(const Params &p, int b, int head, int slice, int w0,
                                             int n, int used, float *buf) {
-  constexpr int PF = piece_floats(D, NT), ML = NT * 16 * D, Q = D / 4, U = 8;
+  constexpr int PF = piece_floats(D, NT), ML = NT * 16 * D, Q = D / 4, U = 16;
   const int items = used * Q;
   int strands = 64 * NW / items;
   strands = strands < 1 ? 1 : (strands > n ? n : strands);
