@@ -302,6 +302,7 @@ struct Line {
     uint32_t total = count(p, lane);
     if (chunk == kTile && rows * p.B <= most) {
       const uint32_t even = (total + NW * most - 1) / (NW * most) * NW;
+#pragma unroll 1
       for (uint32_t more = 0; more <= 20 && chunk == kTile; more += NW) {
         chunk = (even + more) * kTile;
         const uint32_t n = count(p, lane);
@@ -850,9 +851,10 @@ struct Wave {
           take_scales(g, strip, 0, lane);
         }
         scores(k, g, t);
-        // the last tile fetches itself again: loads without a branch let the
-        // waits count only what they need
+        // after the last tile fetches of no bytes: loads without a branch let
+        // the waits count only what they need
         locate(last ? tile : tile + 1, on_next);
+        if (last) on_next[0] = on_next[1] = false;
         // (into the registers just used: nothing moves across)
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (QUANT) load_scales(raw, from, rows);
@@ -880,7 +882,7 @@ struct Wave {
             }
             gather(v, g, w);
           }
-          if (edge) locate(last ? tile : tile + 1, on_next);
+          if (edge && !last) locate(tile + 1, on_next);
         }
         __builtin_amdgcn_sched_barrier(0);
         load_values(v, p, rows, on_next, lane);
@@ -897,36 +899,33 @@ struct Wave {
     }
   }
 
-  // The wave's (m, l, o), the biases' part folded in, to its place in LDS: rows
-  // of D results per column, then the columns' m and l.
+  // (m, l, o) of the wave's tile nt of columns, the biases' part folded in, to
+  // its place in LDS: rows of D results per column, then the columns' m and l.
   static constexpr int PF = piece_floats(D, NT);
   static constexpr int ROW = D + 4;  // columns on different banks
-  static constexpr int SHARE = NT * 16 * ROW;
-  __device__ __forceinline__ void give(float *o_at, float *ml_at, int used) {
+  static constexpr int SHARE = 16 * ROW;
+  __device__ __forceinline__ void give(int nt, float *o_at, float *ml_at, int used) {
     const int lane = lane_here(), c = lane & 15, h = lane >> 4;
+    const float sum = quarters_sum(l[nt]);
+    if (lane < 16) {
+      ml_at[lane] = m[nt];
+      ml_at[16 + lane] = sum;
+    }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float sum = quarters_sum(l[nt]);
-      if (lane < 16) {
-        ml_at[nt * 32 + lane] = m[nt];
-        ml_at[nt * 32 + 16 + lane] = sum;
-      }
+    for (int g = 0; g < NG; ++g) {
+      const float add = QUANT ? quarters_sum(bacc[nt][g]) : 0.f;
+      if (nt * 16 + c < used) {
+        float *at = o_at + c * ROW + g * G + 4 * h * VN;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const float add = QUANT ? quarters_sum(bacc[nt][g]) : 0.f;
-        if (nt * 16 + c < used) {
-          float *at = o_at + (nt * 16 + c) * ROW + g * G + 4 * h * VN;
+        for (int e = 0; e < 4 * VN; e += 4) {  // value e: row e / VN of product e % VN
+          f32x4v y;
 #pragma unroll
-          for (int e = 0; e < 4 * VN; e += 4) {  // value e: row e / VN of product e % VN
-            f32x4v y;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int n = (e + x) % VN;
-              const float r = o[nt][g][n][(e + x) / VN];
-              y[x] = QUANT ? __builtin_fmaf(r, BITS == 4 && (n & 1) ? 0x1p20f : 0x1p24f, add) : r;
-            }
-            *reinterpret_cast<f32x4v *>(at + e) = y;
+          for (int x = 0; x < 4; ++x) {
+            const int n = (e + x) % VN;
+            const float r = o[nt][g][n][(e + x) / VN];
+            y[x] = QUANT ? __builtin_fmaf(r, BITS == 4 && (n & 1) ? 0x1p20f : 0x1p24f, add) : r;
           }
+          *reinterpret_cast<f32x4v *>(at + e) = y;
         }
       }
     }
@@ -1017,7 +1016,7 @@ template <int BITS, bool BF, int D, int G, int NT, int WGS>
 __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
   using W = Wave<BITS, BF, D, G, NT>;
   __shared__ f32x4v buf4[NW * W::SHARE / 4];
-  __shared__ float ml[NW * NT * 32];
+  __shared__ float ml[NW * 32];
   __shared__ uint32_t last;
   float *buf = reinterpret_cast<float *>(buf4);
   const int wave = uniform(threadIdx.x >> 6);
@@ -1066,41 +1065,45 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
     tile1 = tile1 < tiles ? tile1 : tiles;
     const int busy = tile1 - tile0 < NW ? tile1 - tile0 : NW;
     const int cols = p.L * p.group - slice * NT * 16, used = cols < NT * 16 ? cols : NT * 16;
-    __syncthreads();  // the last round's readers of LDS are done
-    if (wave < busy) {
-      st.run(p, b, head, slice, len, tile0 + wave, tile1,
-             reinterpret_cast<char *>(buf + wave * W::SHARE));
-      st.give(buf + wave * W::SHARE, ml + wave * NT * 32, used);
-    }
-    __syncthreads();
-
-    // every four values of the rows, over the waves' shares: to the output, or,
-    // where this is only a piece of the unit, to the workspace (a workgroup's
-    // second place is for the piece that starts its unit)
     const bool whole = c0 == 0 && c1 == chunks;
     const Span to = span(p.parts, (2 * (int64_t)blockIdx.x + (c0 == 0)) * (W::PF * 4), W::PF * 4);
+    __syncthreads();  // the last round's readers of LDS are done
+    if (wave < busy)
+      st.run(p, b, head, slice, len, tile0 + wave, tile1,
+             reinterpret_cast<char *>(buf + wave * W::SHARE));
+    // a tile of columns after the other: the waves' shares, then every four
+    // values of the rows over them, to the output or, where this is only a
+    // piece of the unit, to the workspace (a workgroup's second place is for
+    // the piece that starts its unit)
     constexpr int Q = D / 4;
-    for (int item = threadIdx.x; item < used * Q; item += 64 * NW) {
-      const int c = item / Q, at = (item % Q) * 4;
-      const float *mc = ml + (c >> 4) * 32 + (c & 15);
-      float top = kNegInf, l = 0.f;
-      for (int w = 0; w < busy; ++w) top = __builtin_fmaxf(top, mc[w * NT * 32]);
-      const float base = top == kNegInf ? 0.f : top;
-      f32x4v y = {0.f, 0.f, 0.f, 0.f};
-      for (int w = 0; w < busy; ++w) {
-        const float f = exp2_fast(mc[w * NT * 32] - base);
-        l += mc[w * NT * 32 + 16] * f;
-        y += *reinterpret_cast<const f32x4v *>(buf + w * W::SHARE + c * W::ROW + at) * f;
-      }
-      if (whole) {
-        put_result<D>(p, b, head, slice * NT * 16 + c, at, y * (l == 0.f ? 0.f : 1.f / l));
-      } else {
-        put_piece(to, c * D + at, y);
-        if (at == 0) {
-          put_piece1(to, NT * 16 * D + c, top);
-          put_piece1(to, NT * 16 * D + NT * 16 + c, l);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (wave < busy) st.give(nt, buf + wave * W::SHARE, ml + wave * 32, used);
+      __syncthreads();
+      const int live = used - nt * 16 < 16 ? used - nt * 16 : 16;
+      for (int item = threadIdx.x; item < live * Q; item += 64 * NW) {
+        const int c = item / Q, at = (item % Q) * 4;
+        float top = kNegInf, l = 0.f;
+        for (int w = 0; w < busy; ++w) top = __builtin_fmaxf(top, ml[w * 32 + c]);
+        const float base = top == kNegInf ? 0.f : top;
+        f32x4v y = {0.f, 0.f, 0.f, 0.f};
+        for (int w = 0; w < busy; ++w) {
+          const float f = exp2_fast(ml[w * 32 + c] - base);
+          l += ml[w * 32 + 16 + c] * f;
+          y += *reinterpret_cast<const f32x4v *>(buf + w * W::SHARE + c * W::ROW + at) * f;
+        }
+        const int r = nt * 16 + c;
+        if (whole) {
+          put_result<D>(p, b, head, slice * NT * 16 + r, at, y * (l == 0.f ? 0.f : 1.f / l));
+        } else {
+          put_piece(to, r * D + at, y);
+          if (at == 0) {
+            put_piece1(to, NT * 16 * D + r, top);
+            put_piece1(to, NT * 16 * D + NT * 16 + r, l);
+          }
         }
       }
+      if (nt + 1 < NT) __syncthreads();
     }
     if (whole) continue;
 
@@ -1176,8 +1179,17 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, in
   put_result<D>(p, b, head, slice * nt * 16 + c, d, st.result());
 }
 
-// query rows per slice: two tiles of 16 where there are more than 16
-int tiles_for(int64_t cols) { return cols > 16 ? 2 : 1; }
+// Query rows per key head go to a wave in one or two tiles of 16; more rows are
+// further slices, each of which reads the cache again.  (40 rows, 8 bits, 8
+// sequences of up to 8192 tokens: 45 us in two slices of two tiles; 47 in one
+// of three, which takes the registers of three waves; 59 as four waves with a
+// tile of rows each on the same tokens, too few tokens are then under way.)
+constexpr int kMostTiles = 2;
+void tiles_for(int64_t cols, int &nt, int &slices) {
+  const int64_t tiles = (cols + 15) / 16;
+  slices = (int)((tiles + kMostTiles - 1) / kMostTiles);
+  nt = tiles > 1 ? kMostTiles : 1;
+}
 
 // workgroups per CU the kernel is built for: what its registers allow (a
 // lane's scales and biases grow with the groups of a row)
@@ -1188,7 +1200,8 @@ constexpr int wgs_per_cu(int D, int NG, int NT) {
 }  // namespace
 
 int64_t attn_workspace_bytes(int64_t, int L, int q_heads, int kv_heads, int head_dim) {
-  const int nt = tiles_for((int64_t)L * (q_heads / kv_heads));
+  int nt, slices;
+  tiles_for((int64_t)L * (q_heads / kv_heads), nt, slices);
   const int wgs = device_cus() * wgs_per_cu(head_dim, 1, nt);
   return kMaxGrid * 20 + (int64_t)(wgs < kMaxGrid ? wgs : kMaxGrid) * 2 * piece_floats(head_dim, nt) * 4;
 }
@@ -1217,8 +1230,8 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
   p.x_dtype = a.x_dtype;
   p.scale = a.scale;
   const int64_t cols = (int64_t)a.L * p.group;
-  const int nt = tiles_for(cols);
-  p.slices = (int)((cols + 16 * nt - 1) / (16 * nt));
+  int nt;
+  tiles_for(cols, nt, p.slices);
   // The line's chunks are counted in 32 bits: where the table could hold more
   // tiles than that they are longer.  A table that holds no more than one tile
   // per wave leaves units whole.
