@@ -130,14 +130,16 @@ def aq_qweight_bytes(N: int, K: int, group_size: int, bits: int) -> int:
 
 # ---- marshalling -----------------------------------------------------------------------
 _torch_module = None
+_raw_stream = None  # the current stream's handle of a device, the short way if torch has it
 _dtype_codes = {}
 
 
 def _torch():
-    global _torch_module
+    global _torch_module, _raw_stream
     if _torch_module is None:
         import torch
         _dtype_codes.update({torch.float32: AQ_F32, torch.float16: AQ_F16, torch.bfloat16: AQ_BF16})
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _torch_module = torch
     return _torch_module
 
@@ -493,61 +495,55 @@ def _queue(stream, t):
     """The stream's handle; without one, that of the current stream of t's device."""
     if stream is not None:
         return stream.cuda_stream
-    torch = _torch()
-    try:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
-    except AttributeError:  # (a torch without the short way)
-        return torch.cuda.current_stream(t.device).cuda_stream
+    raw = _raw_stream
+    return raw(t.get_device()) if raw else _torch().cuda.current_stream(t.device).cuda_stream
 
 
 def _rows(t, name):
     """Device address of [tokens, heads, head_dim] rows, heads and head_dim contiguous, and the
     tokens' distance in elements."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
     stride, inner, last = t.stride()
     n, h, d = t.shape
-    if last != 1 or (h > 1 and inner != d):
-        raise ValueError(f"{name}: heads and head_dim must be contiguous")
+    if last != 1 or (h > 1 and inner != d) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor, heads and head_dim contiguous")
     return t.data_ptr(), (stride if n > 1 else h * d)
 
 
-def _array(t, dtype, shape, name):
-    if t is None:
-        return None
+def _array(t, dtype, count, name):
+    """Device address of a contiguous array of `count` elements (None: any number)."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, {dtype} expected")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} expected")
     if not (t.is_cuda and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous device tensor")
+    if count is not None and t.numel() != count:
+        raise ValueError(f"{name}: {t.numel()} elements, {count} expected")
     return t.data_ptr()
 
 
 def _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits):
     torch = _torch()
-    shape = k_codes.shape
-    pages, heads, page, words = shape
+    pages, heads, page, words = k_codes.shape
+    rows = pages * heads * page
     if bits == 16:
         code = _dtype_code(k_codes)
         if code == AQ_F32:
             raise TypeError("a 16-bit cache holds float16 or bfloat16")
-        kind = k_codes.dtype
-        return _KVCache(_array(k_codes, kind, shape, "k_codes"), None, None,
-                        _array(v_codes, kind, shape, "v_codes"), None, None,
+        kind, count = k_codes.dtype, rows * words
+        return _KVCache(_array(k_codes, kind, count, "k_codes"), None, None,
+                        _array(v_codes, kind, count, "v_codes"), None, None,
                         pages, page, heads, words, 0, 16, code)
     if bits != 4 and bits != 8:
         raise AQError(-2 if 2 <= bits <= 8 else -1, "aq_kv_cache")
     dim = words * 32 // bits
-    if group_size < 1 or dim % group_size:
+    if group_size < 1 or dim % group_size or k_scales is None or v_scales is None:
         raise AQError(-1, "aq_kv_cache")
-    groups, half, word = (pages, heads, page, dim // group_size), torch.float16, torch.int32
-    return _KVCache(_array(k_codes, word, shape, "k_codes"),
+    word, half, count, groups = torch.int32, torch.float16, rows * words, rows * (dim // group_size)
+    return _KVCache(_array(k_codes, word, count, "k_codes"),
                     _array(k_scales, half, groups, "k_scales"),
-                    _array(k_biases, half, groups, "k_biases"),
-                    _array(v_codes, word, shape, "v_codes"),
+                    None if k_biases is None else _array(k_biases, half, groups, "k_biases"),
+                    _array(v_codes, word, count, "v_codes"),
                     _array(v_scales, half, groups, "v_scales"),
-                    _array(v_biases, half, groups, "v_biases"),
+                    None if v_biases is None else _array(v_biases, half, groups, "v_biases"),
                     pages, page, heads, dim, group_size, bits, 0)
 
 
@@ -564,31 +560,37 @@ def aq_kv_append(k, v, slots, k_codes, k_scales, k_biases, v_codes, v_scales, v_
     kp, ks = _rows(k, "k")
     vp, vs = _rows(v, "v")
     st = lib.aq_kv_append(kp, vp, _dtype_code(k), T, ks, vs,
-                          _array(slots, _torch().int64, None, "slots"), ctypes.byref(cache),
+                          _array(slots, _torch_module.int64, None, "slots"), ctypes.byref(cache),
                           _queue(stream, slots))
-    _check(st, "aq_kv_append")
+    if st != AQ_OK:
+        raise AQError(st, "aq_kv_append")
 
 
 def aq_kv_read(slots, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size: int,
                bits: int, out_dtype=None, k=None, v=None, stream=None):
     """Rows of the cache at slots int64 [T] -> (k, v) [T, kv_heads, head_dim] in out_dtype
     (default fp16); a slot outside the cache gives zeros."""
-    torch = _torch()
     lib = load_library()
     cache = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
-    T = slots.numel()
-    shape = (T, cache.kv_heads, cache.head_dim)
+    torch = _torch_module
+    T, H, D = slots.numel(), cache.kv_heads, cache.head_dim
     if k is None and v is None:
-        k, v = torch.empty((2,) + shape, dtype=out_dtype or torch.float16, device=slots.device)
-    elif k is None:
-        k = torch.empty(shape, dtype=v.dtype, device=slots.device)
-    elif v is None:
-        v = torch.empty(shape, dtype=k.dtype, device=slots.device)
-    kind = k.dtype
-    st = lib.aq_kv_read(_array(slots, torch.int64, None, "slots"), T, ctypes.byref(cache),
-                        _array(k, kind, shape, "k"), _array(v, kind, shape, "v"), _dtype_code(k),
-                        _queue(stream, slots))
-    _check(st, "aq_kv_read")
+        k, v = torch.empty((2, T, H, D), dtype=out_dtype or torch.float16, device=slots.device)
+        kind, kp = k.dtype, k.data_ptr()
+        vp = kp + T * H * D * k.element_size()
+    else:
+        if k is None:
+            k = torch.empty((T, H, D), dtype=v.dtype, device=slots.device)
+        elif v is None:
+            v = torch.empty((T, H, D), dtype=k.dtype, device=slots.device)
+        if k.shape != (T, H, D) or v.shape != (T, H, D):
+            raise ValueError(f"aq_kv_read: k and v must be {(T, H, D)}")
+        kind = k.dtype
+        kp, vp = _array(k, kind, None, "k"), _array(v, kind, None, "v")
+    st = lib.aq_kv_read(_array(slots, torch.int64, None, "slots"), T, ctypes.byref(cache), kp, vp,
+                        _dtype_code(k), _queue(stream, slots))
+    if st != AQ_OK:
+        raise AQError(st, "aq_kv_read")
     return k, v
 
 
@@ -610,40 +612,47 @@ def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_bias
     scale: default head_dim ** -0.5.  workspace: a device buffer of
     aq_paged_attention_workspace bytes, zeroed once before its first use; without one each call
     makes and clears its own."""
-    torch = _torch()
     lib = load_library()
     cache = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
-    dim = cache.head_dim
-    if q.dim() == 3:
-        B, Hq, D = q.shape
+    torch = _torch_module
+    shape, strides = q.shape, q.stride()
+    if len(shape) == 3:
+        B, Hq, D = shape
         L = 1
-        step, inner, last = q.stride()
+        step, inner, last = strides
     else:
-        B, L, Hq, D = q.shape
-        outer, step, inner, last = q.stride()
+        B, L, Hq, D = shape
+        outer, step, inner, last = strides
         if L == 1:
             step = outer
         elif B > 1 and outer != L * step:
             raise ValueError("q: all tokens must lie at one distance")
-    if D != dim:
-        raise ValueError(f"q: head_dim {D}, the cache has {dim}")
+    if D != cache.head_dim:
+        raise ValueError(f"q: head_dim {D}, the cache has {cache.head_dim}")
     if last != 1 or (Hq > 1 and inner != D) or not q.is_cuda:
         raise ValueError("q: a device tensor, heads and head_dim contiguous")
     if B * L == 1:
         step = Hq * D
-    if page_table.dim() != 2 or page_table.shape[0] != B or lengths.numel() != B:
-        raise ValueError(f"page_table must be [{B}, max_pages] and lengths [{B}]")
+    rows, max_pages = page_table.shape
+    if rows != B:
+        raise ValueError(f"page_table must be [{B}, max_pages]")
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        op = out.data_ptr()
+    else:
+        if out.shape != shape:
+            raise ValueError("out must have q's shape and dtype")
+        op = _array(out, q.dtype, None, "out")
     if workspace is None:
-        need = lib.aq_paged_attention_workspace(B, L, Hq, cache.kv_heads, dim)
+        need = lib.aq_paged_attention_workspace(B, L, Hq, cache.kv_heads, D)
         workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
+    int32 = torch.int32
     st = lib.aq_paged_attention(q.data_ptr(), _dtype_code(q), B, L, Hq, step, ctypes.byref(cache),
-                                _array(page_table, torch.int32, None, "page_table"),
-                                page_table.shape[1], _array(lengths, torch.int32, None, "lengths"),
-                                dim ** -0.5 if scale is None else scale,
-                                _array(out, q.dtype, q.shape, "out"),
+                                _array(page_table, int32, None, "page_table"), max_pages,
+                                _array(lengths, int32, B, "lengths"),
+                                D ** -0.5 if scale is None else scale, op,
                                 _array(workspace, workspace.dtype, None, "workspace"),
-                                workspace.numel() * workspace.element_size(), _queue(stream, q))
-    _check(st, "aq_paged_attention")
+                                workspace.nbytes, _queue(stream, q))
+    if st != AQ_OK:
+        raise AQError(st, "aq_paged_attention")
     return out
