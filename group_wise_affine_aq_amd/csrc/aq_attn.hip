@@ -203,8 +203,7 @@ struct Params {
   uint32_t *arrived;  // per workgroup: pieces there of the unit that starts in its last piece;
                       // zero between calls
   int inside;    // pieces are joined by the workgroup that finishes a unit's last
-  int4 *cuts;    // (else) per workgroup: pieces, sequence, key head and slice of the unit that starts in
-                 // its last piece, 0 pieces where none does
+  uint2 *cuts;   // (else) per unit: its pieces, 0 if it was not cut, and the first one's workgroup
   int64_t max_pages, num_pages;
   uint32_t page_subs, page_magic;  // page_size / 16 and floor(2^32 / that) + 1
   int kv_heads, group, L, B, slices, x_dtype;
@@ -234,7 +233,7 @@ __device__ __forceinline__ int clamped_length(const Params &p, int b) {
 // (Ordinary stores with a device-wide fence write back and drop whole L2s: 118
 // against 37 us for 16 sequences of up to 4096 tokens, 8 bits, at that step.)
 constexpr int kDeviceScope = 16;
-constexpr int kMaxGrid = 1024;  // counters and records in the workspace
+constexpr int kMaxGrid = 1024;  // of counters, and of records of units, in the workspace
 constexpr int piece_floats(int D, int NT) { return NT * (16 * D + 32); }
 
 __device__ __forceinline__ void put_piece(Span to, int at, f32x4v v) {
@@ -1030,12 +1029,13 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
         for (int64_t i = threadIdx.x; i < row_halves / 8; i += 64 * NW)
           reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + b * row_halves)[i] =
               make_uint4(0, 0, 0, 0);
+    if (!p.inside)
+      for (int64_t b = blockIdx.x; b < p.B; b += gridDim.x)
+        if (clamped_length(p, (int)b) == 0)
+          for (uint32_t u = threadIdx.x; u < line.rows; u += 64 * NW)
+            p.cuts[b * line.rows + u] = make_uint2(0, 0);
   }
-  if (blockIdx.x >= line.grid) {
-    if (threadIdx.x == 0 && !p.inside) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  int4 cut = make_int4(0, 0, 0, 0);
+  if (blockIdx.x >= line.grid) return;
   uint32_t pos = line.begin(blockIdx.x);
   const uint32_t end = line.begin(blockIdx.x + 1);
   const int at = __builtin_ctzll(__ballot(pos < line.upto * line.rows));
@@ -1105,13 +1105,15 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
       }
       if (nt + 1 < NT) __syncthreads();
     }
-    if (whole) continue;
-
     if (!p.inside) {
-      if (c0 == 0)
-        cut = make_int4((int)(line.owner(unit_begin + chunks - 1) - blockIdx.x) + 1, b, head, slice);
+      if (c0 == 0 && threadIdx.x == 0) {
+        const uint32_t n = whole ? 0 : line.owner(unit_begin + chunks - 1) - blockIdx.x + 1;
+        p.cuts[b * line.rows + unit] = make_uint2(n, blockIdx.x);
+      }
       continue;
     }
+    if (whole) continue;
+
     // count this piece in, and join them if it is the unit's last to arrive
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
@@ -1128,7 +1130,6 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
       join_inside<D, NT>(p, b, head, slice, w0, n, used, buf);
     }
   }
-  if (threadIdx.x == 0 && !p.inside) p.cuts[blockIdx.x] = cut;
 }
 
 // Joins the pieces of units that were cut, in a launch of its own: a workgroup
@@ -1138,10 +1139,11 @@ constexpr int kJoinWaves = 8;
 template <int D>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, int nt) {
   __shared__ float part[kJoinWaves][6][64];
-  const int w0 = blockIdx.x;
-  const int4 cut = p.cuts[w0];
-  const int n = uniform(cut.x), b = uniform(cut.y), head = uniform(cut.z), slice = uniform(cut.w);
+  const uint2 cut = p.cuts[blockIdx.x];
+  const int n = uniform(cut.x), w0 = uniform(cut.y);
   if (n == 0) return;
+  const int rows = p.kv_heads * p.slices, b = blockIdx.x / rows, unit = blockIdx.x - b * rows;
+  const int head = unit / p.slices, slice = unit - head * p.slices;
   const int lane = lane_here(), wave = uniform(threadIdx.x >> 6);
   constexpr int Q = D / 4;
   const int cols = p.L * p.group - slice * nt * 16, used = cols < nt * 16 ? cols : nt * 16;
@@ -1151,7 +1153,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, in
   const int PF = piece_floats(D, nt);
   const float *first = p.parts + (2 * (int64_t)w0 + 1) * PF;
   Strand st;
-  constexpr int U = 4;
+  constexpr int U = 8;
   for (int i = wave; i < n; i += U * kJoinWaves) {
     f32x4v v[U];
     float pm[U], pl[U];
@@ -1203,7 +1205,7 @@ int64_t attn_workspace_bytes(int64_t, int L, int q_heads, int kv_heads, int head
   int nt, slices;
   tiles_for((int64_t)L * (q_heads / kv_heads), nt, slices);
   const int wgs = device_cus() * wgs_per_cu(head_dim, 1, nt);
-  return kMaxGrid * 20 + (int64_t)(wgs < kMaxGrid ? wgs : kMaxGrid) * 2 * piece_floats(head_dim, nt) * 4;
+  return kMaxGrid * 12 + (int64_t)(wgs < kMaxGrid ? wgs : kMaxGrid) * 2 * piece_floats(head_dim, nt) * 4;
 }
 
 hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream_t s) {
@@ -1245,7 +1247,7 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
                  wgs_per_cu(c.head_dim, c.bits == 16 ? 1 : c.head_dim / c.group_size, nt);
   if (grid > kMaxGrid) grid = kMaxGrid;
   if (most < grid) grid = most;
-  p.cuts = reinterpret_cast<int4 *>(a.workspace);
+  p.cuts = reinterpret_cast<uint2 *>(a.workspace);
   p.arrived = reinterpret_cast<uint32_t *>(p.cuts + kMaxGrid);
   p.parts = reinterpret_cast<float *>(p.arrived + kMaxGrid);
   // A unit's pieces, each `items` times four values, are joined by one
@@ -1255,7 +1257,7 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
   // thousand of pieces times items (85 pieces of 1024 items: 83 us).
   const int items = (int)(cols < 16 * nt ? cols : 16 * nt) * c.head_dim / 4;
   const int64_t pieces = (cap + NW * kTile - 1) / (NW * kTile);
-  p.inside = (pieces < grid ? pieces : grid) * items <= 16384;
+  p.inside = per_tile > kMaxGrid || (pieces < grid ? pieces : grid) * items <= 16384;
   hipError_t err = hipErrorInvalidValue;
 #define AQ_KT(B, F, D, G, T)                                                           \
   hipLaunchKernelGGL((attn_kernel<B, F, D, G, T, wgs_per_cu(D, D / G, T)>),            \
@@ -1290,7 +1292,7 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
 #undef AQ_KT
   // (a chunk that holds the whole table: no unit is cut)
   if (err != hipSuccess || cap <= chunk || p.inside) return err;
-  const dim3 join((unsigned)grid, (unsigned)((items + 63) / 64));
+  const dim3 join((unsigned)per_tile, (unsigned)((items + 63) / 64));
 #define AQ_J(D) \
   hipLaunchKernelGGL((attn_join_kernel<D>), join, dim3(64 * kJoinWaves), 0, s, p, nt)
   if (c.head_dim == 64) AQ_J(64);
