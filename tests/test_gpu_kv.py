@@ -490,3 +490,104 @@ def test_binding_refusals(aq):
     half = torch.zeros((2, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
     with pytest.raises(aq.AQError):  # a 16-bit cache of another type
         aq.aq_paged_attention(q, half, None, None, half, None, None, table, n, 0, 16)
+
+
+# Long tables with many rows a key head: their pieces are joined by a launch of
+# its own.  The last: more units than the workspace has counters.
+LONG = [
+    ([4097, 0, 900, 1], 16, 1, 256, 64, 8, 16, 1, "f16"),
+    ([2500, 2400], 16, 1, 256, 0, 16, 32, 1, "bf16"),
+    ([5200, 33], 4, 2, 128, 128, 4, 64, 8, "bf16"),
+    ([3100], 40, 1, 128, 32, 8, 16, 1, "f16"),       # two slices, the second of 8 rows
+    ([8200, 0], 32, 1, 64, 32, 4, 48, 1, "f16"),
+    ([5000] + [7, 0, 40] * 200, 16, 2, 128, 64, 8, 16, 1, "f16"),
+]
+
+
+@pytest.mark.parametrize("lengths,per,heads,dim,G,bits,page,L,dtype", LONG)
+def test_attention_of_long_tables(aq, lengths, per, heads, dim, G, bits, page, L, dtype):
+    test_attention(aq, lengths, per, heads, dim, G, bits, page, L, dtype)
+
+
+def test_one_workspace_joined_both_ways(aq):
+    """Calls whose pieces are joined inside the launch and by a second one, in
+    turn, in one workspace; equal calls give equal bits."""
+    import torch
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    calls = []
+    for lengths, per, heads, dim, G, bits, page, L, dtype in (LONG[0], CASES[14], LONG[2], CASES[1]):
+        cache, table = _build(lengths, heads, dim, G, bits, page, dtype, seed=31)
+        qb, _ = kv_ref.to_bits(np.random.default_rng(32).standard_normal(
+            (len(lengths), L, per * heads, dim)), dtype)
+        args = (_dev16(qb, dtype), *cache.device(), torch.from_numpy(table).cuda(),
+                torch.tensor(lengths, dtype=torch.int32, device="cuda"), G, bits)
+        calls.append((args, aq.aq_paged_attention(*args)))
+    for _ in range(5):
+        for args, first in calls:
+            assert torch.equal(first, aq.aq_paged_attention(*args, workspace=ws))
+
+
+def test_attention_with_a_table_for_two_billion_tokens(aq):
+    """A table whose tiles would pass 32 bits, of pages of 2^22 tokens; only the
+    first is in the cache."""
+    import torch
+    B, page, ids, dim, G, bits = 40, 1 << 22, 511, 64, 64, 4
+    rng = np.random.default_rng(33)
+    n = 5000
+    small = kv_ref.Cache(1, 1, n, dim, G, bits)
+    big = []
+    for name in "kv":
+        _, x = kv_ref.to_bits(rng.standard_normal((n, dim)), "f16")
+        for part, got in zip(small.parts[name], oracle.quantize(x.astype(np.float32), G, bits)):
+            part[0, 0] = got
+            t = torch.from_numpy(part.view({2: np.int16, 4: np.int32}[part.itemsize])).cuda()
+            t = t if part.itemsize == 4 else t.view(torch.float16)
+            big.append(torch.empty((1, 1, page) + t.shape[3:], dtype=t.dtype, device="cuda"))
+            big[-1][:, :, :n] = t
+    lengths = [n, 0, 31, 32, 33, 4000] + rng.integers(0, 300, B - 6).tolist()
+    table = np.full((B, ids), 1, np.int32)
+    table[:, 0] = 0
+    qb, q = kv_ref.to_bits(rng.standard_normal((B, 1, 2, dim)), "f16")
+    out = aq.aq_paged_attention(_dev16(qb, "f16"), *big, torch.from_numpy(table).cuda(),
+                                torch.tensor(lengths, dtype=torch.int32, device="cuda"), G, bits)
+    ref, bound = kv_ref.attention(q, small, table[:, :1], lengths, dim ** -0.5)
+    _close(out, ref, bound, "f16")
+
+
+def test_cache_of_more_rows_than_31_bits(aq):
+    """Row numbers past 2^31, keys and values in the same 69 GB."""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 77 GB of device memory")
+    H, D, G, bits, page = 8, 64, 64, 4, 64
+    pages = (1 << 31) // (H * page) + 3
+    shape = (pages, H, page)
+    part = [torch.empty(shape + (D * bits // 32,), dtype=torch.int32, device="cuda")]
+    part += [torch.empty(shape + (1,), dtype=torch.float16, device="cuda") for _ in range(2)]
+    n = 150
+    ids = np.array([pages - 1, 3, pages - 3], np.int64)
+    small = kv_ref.Cache(3, H, page, D, G, bits)
+    rng = np.random.default_rng(34)
+    xb, x = kv_ref.to_bits(rng.standard_normal((n, H, D)), "f16")
+    for t in range(n):
+        small.put("k", t, xb[t], x[t])
+        small.put("v", t, xb[t], x[t])
+    slots = torch.from_numpy(ids[np.arange(n) // page] * page + np.arange(n) % page).cuda()
+    aq.aq_kv_append(_dev16(xb, "f16"), _dev16(xb, "f16"), slots, *part, *part, G, bits)
+    for i, got in enumerate(part):  # where torch's own indexing has them
+        got = got[torch.from_numpy(ids).cuda()]
+        want = small.parts["k"][i]
+        keep = (np.arange(3)[:, None] * page + np.arange(page)) < n
+        assert np.array_equal(_cache_bits(got).transpose(0, 2, 1, 3)[keep],
+                              want.transpose(0, 2, 1, 3)[keep])
+    k, v = aq.aq_kv_read(slots, *part, *part, G, bits, out_dtype=torch.float32)
+    assert torch.equal(k, v)
+    for h in range(H):
+        ref = np.concatenate([small.row("k", p, h, page)[0] for p in range(3)])[:n]
+        assert np.array_equal(out_to_f64(k)[:, h], ref.astype(np.float32).astype(np.float64))
+    qb, q = kv_ref.to_bits(rng.standard_normal((1, 1, 32, D)), "f16")
+    out = aq.aq_paged_attention(_dev16(qb, "f16"), *part, *part,
+                                torch.tensor([ids.tolist()], dtype=torch.int32, device="cuda"),
+                                torch.tensor([n], dtype=torch.int32, device="cuda"), G, bits)
+    ref, bound = kv_ref.attention(q, small, np.array([[0, 1, 2]], np.int32), [n], D ** -0.5)
+    _close(out, ref, bound, "f16")
