@@ -14,6 +14,7 @@ scales and biases fp16 [N, K/group_size].  Consumers accept biases=None
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -499,6 +500,15 @@ def _queue(stream, t):
     return raw(t.get_device()) if raw else _torch().cuda.current_stream(t.device).cuda_stream
 
 
+_same_stream = contextlib.nullcontext()
+
+
+def _its(stream):
+    """What a call makes for itself is made on the stream that it runs on: cleared there, and not
+    another's again before it is done with it."""
+    return _same_stream if stream is None else _torch_module.cuda.stream(stream)
+
+
 def _rows(t, name):
     """Device address of [tokens, heads, head_dim] rows, heads and head_dim contiguous, and the
     tokens' distance in elements."""
@@ -575,18 +585,20 @@ def aq_kv_read(slots, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, 
     torch = _torch_module
     T, H, D = slots.numel(), cache.kv_heads, cache.head_dim
     if k is None and v is None:
-        k, v = torch.empty((2, T, H, D), dtype=out_dtype or torch.float16, device=slots.device)
-        kind, kp = k.dtype, k.data_ptr()
-        vp = kp + T * H * D * k.element_size()
+        with _its(stream):
+            k = torch.empty((T, H, D), dtype=out_dtype or torch.float16, device=slots.device)
+            v = torch.empty_like(k)
+        kp, vp = k.data_ptr(), v.data_ptr()
     else:
         if k is None:
-            k = torch.empty((T, H, D), dtype=v.dtype, device=slots.device)
+            with _its(stream):
+                k = torch.empty((T, H, D), dtype=v.dtype, device=slots.device)
         elif v is None:
-            v = torch.empty((T, H, D), dtype=k.dtype, device=slots.device)
+            with _its(stream):
+                v = torch.empty((T, H, D), dtype=k.dtype, device=slots.device)
         if k.shape != (T, H, D) or v.shape != (T, H, D):
             raise ValueError(f"aq_kv_read: k and v must be {(T, H, D)}")
-        kind = k.dtype
-        kp, vp = _array(k, kind, None, "k"), _array(v, kind, None, "v")
+        kp, vp = _array(k, k.dtype, None, "k"), _array(v, k.dtype, None, "v")
     st = lib.aq_kv_read(_array(slots, torch.int64, None, "slots"), T, ctypes.byref(cache), kp, vp,
                         _dtype_code(k), _queue(stream, slots))
     if st != AQ_OK:
@@ -637,7 +649,8 @@ def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_bias
     if rows != B:
         raise ValueError(f"page_table must be [{B}, max_pages]")
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        with _its(stream):
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         op = out.data_ptr()
     else:
         if out.shape != shape:
@@ -645,7 +658,8 @@ def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_bias
         op = _array(out, q.dtype, None, "out")
     if workspace is None:
         need = lib.aq_paged_attention_workspace(B, L, Hq, cache.kv_heads, D)
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
+        with _its(stream):
+            workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
     int32 = torch.int32
     st = lib.aq_paged_attention(q.data_ptr(), _dtype_code(q), B, L, Hq, step, ctypes.byref(cache),
                                 _array(page_table, int32, None, "page_table"), max_pages,

@@ -373,6 +373,33 @@ def test_on_another_stream(aq):
     assert torch.equal(a, b) and torch.equal(a, c)
 
 
+def test_what_a_call_makes_is_made_on_its_stream(aq):
+    """A call on a given stream while the current one is busy: its own workspace
+    is cleared where it is used."""
+    import torch
+    lengths = [5000, 1, 2600]  # cut: the workspace's counters are used
+    cache, table = _build(lengths, 1, 128, 64, 4, 16, "f16", seed=41)
+    qb, _ = kv_ref.to_bits(np.random.default_rng(42).standard_normal((3, 1, 4, 128)), "f16")
+    q = _dev16(qb, "f16")
+    args = (*cache.device(), torch.from_numpy(table).cuda(),
+            torch.tensor(lengths, dtype=torch.int32, device="cuda"), 64, 4)
+    want = aq.aq_paged_attention(q, *args)
+    rows = torch.arange(90, device="cuda")
+    want_rows = aq.aq_kv_read(rows, *args[:6], 64, 4)
+    s = torch.cuda.Stream()
+    need = aq.aq_paged_attention_workspace(3, 1, 4, 1, 128)
+    torch.empty(need, dtype=torch.uint8, device="cuda").fill_(0x7F)  # freed at once
+    torch.cuda.synchronize()
+    busy = torch.randn((4096, 4096), device="cuda")
+    for _ in range(20):
+        busy = busy @ busy
+    got = aq.aq_paged_attention(q, *args, stream=s)
+    rows = aq.aq_kv_read(rows, *args[:6], 64, 4, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    assert torch.equal(rows[0], want_rows[0]) and torch.equal(rows[1], want_rows[1])
+
+
 def test_graph_follows_growing_lengths(aq):
     """A captured step of append and attention, replayed while the sequences
     grow, gives what the eager calls give."""
