@@ -830,12 +830,12 @@ struct Wave {
       Queries qs;
       load_queries(qs, p, b, head, slice, len, lane);
       look_up();
-      start(qs, p);
-      __builtin_amdgcn_sched_barrier(0);
       locate(0, on);
       if constexpr (QUANT) load_scales(raw, from, rows);
       load_keys(k, p, rows, on, lane);
       load_values(v, p, rows, on, lane);
+      __builtin_amdgcn_sched_barrier(0);
+      start(qs, p);
       clear();
     }
     for (;;) {
@@ -958,57 +958,87 @@ struct Strand {
 
 // Joins, inside the launch, the n pieces of a unit from workgroup w0's second
 // on, and writes the rows.  Every four values are one thread's, or, where the
-// workgroup has more threads, several threads' with every so many-th piece
-// each, joined through LDS: the order of all sums is the pieces' own.
-template <int D, int NT>
-__device__ __forceinline__ void join_inside(const Params &p, int b, int head, int slice, int w0,
-                                            int n, int used, float *buf) {
-  constexpr int PF = piece_floats(D, NT), ML = NT * 16 * D, Q = D / 4, U = 16;
+// workgroup has more threads, several threads' (strands) with every so many-th
+// piece each, joined through LDS: the order of all sums is the pieces' own.  A
+// thread has the loads of U pieces for V times four values under way at once.
+template <int D, int NT, int U, int V>
+__device__ __forceinline__ void join_pieces(const Params &p, int b, int head, int slice, int w0,
+                                            int n, int used, int strands, float *buf) {
+  constexpr int PF = piece_floats(D, NT), ML = NT * 16 * D, Q = D / 4;
   const int items = used * Q;
-  int strands = 64 * NW / items;
-  strands = strands < 1 ? 1 : (strands > n ? n : strands);
+  const int strand = strands == 1 ? 0 : (int)threadIdx.x / items;
   const int step = strands == 1 ? 64 * NW : items;  // items at a time
-  const float *first = p.parts + (2 * (int64_t)w0 + 1) * PF;
-  for (int i0 = 0; i0 < items; i0 += step) {
-    const int strand = strands == 1 ? 0 : (int)threadIdx.x / items;
-    const int item = i0 + (strands == 1 ? (int)threadIdx.x : (int)threadIdx.x - strand * items);
-    const bool on = strand < strands && item < items;
-    const int c = on ? item / Q : 0, at = on ? (item % Q) * 4 : 0;
-    Strand st;
-    // pieces in rounds of U strands' worth; every thread's piece of a round is
-    // `strand` past a uniform one, piece k > 0 (2 k - 1) pieces past the first
+  const Span from = span(p.parts, (2 * (int64_t)w0 + 1) * (PF * 4), 0x7FFFFFFF);
+  for (int i0 = 0; i0 < items; i0 += V * step) {
+    Strand st[V];
+    int c[V], at[V];
+    bool on[V];
+#pragma unroll
+    for (int y = 0; y < V; ++y) {
+      const int item = i0 + y * step + (int)threadIdx.x - strand * items;
+      on[y] = strand < strands && item < items;
+      c[y] = on[y] ? item / Q : 0;
+      at[y] = on[y] ? (item % Q) * 4 : 0;
+    }
+    // every thread's piece of a round is `strand` past a uniform one, piece
+    // k > 0 (2 k - 1) pieces past the first
     for (int k0 = 0; k0 < n; k0 += U * strands) {
-      f32x4v v[U];
-      float pm[U], pl[U];
+      f32x4v v[U][V];
+      float pm[U][V], pl[U][V];
 #pragma unroll
       for (int x = 0; x < U; ++x) {
         const int k = k0 + x * strands + strand, kk = k < n ? k : n - 1;
         const int off = kk ? (2 * kk - 1) * PF : 0;
-        const Span from = span(first, 0, 0x7FFFFFFF);
-        v[x] = get_piece(from, off + c * D + at);
-        pm[x] = get_piece1(from, off + ML + c);
-        pl[x] = get_piece1(from, off + ML + NT * 16 + c);
+#pragma unroll
+        for (int y = 0; y < V; ++y) {
+          v[x][y] = get_piece(from, off + c[y] * D + at[y]);
+          pm[x][y] = get_piece1(from, off + ML + c[y]);
+          pl[x][y] = get_piece1(from, off + ML + NT * 16 + c[y]);
+        }
       }
 #pragma unroll
       for (int x = 0; x < U; ++x)
-        if (k0 + x * strands + strand < n) st.add(pm[x], pl[x], v[x]);
-    }
-    if (strands > 1) {
-      if (on) {
-        float *to = buf + (strand * items + item) * 6;
-        to[0] = st.m, to[1] = st.l;
+        if (k0 + x * strands + strand < n)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) to[2 + x] = st.acc[x];
+          for (int y = 0; y < V; ++y) st[y].add(pm[x][y], pl[x][y], v[x][y]);
+    }
+    if (strands > 1) {  // (one item a thread then)
+      if (on[0]) {
+        float *to = buf + (int)threadIdx.x * 6;
+        to[0] = st[0].m, to[1] = st[0].l;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) to[2 + x] = st[0].acc[x];
       }
       __syncthreads();
-      if (on && strand == 0)
+      if (on[0] && strand == 0)
         for (int k = 1; k < strands; ++k) {
-          const float *from = buf + (k * items + item) * 6;
-          st.add(from[0], from[1], f32x4v{from[2], from[3], from[4], from[5]});
+          const float *other = buf + (k * items + (int)threadIdx.x) * 6;
+          st[0].add(other[0], other[1], f32x4v{other[2], other[3], other[4], other[5]});
         }
     }
-    if (on && strand == 0) put_result<D>(p, b, head, slice * NT * 16 + c, at, st.result());
+#pragma unroll
+    for (int y = 0; y < V; ++y)
+      if (on[y] && strand == 0)
+        put_result<D>(p, b, head, slice * NT * 16 + c[y], at[y], st[y].result());
   }
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void join_inside(const Params &p, int b, int head, int slice, int w0,
+                                            int n, int used, float *buf) {
+  const int items = used * (D / 4);
+  int strands = 64 * NW / items;
+  strands = strands < 1 ? 1 : (strands > n ? n : strands);
+  // 16 loads a thread in as few rounds as the pieces and items make, fewer
+  // loads where they are few
+  if (items > 128 * NW && n <= 4)
+    join_pieces<D, NT, 4, 4>(p, b, head, slice, w0, n, used, strands, buf);
+  else if (items > 64 * NW)
+    join_pieces<D, NT, 8, 2>(p, b, head, slice, w0, n, used, strands, buf);
+  else if (n <= 4 * strands)
+    join_pieces<D, NT, 4, 1>(p, b, head, slice, w0, n, used, strands, buf);
+  else
+    join_pieces<D, NT, 16, 1>(p, b, head, slice, w0, n, used, strands, buf);
 }
 
 template <int BITS, bool BF, int D, int G, int NT, int WGS>
