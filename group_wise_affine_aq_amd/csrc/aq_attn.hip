@@ -1113,15 +1113,25 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
       const int live = used - nt * 16 < 16 ? used - nt * 16 : 16;
       for (int item = threadIdx.x; item < live * Q; item += 64 * NW) {
         const int c = item / Q, at = (item % Q) * 4;
-        float top = kNegInf, l = 0.f;
-        for (int w = 0; w < busy; ++w) top = __builtin_fmaxf(top, ml[w * 32 + c]);
-        const float base = top == kNegInf ? 0.f : top;
-        f32x4v y = {0.f, 0.f, 0.f, 0.f};
-        for (int w = 0; w < busy; ++w) {
-          const float f = exp2_fast(ml[w * 32 + c] - base);
-          l += ml[w * 32 + 16 + c] * f;
-          y += *reinterpret_cast<const f32x4v *>(buf + w * W::SHARE + c * W::ROW + at) * f;
+        // (all reads at once, the idle waves' too, which count for nothing)
+        float wm[NW], wl[NW], top = kNegInf, l = 0.f;
+        f32x4v wo[NW], y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          wm[w] = ml[w * 32 + c];
+          wl[w] = ml[w * 32 + 16 + c];
+          wo[w] = *reinterpret_cast<const f32x4v *>(buf + w * W::SHARE + c * W::ROW + at);
         }
+#pragma unroll
+        for (int w = 0; w < NW; ++w) top = __builtin_fmaxf(top, w < busy ? wm[w] : kNegInf);
+        const float base = top == kNegInf ? 0.f : top;
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+          if (w < busy) {
+            const float f = exp2_fast(wm[w] - base);
+            l += wl[w] * f;
+            y += wo[w] * f;
+          }
         const int r = nt * 16 + c;
         if (whole) {
           put_result<D>(p, b, head, slice * NT * 16 + r, at, y * (l == 0.f ? 0.f : 1.f / l));
