@@ -1215,7 +1215,9 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, in
   for (int x = 0; x < 4; ++x) part[wave][2 + x][lane] = st.acc[x];
   __syncthreads();
   if (wave != 0 || !on) return;
-  for (int w = 1; w < kJoinWaves && w < n; ++w)
+  // (waves without a piece left a maximum of -inf and zeros)
+#pragma unroll
+  for (int w = 1; w < kJoinWaves; ++w)
     st.add(part[w][0][lane], part[w][1][lane],
            f32x4v{part[w][2][lane], part[w][3][lane], part[w][4][lane], part[w][5][lane]});
   put_result<D>(p, b, head, slice * nt * 16 + c, d, st.result());
