@@ -44,19 +44,26 @@
 //    8 bits more than the output rounds off, so it is split in two bf16 parts,
 //    two products per tile.
 //
-// Work division.  All tokens of all (sequence, key head, slice of 16 NT query
-// rows) form one line of 128-token blocks that the workgroups cut evenly, so
-// a batch of ragged lengths and one long sequence load the chip alike and the
-// launch does not depend on the lengths.  In a block each of the four waves
-// takes 32 tokens; the waves' (m, l, o) are joined through LDS.  A piece that
-// does not cover its unit goes to the workspace; the workgroup that finishes
-// last among a unit's pieces joins them, in the pieces' order whoever comes
-// last, so results do not depend on timing.
+// Work division.  The tokens of all units -- a unit is one sequence, one key
+// head and one slice of at most 32 of its query rows -- form one line of
+// 32-token tiles that the workgroups cut evenly, so a batch of ragged lengths
+// and one long sequence load the chip alike and the launch does not depend on
+// the lengths, which stay on the device.  The four waves of a workgroup take
+// every fourth tile of its part; their (m, l, o) are joined through LDS.  A
+// part that does not cover its unit is a piece in the workspace; the pieces
+// are joined by the workgroup that finishes last among them or, where they may
+// be many, by a second launch, in the pieces' order either way, so results do
+// not depend on timing.
 //
 // Bound: HBM, the codes, scales and biases read once.  At 8 bits a tile of 32
-// tokens x 128 values is 8.7 KB and costs about 240 vector and 16 matrix
-// instructions; four waves a CU would take 36 bytes a clock at that rate where
-// HBM gives a CU about 9.
+// tokens x 128 values (groups of 64, one tile of query rows) is 8.7 KB and
+// costs a wave about 250 vector and 16 matrix instructions (4 bits: 4.6 KB,
+// 290); eight waves a CU could take 35 bytes a clock at that rate where HBM
+// gives a CU about 9.  64 sequences of up to 16384 tokens (1.01 GB) take 187
+// us, 5.4 TB/s; a large copy reaches 5.2, a large read 6.3.  Below about 100 MB
+// what surrounds the stream shows: lengths, page ids and first codes are three
+// loads that wait for each other (5 us to the first score), and joining pieces
+// is three more (5 us): 16 sequences of up to 4096 tokens (71 MB) 20.5 us.
 #include "aq_device.hpp"
 #include "aq_internal.hpp"
 
@@ -200,10 +207,11 @@ struct Params {
   const int32_t *table, *lengths;
   void *out;
   float *parts;  // two pieces per workgroup
-  uint32_t *arrived;  // per workgroup: pieces there of the unit that starts in its last piece;
-                      // zero between calls
-  int inside;    // pieces are joined by the workgroup that finishes a unit's last
-  uint2 *cuts;   // (else) per unit: its pieces, 0 if it was not cut, and the first one's workgroup
+  int inside;    // pieces are joined by the workgroup that finishes a unit's last, else by
+                 // attn_join_kernel
+  uint32_t *arrived;  // inside: per workgroup, pieces there of the unit that starts in its last
+                      // piece; zero between calls
+  uint2 *cuts;   // else: per unit, its pieces, 0 if it was not cut, and the first one's workgroup
   int64_t max_pages, num_pages;
   uint32_t page_subs, page_magic;  // page_size / 16 and floor(2^32 / that) + 1
   int kv_heads, group, L, B, slices, x_dtype;
@@ -251,12 +259,14 @@ __device__ __forceinline__ float get_piece1(Span from, int at) {
 }
 
 // ---- the work line ------------------------------------------------------------------
-// All tiles of all units -- a unit is one sequence, key head and slice of query
-// rows -- in one line, sequences first, cut evenly.  A workgroup whose part
-// begins in one unit and ends in another waits twice for first loads (about
-// 7 us), so the line is counted in chunks that do not cross units, as many as
-// there are workgroups at most, as long as they need not be more than 20 tiles
-// (the work of 7 us) larger than an even cut in single tiles.
+// All tiles of all units in one line, sequences first, cut evenly.  A workgroup
+// whose part begins in one unit and ends in another waits twice for first loads
+// (about 5 us), so the line is counted in chunks that do not cross units, as
+// many as there are workgroups at most, as long as they need not be more than
+// 20 tiles larger than an even cut in single tiles.  (Cut evenly against in
+// chunks: 26.9 and 21.9 us for 16 sequences of up to 4096 tokens, 8 bits; 50.1
+// and 44.9 with 40 rows a key head; 59.1 and 53.6 at 16 bits; 195 and 196 for
+// 64 sequences, whose parts are long.  4, 10 and 20 tiles measured the same.)
 
 // inclusive sum over the lanes, a row of 16 and then the rows
 __device__ __forceinline__ uint32_t lanes_prefix(uint32_t v) {
@@ -1224,10 +1234,12 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, in
 }
 
 // Query rows per key head go to a wave in one or two tiles of 16; more rows are
-// further slices, each of which reads the cache again.  (40 rows, 8 bits, 8
-// sequences of up to 8192 tokens: 45 us in two slices of two tiles; 47 in one
-// of three, which takes the registers of three waves; 59 as four waves with a
-// tile of rows each on the same tokens, too few tokens are then under way.)
+// further slices, each of which reads the cache again, mostly from a cache of
+// the chip.  (40 rows, 8 bits, 8 sequences of up to 8192 tokens, at one step: 45
+// us in two slices of two tiles; 47 in one of three, which takes the registers
+// of the second workgroup on a CU; 59 as four waves with a tile of rows each on
+// the same tokens, too few tokens are then under way.  The second slice's one
+// tile of 8 rows computed as one, not two: no faster, 46.4 against 45.3.)
 constexpr int kMostTiles = 2;
 void tiles_for(int64_t cols, int &nt, int &slices) {
   const int64_t tiles = (cols + 15) / 16;
@@ -1235,8 +1247,10 @@ void tiles_for(int64_t cols, int &nt, int &slices) {
   nt = tiles > 1 ? kMostTiles : 1;
 }
 
-// workgroups per CU the kernel is built for: what its registers allow (a
-// lane's scales and biases grow with the groups of a row)
+// Workgroups per CU the kernel is built for: what its registers allow (a lane's
+// scales and biases grow with the groups of a row).  Two where three could be
+// built with fewer loads under way: 16 sequences of up to 4096 tokens, 8 bits,
+// 23.9 against 26.4 us at one step; 16 bits 54 against 60.
 constexpr int wgs_per_cu(int D, int NG, int NT) {
   return D * NT <= 64 ? 3 : (D * NT <= 128 || (D * NT <= 256 && NG <= 2) ? 2 : 1);
 }
@@ -1295,8 +1309,11 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
   // A unit's pieces, each `items` times four values, are joined by one
   // workgroup inside the launch, unless one sequence could have so many (a
   // piece is four tiles at least) that a launch over the whole chip is faster:
-  // that costs 2 to 3 us wherever anything is cut, one workgroup about 1 us per
-  // thousand of pieces times items (85 pieces of 1024 items: 83 us).
+  // one sequence, one key head, 64 pieces of 1024 items 15.7 us against 46.5;
+  // one of 131072 tokens, 8 key heads, 64 of 128 items 41 against 46.  Where
+  // there are few, that launch only costs: 16 sequences, 4 pieces of 128 items
+  // each on average 21.8 us against 20.7; 16 with 40 rows a key head, 2 of 1024
+  // items 133 against 123 (which the rule, not knowing lengths, puts there).
   const int items = (int)(cols < 16 * nt ? cols : 16 * nt) * c.head_dim / 4;
   const int64_t pieces = (cap + NW * kTile - 1) / (NW * kTile);
   p.inside = per_tile > kMaxGrid || (pieces < grid ? pieces : grid) * items <= 16384;

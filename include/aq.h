@@ -412,8 +412,8 @@ typedef struct aq_kv_cache {
  * contiguous, tokens k_stride and v_stride elements apart (multiples of 8, at
  * least kv_heads * head_dim), so both may be parts of one projection's rows.
  * slots: device int64 [T]; a slot outside [0, num_pages * page_size) writes
- * nothing; two equal slots in one call leave either token's rows, group by
- * group.  Values are clamped to fp16's finite range first; a group that holds
+ * nothing; the slots of one call are to differ (equal ones leave a mixture of
+ * their tokens' rows).  Values are clamped to fp16's finite range first; a group that holds
  * a NaN gets scale 0, bias NaN and codes 0, so all of it reads back as NaN.
  * bits = 16: x_dtype must be the cache's dtype, rows are copied as they are.
  * T = 0 does nothing.  Scales and biases are required unless bits = 16. */
