@@ -1186,6 +1186,7 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
 // takes 64 times four values of one unit, its eight waves every eighth piece
 // each, and adds the waves' parts in order.
 constexpr int kJoinWaves = 8;
+template <int N> struct Count { static constexpr int value = N; };
 template <int D>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, int nt) {
   __shared__ float part[kJoinWaves][6][64];
@@ -1202,23 +1203,32 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, in
   const int c = on ? item / Q : 0, d = on ? (item % Q) * 4 : 0;
   const int PF = piece_floats(D, nt);
   const float *first = p.parts + (2 * (int64_t)w0 + 1) * PF;
+  // a wave's pieces, U at once (no more loads than there are pieces)
   Strand st;
-  constexpr int U = 8;
-  for (int i = wave; i < n; i += U * kJoinWaves) {
-    f32x4v v[U];
-    float pm[U], pl[U];
+  auto add = [&](auto at_once) {
+    constexpr int U = decltype(at_once)::value;
+    for (int i = wave; i < n; i += U * kJoinWaves) {
+      f32x4v v[U];
+      float pm[U], pl[U];
 #pragma unroll
-    for (int x = 0; x < U; ++x) {
-      const int k = i + x * kJoinWaves < n ? i + x * kJoinWaves : i;
-      const float *src = first + (k ? (2 * (int64_t)k - 1) * PF : 0);
-      v[x] = *reinterpret_cast<const f32x4v *>(src + c * D + d);
-      pm[x] = src[nt * 16 * D + c];
-      pl[x] = src[nt * 16 * D + nt * 16 + c];
+      for (int x = 0; x < U; ++x) {
+        const int k = i + x * kJoinWaves < n ? i + x * kJoinWaves : i;
+        const float *src = first + (k ? (2 * (int64_t)k - 1) * PF : 0);
+        v[x] = *reinterpret_cast<const f32x4v *>(src + c * D + d);
+        pm[x] = src[nt * 16 * D + c];
+        pl[x] = src[nt * 16 * D + nt * 16 + c];
+      }
+#pragma unroll
+      for (int x = 0; x < U; ++x)
+        if (i + x * kJoinWaves < n) st.add(pm[x], pl[x], v[x]);
     }
-#pragma unroll
-    for (int x = 0; x < U; ++x)
-      if (i + x * kJoinWaves < n) st.add(pm[x], pl[x], v[x]);
-  }
+  };
+  if (n <= kJoinWaves)
+    add(Count<1>());
+  else if (n <= 2 * kJoinWaves)
+    add(Count<2>());
+  else
+    add(Count<8>());
   part[wave][0][lane] = st.m;
   part[wave][1][lane] = st.l;
 #pragma unroll
