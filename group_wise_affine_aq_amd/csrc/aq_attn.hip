@@ -1183,13 +1183,12 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
 }
 
 // Joins the pieces of units that were cut, in a launch of its own: a workgroup
-// takes 64 times four values of one unit, its eight waves every eighth piece
-// each, and adds the waves' parts in order.
-constexpr int kJoinWaves = 8;
+// takes 64 times four values of one unit, each of its JW waves every JW-th
+// piece, and adds the waves' parts in order.
 template <int N> struct Count { static constexpr int value = N; };
-template <int D>
-__global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, int nt) {
-  __shared__ float part[kJoinWaves][6][64];
+template <int D, int JW>
+__global__ __launch_bounds__(64 * JW) void attn_join_kernel(Params p, int nt) {
+  __shared__ float part[JW][6][64];
   const uint2 cut = p.cuts[blockIdx.x];
   const int n = uniform(cut.x), w0 = uniform(cut.y);
   if (n == 0) return;
@@ -1207,12 +1206,12 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, in
   Strand st;
   auto add = [&](auto at_once) {
     constexpr int U = decltype(at_once)::value;
-    for (int i = wave; i < n; i += U * kJoinWaves) {
+    for (int i = wave; i < n; i += U * JW) {
       f32x4v v[U];
       float pm[U], pl[U];
 #pragma unroll
       for (int x = 0; x < U; ++x) {
-        const int k = i + x * kJoinWaves < n ? i + x * kJoinWaves : i;
+        const int k = i + x * JW < n ? i + x * JW : i;
         const float *src = first + (k ? (2 * (int64_t)k - 1) * PF : 0);
         v[x] = *reinterpret_cast<const f32x4v *>(src + c * D + d);
         pm[x] = src[nt * 16 * D + c];
@@ -1220,12 +1219,12 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, in
       }
 #pragma unroll
       for (int x = 0; x < U; ++x)
-        if (i + x * kJoinWaves < n) st.add(pm[x], pl[x], v[x]);
+        if (i + x * JW < n) st.add(pm[x], pl[x], v[x]);
     }
   };
-  if (n <= kJoinWaves)
+  if (n <= JW)
     add(Count<1>());
-  else if (n <= 2 * kJoinWaves)
+  else if (n <= 2 * JW)
     add(Count<2>());
   else
     add(Count<8>());
@@ -1237,7 +1236,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(Params p, in
   if (wave != 0 || !on) return;
   // (waves without a piece left a maximum of -inf and zeros)
 #pragma unroll
-  for (int w = 1; w < kJoinWaves; ++w)
+  for (int w = 1; w < JW; ++w)
     st.add(part[w][0][lane], part[w][1][lane],
            f32x4v{part[w][2][lane], part[w][3][lane], part[w][4][lane], part[w][5][lane]});
   put_result<D>(p, b, head, slice * nt * 16 + c, d, st.result());
@@ -1261,8 +1260,11 @@ void tiles_for(int64_t cols, int &nt, int &slices) {
 // scales and biases grow with the groups of a row).  Two where three could be
 // built with fewer loads under way: 16 sequences of up to 4096 tokens, 8 bits,
 // 23.9 against 26.4 us at one step; 16 bits 54 against 60.
-constexpr int wgs_per_cu(int D, int NG, int NT) {
-  return D * NT <= 64 ? 3 : (D * NT <= 128 || (D * NT <= 256 && NG <= 2) ? 2 : 1);
+// Heads of 64, quantized, three: 32 sequences of up to 8192 tokens, 4 bits 41.8
+// against 53.7 us (8 sequences of up to 2048 14.1 against 11.5); not at 16 bits,
+// 34.5 against 29.6.
+constexpr int wgs_per_cu(int BITS, int D, int NG, int NT) {
+  return D * NT <= 64 && BITS != 16 ? 3 : (D * NT <= 128 || (D * NT <= 256 && NG <= 2) ? 2 : 1);
 }
 
 }  // namespace
@@ -1270,7 +1272,7 @@ constexpr int wgs_per_cu(int D, int NG, int NT) {
 int64_t attn_workspace_bytes(int64_t, int L, int q_heads, int kv_heads, int head_dim) {
   int nt, slices;
   tiles_for((int64_t)L * (q_heads / kv_heads), nt, slices);
-  const int wgs = device_cus() * wgs_per_cu(head_dim, 1, nt);
+  const int wgs = device_cus() * wgs_per_cu(8, head_dim, 1, nt);
   return kMaxGrid * 12 + (int64_t)(wgs < kMaxGrid ? wgs : kMaxGrid) * 2 * piece_floats(head_dim, nt) * 4;
 }
 
@@ -1310,7 +1312,7 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
   // no more workgroups than chunks the table can hold
   const int64_t most = (cap + chunk - 1) / chunk * per_tile;
   int64_t grid = (int64_t)device_cus() *
-                 wgs_per_cu(c.head_dim, c.bits == 16 ? 1 : c.head_dim / c.group_size, nt);
+                 wgs_per_cu(c.bits, c.head_dim, c.bits == 16 ? 1 : c.head_dim / c.group_size, nt);
   if (grid > kMaxGrid) grid = kMaxGrid;
   if (most < grid) grid = most;
   p.cuts = reinterpret_cast<uint2 *>(a.workspace);
@@ -1329,7 +1331,7 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
   p.inside = per_tile > kMaxGrid || (pieces < grid ? pieces : grid) * items <= 16384;
   hipError_t err = hipErrorInvalidValue;
 #define AQ_KT(B, F, D, G, T)                                                           \
-  hipLaunchKernelGGL((attn_kernel<B, F, D, G, T, wgs_per_cu(D, D / G, T)>),            \
+  hipLaunchKernelGGL((attn_kernel<B, F, D, G, T, wgs_per_cu(B, D, D / G, T)>),         \
                      dim3((unsigned)grid), dim3(64 * NW), 0, s, p)
 #define AQ_K(B, F, D, G)                                                               \
   do {                                                                                 \
@@ -1362,8 +1364,17 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
   // (a chunk that holds the whole table: no unit is cut)
   if (err != hipSuccess || cap <= chunk || p.inside) return err;
   const dim3 join((unsigned)per_tile, (unsigned)((items + 63) / 64));
-#define AQ_J(D) \
-  hipLaunchKernelGGL((attn_join_kernel<D>), join, dim3(64 * kJoinWaves), 0, s, p, nt)
+  // Eight waves, as long as the chip holds them all; else four: 128 units of
+  // 1024 items 39.5 us a call against 41.2, 256 124.5 against 127.8; 8 of 128
+  // items 42.6 against 41.9.
+  const bool room = (int64_t)join.x * join.y * 8 <= (int64_t)device_cus() * 32;
+#define AQ_J(D)                                                                          \
+  do {                                                                                   \
+    if (room)                                                                            \
+      hipLaunchKernelGGL((attn_join_kernel<D, 8>), join, dim3(64 * 8), 0, s, p, nt);     \
+    else                                                                                 \
+      hipLaunchKernelGGL((attn_join_kernel<D, 4>), join, dim3(64 * 4), 0, s, p, nt);     \
+  } while (0)
   if (c.head_dim == 64) AQ_J(64);
   else if (c.head_dim == 128) AQ_J(128);
   else AQ_J(256);
