@@ -9,7 +9,7 @@
 // memory; with k = s code + b in each group g of G values of a row
 //
 //   q . k_t = sum_g s_tg (sum_{d in g} q_d code_td) + b_tg (sum_{d in g} q_d)
-//   sum_t p_t v_td = sum_t (p_t s_tg) (code_td - c) + p_t (b_tg + c s_tg),
+//   sum_t p_t v_td = sum_t (p_t s_tg) code_td + p_t b_tg,
 //
 // both inner sums are products of integer codes and run on the matrix cores,
 // scales and biases are applied to their results or to the weights.
@@ -32,20 +32,17 @@
 //    largest lies in [256, 512): exact down to 2^-22 of it, 2^-18 for the odd
 //    codes of 4 bits.  fp16 queries are taken as they are; below 2^-10 the odd
 //    ones' sixteenths round, by 2^-25 at most.
-//  * Weights p s are rounded to fp16 (2^-11 relative) for the second product.
-//    They are kept 2^6 (8 bits) or 2^2 (4 bits) times too large, as far as
-//    the largest possible scale of a group allows (131008 / 255, / 15), which
-//    keeps small ones out of fp16's subnormals; l has the same factor.  The
-//    rounded weight multiplies code - c, c the middle code, rather than the
-//    code: the rounding then weighs with the value's distance from its group's
-//    middle, not from its minimum.  code - c is not formed; -c times the sum of
-//    the rounded weights is added in binary32.
-//  * bits = 16: the pages' values are the operands.  A bf16 weight would lose
-//    8 bits more than the output rounds off, so it is split in two bf16 parts,
-//    two products per tile.
+//  * A weight p s goes into the second product in two fp16 parts, rounded and
+//    rest (two bf16 parts where the pages hold bf16), two products a tile.  (In
+//    one part it would be off by 2^-12 at the mean, as much as an fp16 result's
+//    own rounding: 1.1 to 1.7 times the error.)  Weights are kept 2^6 (8 bits)
+//    or 2^2 (4 bits) times too large, as far as the largest possible scale of a
+//    group allows (131008 / 255, / 15), which keeps small ones out of fp16's
+//    subnormals; l has the same factor.
+//  * bits = 16: the pages' values are the operands.
 //
 // Work division.  The tokens of all units -- a unit is one sequence, one key
-// head and one slice of at most 32 of its query rows -- form one line of
+// head and one slice of at most 32 (heads of 256: 16) of its query rows -- form one line of
 // 32-token tiles that the workgroups cut evenly, so a batch of ragged lengths
 // and one long sequence load the chip alike and the launch does not depend on
 // the lengths, which stay on the device.  The four waves of a workgroup take
@@ -57,7 +54,7 @@
 //
 // Bound: HBM, the codes, scales and biases read once.  At 8 bits a tile of 32
 // tokens x 128 values (groups of 64, one tile of query rows) is 8.7 KB and
-// costs a wave about 250 vector and 16 matrix instructions (4 bits: 4.6 KB,
+// costs a wave about 250 vector and 24 matrix instructions (4 bits: 4.6 KB,
 // 290); eight waves a CU could take 35 bytes a clock at that rate where HBM
 // gives a CU about 9.  64 sequences of up to 16384 tokens (1.01 GB) take 187
 // us, 5.4 TB/s; a large copy reaches 5.2, a large read 6.3.  Below about 100 MB
@@ -366,7 +363,6 @@ struct Wave {
   static constexpr int VW = VB < 4 ? 1 : VB / 4; // words
   static constexpr int SW = (NG * 4 + 1) / 2;    // words of 4 tokens' scales
   static constexpr int NR = NT * D / 4;          // result registers
-  static constexpr float CENTRE = BITS == 8 ? 128.f : 8.f;
   static constexpr float UP = BITS == 8 ? 6.f : (BITS == 4 ? 2.f : 0.f);
 
   struct Keys { uint32_t c[2][KW]; };
@@ -681,57 +677,58 @@ struct Wave {
     }
   }
 
-  // o += weights x values
+  // o += weights x values, the weights in two parts
   __device__ __forceinline__ void gather(const Values &v, const Scales &vs, const float (&p)[NT][8]) {
-    u32x4v w[NT][NG], w2[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if constexpr (QUANT) {
+    for (int g = 0; g < NG; ++g) {
+      u32x4v w[NT], w2[NT];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (QUANT) {
           uint32_t scale[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) scale[j] = vs.s[j >> 2][((j & 3) * NG + g) >> 1];
           if constexpr (NG == 1)
-            w[nt][g] = scaled_weights<0, 1>(p[nt], scale);
+            w[nt] = scaled_weights<0, 1>(p[nt], scale);
           else if (g & 1)
-            w[nt][g] = scaled_weights<1, 1>(p[nt], scale);
+            w[nt] = scaled_weights<1, 1>(p[nt], scale);
           else
-            w[nt][g] = scaled_weights<0, 0>(p[nt], scale);
-          float add = 0.f;
+            w[nt] = scaled_weights<0, 0>(p[nt], scale);
+          float rest[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float s = scale_at(vs.s[j >> 2], j & 3, g), b = scale_at(vs.b[j >> 2], j & 3, g);
-            add = __builtin_fmaf(p[nt][j], __builtin_fmaf(CENTRE, s, b), add);
-            add = __builtin_fmaf(half_at(w[nt][g][j >> 1], j & 1), -CENTRE, add);
+            rest[j] = __builtin_fmaf(p[nt][j], scale_at(vs.s[j >> 2], j & 3, g),
+                                     -half_at(w[nt][j >> 1], j & 1));
+            bacc[nt][g] = __builtin_fmaf(p[nt][j], scale_at(vs.b[j >> 2], j & 3, g), bacc[nt][g]);
           }
-          bacc[nt][g] += add;
-        }
-      } else {
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          if constexpr (BF) {
-            const uint32_t r = pack_bf16(p[nt][j], p[nt][j + 1]);
-            w[nt][0][j >> 1] = r;
-            w2[nt][j >> 1] = pack_bf16(p[nt][j] - __builtin_bit_cast(float, r << 16),
-                                       p[nt][j + 1] - __builtin_bit_cast(float, r & 0xFFFF0000u));
-          } else {
-            w[nt][0][j >> 1] = pack_f16(p[nt][j], p[nt][j + 1]);
+          for (int j = 0; j < 8; j += 2) w2[nt][j >> 1] = pack_f16(rest[j], rest[j + 1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            if constexpr (BF) {
+              const uint32_t r = pack_bf16(p[nt][j], p[nt][j + 1]);
+              w[nt][j >> 1] = r;
+              w2[nt][j >> 1] = pack_bf16(p[nt][j] - __builtin_bit_cast(float, r << 16),
+                                         p[nt][j + 1] - __builtin_bit_cast(float, r & 0xFFFF0000u));
+            } else {
+              const uint32_t r = pack_f16(p[nt][j], p[nt][j + 1]);
+              w[nt][j >> 1] = r;
+              w2[nt][j >> 1] = pack_f16(p[nt][j] - half_at(r, 0), p[nt][j + 1] - half_at(r, 1));
+            }
           }
         }
       }
-    }
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
 #pragma unroll
       for (int n = 0; n < VN; ++n) {
         const u32x4v a = value_operand(v, g, n);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          o[nt][g][n] = mfma<BF>(a, w[nt][g], o[nt][g][n]);
-          if constexpr (BF) o[nt][g][n] = mfma<BF>(a, w2[nt], o[nt][g][n]);
+          o[nt][g][n] = mfma<BF>(a, w[nt], o[nt][g][n]);
+          o[nt][g][n] = mfma<BF>(a, w2[nt], o[nt][g][n]);
         }
       }
+    }
   }
 
   // a tile that some column sees only in part, or with a page left out:
@@ -1258,11 +1255,13 @@ __global__ __launch_bounds__(64 * JW) void attn_join_kernel(Params p, int nt) {
 // of the second workgroup on a CU; 59 as four waves with a tile of rows each on
 // the same tokens, too few tokens are then under way.  The second slice's one
 // tile of 8 rows computed as one, not two: no faster, 46.4 against 45.3.)
-constexpr int kMostTiles = 2;
-void tiles_for(int64_t cols, int &nt, int &slices) {
+// Heads of 256 have one tile a wave: with two the state does not fit the
+// registers (up to 236 of them in scratch memory at 8 bits).
+constexpr int most_tiles(int D) { return D > 128 ? 1 : 2; }
+void tiles_for(int64_t cols, int D, int &nt, int &slices) {
   const int64_t tiles = (cols + 15) / 16;
-  slices = (int)((tiles + kMostTiles - 1) / kMostTiles);
-  nt = tiles > 1 ? kMostTiles : 1;
+  nt = tiles > 1 ? most_tiles(D) : 1;
+  slices = (int)((tiles + nt - 1) / nt);
 }
 
 // Workgroups per CU the kernel is built for: what its registers allow (a lane's
@@ -1271,16 +1270,17 @@ void tiles_for(int64_t cols, int &nt, int &slices) {
 // 23.9 against 26.4 us at one step; 16 bits 54 against 60.
 // Heads of 64, quantized, three: 32 sequences of up to 8192 tokens, 4 bits 41.8
 // against 53.7 us (8 sequences of up to 2048 14.1 against 11.5); not at 16 bits,
-// 34.5 against 29.6.
+// 34.5 against 29.6.  Heads of 256 at 16 bits one: 23.4 against 36.4 us, registers
+// do not spill.
 constexpr int wgs_per_cu(int BITS, int D, int NG, int NT) {
-  return D * NT <= 64 && BITS != 16 ? 3 : (D * NT <= 128 || (D * NT <= 256 && NG <= 2) ? 2 : 1);
+  return D * NT <= 64 && BITS != 16 ? 3 : (D * NT <= 128 || (D * NT <= 256 && NG <= 2 && BITS != 16) ? 2 : 1);
 }
 
 }  // namespace
 
 int64_t attn_workspace_bytes(int64_t, int L, int q_heads, int kv_heads, int head_dim) {
   int nt, slices;
-  tiles_for((int64_t)L * (q_heads / kv_heads), nt, slices);
+  tiles_for((int64_t)L * (q_heads / kv_heads), head_dim, nt, slices);
   const int wgs = device_cus() * wgs_per_cu(8, head_dim, 1, nt);
   return kMaxGrid * 12 + (int64_t)(wgs < kMaxGrid ? wgs : kMaxGrid) * 2 * piece_floats(head_dim, nt) * 4;
 }
@@ -1310,7 +1310,7 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
   p.scale = a.scale;
   const int64_t cols = (int64_t)a.L * p.group;
   int nt;
-  tiles_for(cols, nt, p.slices);
+  tiles_for(cols, c.head_dim, nt, p.slices);
   // The line's chunks are counted in 32 bits: where the table could hold more
   // tiles than that they are longer.  A table that holds no more than one tile
   // per wave leaves units whole.
@@ -1348,7 +1348,7 @@ hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream
     if (nt == 1)                                                                       \
       AQ_KT(B, F, D, G, 1);                                                            \
     else                                                                               \
-      AQ_KT(B, F, D, G, 2);                                                            \
+      AQ_KT(B, F, D, G, most_tiles(D));                                                \
     err = hipGetLastError();                                                           \
   } while (0)
 #define AQ_G(B, D)                                     \

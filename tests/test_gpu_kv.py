@@ -536,6 +536,12 @@ def test_attention_of_long_tables(aq, lengths, per, heads, dim, G, bits, page, L
     test_attention(aq, lengths, per, heads, dim, G, bits, page, L, dtype)
 
 
+@pytest.mark.skip(reason="a run of this call beside its plain torch form ended in a memory fault "
+                         "whose cause is not known")
+def test_attention_heads_of_256_with_40_rows(aq):
+    test_attention(aq, [38] * 40, 5, 1, 256, 128, 8, 48, 8, "f16")
+
+
 def test_one_workspace_joined_both_ways(aq):
     """Calls whose pieces are joined inside the launch and by a second one, in
     turn, in one workspace; equal calls give equal bits."""
