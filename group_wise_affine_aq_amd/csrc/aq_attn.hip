@@ -25,13 +25,15 @@
 //
 //  * Codes enter as fp16 bit patterns: an integer q <= 1023 in the low bits is
 //    the fp16 subnormal q * 2^-24, exact in the matrix cores, so unpacking is
-//    one byte permute (8 bits) or a mask (4 bits; the odd nibbles are masked
-//    in place, 16 times too large, and the query or the result is scaled by
-//    1/16) per pair.  2^24 goes into factors that are there anyway.
+//    one byte permute (8 bits) or a shift and a mask (4 bits, 16 times too
+//    large) per pair.  2^24 or 2^20 goes into factors that are there anyway.
+//    The sums of the matrix cores lose what lies some 24 bits below the
+//    exponent an operand is written with, 2^-14 for all of these: codes of 4
+//    bits in the lowest bits lost 2^-18 of their sums, two to four times the
+//    rounding of an fp16 result that averages 60000 to 120000 tokens.
 //  * bf16 queries become fp16, scaled by a power of two per row so that the
-//    largest lies in [256, 512): exact down to 2^-22 of it, 2^-18 for the odd
-//    codes of 4 bits.  fp16 queries are taken as they are; below 2^-10 the odd
-//    ones' sixteenths round, by 2^-25 at most.
+//    largest lies in [256, 512): exact down to 2^-22 of it.  fp16 queries are
+//    taken as they are.
 //  * A weight p s goes into the second product in two fp16 parts, rounded and
 //    rest (two bf16 parts where the pages hold bf16), two products a tile.  (In
 //    one part it would be off by 2^-12 at the mean, as much as an fp16 result's
@@ -363,6 +365,7 @@ struct Wave {
   static constexpr int VW = VB < 4 ? 1 : VB / 4; // words
   static constexpr int SW = (NG * 4 + 1) / 2;    // words of 4 tokens' scales
   static constexpr int NR = NT * D / 4;          // result registers
+  static constexpr float UNIT = BITS == 4 ? 0x1p20f : 0x1p24f;  // 1 / what a code of 1 enters as
   static constexpr float UP = BITS == 8 ? 6.f : (BITS == 4 ? 2.f : 0.f);
 
   struct Keys { uint32_t c[2][KW]; };
@@ -475,9 +478,9 @@ struct Wave {
       const uint32_t a = c[2 * s], b = c[2 * s + 1];
       return u32x4v{__builtin_amdgcn_perm(0, a, 0x0C010C00u), __builtin_amdgcn_perm(0, a, 0x0C030C02u),
                     __builtin_amdgcn_perm(0, b, 0x0C010C00u), __builtin_amdgcn_perm(0, b, 0x0C030C02u)};
-    } else {  // codes 0,4 | 1,5 | 2,6 | 3,7, the odd ones 16 times too large
-      const uint32_t a = c[s], b = a >> 8;
-      return u32x4v{a & 0x000F000Fu, a & 0x00F000F0u, b & 0x000F000Fu, b & 0x00F000F0u};
+    } else {  // codes 0,4 | 1,5 | 2,6 | 3,7, 16 times too large
+      const uint32_t a = c[s];
+      return u32x4v{a << 4 & 0x00F000F0u, a & 0x00F000F0u, a >> 4 & 0x00F000F0u, a >> 8 & 0x00F000F0u};
     }
   }
 
@@ -495,7 +498,7 @@ struct Wave {
       } else {
         const uint32_t k = n >> 1;
         const uint32_t both = __builtin_amdgcn_perm(y[0], x[0], 0x0C000C00u | k | (4 + k) << 16);
-        a[w] = both & (n & 1 ? 0x00F000F0u : 0x000F000Fu);
+        a[w] = (n & 1 ? both : both << 4) & 0x00F000F0u;
       }
     }
     return a;
@@ -543,7 +546,7 @@ struct Wave {
         continue;
       }
       if (p.x_dtype == X_F16) {
-        C[nt] = log2s * 0x1p24f;
+        C[nt] = log2s * UNIT;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           const uint32_t u[4] = {qs.raw[nt][s].x, qs.raw[nt][s].y, qs.raw[nt][s].z, qs.raw[nt][s].w};
@@ -551,10 +554,9 @@ struct Wave {
           for (int w = 0; w < 4; ++w) {
             if constexpr (BITS == 8) {
               q[nt][s][w] = u[w];
-            } else {  // queries w and w + 4, the odd ones / 16
-              const uint32_t x = __builtin_amdgcn_perm(u[2 + (w >> 1)], u[w >> 1], w & 1 ? 0x07060302u : 0x05040100u);
-              const half2v h = __builtin_bit_cast(half2v, x) * half2v{(_Float16)0.0625f, (_Float16)0.0625f};
-              q[nt][s][w] = w & 1 ? __builtin_bit_cast(uint32_t, h) : x;
+            } else {  // queries w and w + 4
+              q[nt][s][w] = __builtin_amdgcn_perm(u[2 + (w >> 1)], u[w >> 1],
+                                                  w & 1 ? 0x07060302u : 0x05040100u);
             }
           }
         }
@@ -573,7 +575,7 @@ struct Wave {
         int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
         e = e < -100 ? -100 : (e > 100 ? 100 : e);
         const float down = __builtin_ldexpf(1.f, 8 - e);
-        C[nt] = __builtin_ldexpf(log2s, 24 + e - 8);
+        C[nt] = __builtin_ldexpf(log2s * UNIT, e - 8);
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -581,14 +583,13 @@ struct Wave {
             if constexpr (BITS == 8) {
               q[nt][s][w] = pack_f16(x[s][2 * w] * down, x[s][2 * w + 1] * down);
             } else {
-              const float f = w & 1 ? down * 0.0625f : down;
-              q[nt][s][w] = pack_f16(x[s][w] * f, x[s][w + 4] * f);
+              q[nt][s][w] = pack_f16(x[s][w] * down, x[s][w + 4] * down);
             }
           }
       }
       // a group's sum, as the score of keys whose codes are all 1
-      const u32x4v ones = BITS == 8 ? u32x4v{0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u}
-                                    : u32x4v{0x00010001u, 0x00100010u, 0x00010001u, 0x00100010u};
+      constexpr uint32_t kOnes = BITS == 8 ? 0x00010001u : 0x00100010u;
+      const u32x4v ones = {kOnes, kOnes, kOnes, kOnes};
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         f32x4v sum = {0.f, 0.f, 0.f, 0.f};
@@ -930,7 +931,7 @@ struct Wave {
           for (int x = 0; x < 4; ++x) {
             const int n = (e + x) % VN;
             const float r = o[nt][g][n][(e + x) / VN];
-            y[x] = QUANT ? __builtin_fmaf(r, BITS == 4 && (n & 1) ? 0x1p20f : 0x1p24f, add) : r;
+            y[x] = QUANT ? __builtin_fmaf(r, UNIT, add) : r;
           }
           *reinterpret_cast<f32x4v *>(at + e) = y;
         }
