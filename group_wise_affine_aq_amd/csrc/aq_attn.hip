@@ -809,22 +809,24 @@ struct Wave {
     int64_t rows[2];
     bool on[2], on_next[2];
     int c0 = tile0, first, tiles;
-    // up to 32 tiles' pages at once
+    // up to 32 tiles' pages at once; lanes without one look up the first.  No
+    // branch: where some lanes of a wave leave a branch, the compiler may place
+    // copies of any live register ahead of the instruction that turns the other
+    // lanes on again, and those lose it.  It did so here in a build of two tiles
+    // of columns at heads of 256: lanes lost their thread's number and with it
+    // the address of the rows they write.
     auto look_up = [&] {
       first = c0 * kTile;
       const int left = (end - c0 + NW - 1) / NW;
       tiles = left < 32 ? left : 32;
-      row_lo = 0, row_hi = 0x80000000u;
       const int64_t t = (int64_t)first + (lane >> 1) * (NW * kTile) + (lane & 1) * 16;
-      if ((lane >> 1) < tiles && t < len) {
-        const uint32_t s = (uint32_t)(t >> 4), pg = page_of(p, s);
-        const int id = p.table[(int64_t)b * p.max_pages + pg];
-        if (id >= 0 && id < p.num_pages) {
-          const int64_t row = (((int64_t)id * p.kv_heads + head) * p.page_subs + (s - pg * p.page_subs)) * 16;
-          row_lo = (uint32_t)row;
-          row_hi = (uint32_t)(row >> 32);
-        }
-      }
+      const bool want = (lane >> 1) < tiles && t < len;
+      const uint32_t s = (uint32_t)((want ? t : (int64_t)first) >> 4), pg = page_of(p, s);
+      const int id = p.table[(int64_t)b * p.max_pages + pg];
+      const bool there = want && id >= 0 && id < p.num_pages;
+      const int64_t row = (((int64_t)id * p.kv_heads + head) * p.page_subs + (s - pg * p.page_subs)) * 16;
+      row_lo = there ? (uint32_t)row : 0u;
+      row_hi = there ? (uint32_t)(row >> 32) : 0x80000000u;
     };
     auto locate = [&](int tile, bool *there) {
 #pragma unroll
@@ -909,32 +911,29 @@ struct Wave {
 
   // (m, l, o) of the wave's tile nt of columns, the biases' part folded in, to
   // its place in LDS: rows of D results per column, then the columns' m and l.
+  // All lanes write (a column's m and l four times), for the reason that the
+  // pages' look-up has no branch.
   static constexpr int PF = piece_floats(D, NT);
   static constexpr int ROW = D + 4;  // columns on different banks
   static constexpr int SHARE = 16 * ROW;
-  __device__ __forceinline__ void give(int nt, float *o_at, float *ml_at, int used) {
+  __device__ __forceinline__ void give(int nt, float *o_at, float *ml_at) {
     const int lane = lane_here(), c = lane & 15, h = lane >> 4;
-    const float sum = quarters_sum(l[nt]);
-    if (lane < 16) {
-      ml_at[lane] = m[nt];
-      ml_at[16 + lane] = sum;
-    }
+    ml_at[c] = m[nt];
+    ml_at[16 + c] = quarters_sum(l[nt]);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const float add = QUANT ? quarters_sum(bacc[nt][g]) : 0.f;
-      if (nt * 16 + c < used) {
-        float *at = o_at + c * ROW + g * G + 4 * h * VN;
+      float *at = o_at + c * ROW + g * G + 4 * h * VN;
 #pragma unroll
-        for (int e = 0; e < 4 * VN; e += 4) {  // value e: row e / VN of product e % VN
-          f32x4v y;
+      for (int e = 0; e < 4 * VN; e += 4) {  // value e: row e / VN of product e % VN
+        f32x4v y;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int n = (e + x) % VN;
-            const float r = o[nt][g][n][(e + x) / VN];
-            y[x] = QUANT ? __builtin_fmaf(r, UNIT, add) : r;
-          }
-          *reinterpret_cast<f32x4v *>(at + e) = y;
+        for (int x = 0; x < 4; ++x) {
+          const int n = (e + x) % VN;
+          const float r = o[nt][g][n][(e + x) / VN];
+          y[x] = QUANT ? __builtin_fmaf(r, UNIT, add) : r;
         }
+        *reinterpret_cast<f32x4v *>(at + e) = y;
       }
     }
   }
@@ -1125,7 +1124,7 @@ __global__ __launch_bounds__(64 * NW, WGS) void attn_kernel(Params p) {
     constexpr int Q = D / 4;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (wave < busy) st.give(nt, buf + wave * W::SHARE, ml + wave * 32, used);
+      if (wave < busy) st.give(nt, buf + wave * W::SHARE, ml + wave * 32);
       __syncthreads();
       const int live = used - nt * 16 < 16 ? used - nt * 16 : 16;
       for (int item = threadIdx.x; item < live * Q; item += 64 * NW) {

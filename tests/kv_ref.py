@@ -126,3 +126,74 @@ def attention(q, cache, table, lengths, scale):
 def rounding(dtype):
     """Unit roundoff of the output type."""
     return {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
+
+
+def attention_rows(q, cache, table, lengths, scale, change=None):
+    """q [B, L, Hq, D] -> (out, slack [B, L, Hq]): the formula in binary64, and
+    how far from it a result's row may lie, as the 2-norm over its D values,
+    before the output's own rounding:
+
+    * sums.  The values enter as p s code + p b, whose absolute values sum to at
+      most V = p . (|b| + 2^bits s) (16 bits: p . |v|).  A wave adds its tiles
+      into one binary32 sum, 64 of them at most in the tests, and a piece or a
+      wave's share is rescaled and added a few more times: 64 * 2^-24 of V.
+    * weights.  The two parts hold 2^-22 of a weight (bf16: 2^-16), rounded to
+      either side, so that over the tokens of a row they add like a random walk:
+      2^-22 (2^-16) of the 2-norm of p times the same sizes.
+    * scores.  The rounding errors of one score's partial sums add like a random
+      walk: 2^-22 of scale times the 2-norm over d of q_d (|b| + 2^bits s), for
+      the largest token; a weight carries it once and the weights' sum once more.
+
+    `change(p, sees)` gives other weights for the softmax's (to show what the
+    comparison refuses)."""
+    B, L, Hq, D = q.shape
+    pages, heads, page = cache.shape
+    group = Hq // heads
+    part = 2.0 ** -16 if cache.bits == 16 and cache.dtype == "bf16" else 2.0 ** -22
+    out, slack = np.zeros(q.shape), np.zeros(q.shape[:3])
+    for b in range(B):
+        n = min(max(0, int(lengths[b])), table.shape[1] * page)
+        for h in range(heads):
+            rows = {"k": [], "v": [], "t": []}
+            for p in range(-(-n // page)):
+                if 0 <= table[b, p] < pages:
+                    count = min(page, n - p * page)
+                    for name in "kv":
+                        rows[name].append(cache.row(name, table[b, p], h, count))
+                    rows["t"].append(np.arange(p * page, p * page + count))
+            if not rows["t"]:
+                continue
+            t = np.concatenate(rows["t"])
+            (k, ka), (v, va) = ([np.concatenate(x) for x in zip(*rows[name])] for name in "kv")
+            at = slice(h * group, (h + 1) * group)
+            for i in range(L):
+                sees = t <= n - L + i
+                if not sees.any():
+                    continue
+                qi = q[b, i, at]
+                s = scale * (qi @ k[sees].T)
+                w = np.exp(s - s.max(1, keepdims=True))
+                w /= w.sum(1, keepdims=True)
+                if change:
+                    w = change(w, t[sees])
+                out[b, i, at] = w @ v[sees]
+                of_sums = 2.0 ** -18 * np.linalg.norm(w @ va[sees], axis=1)
+                of_weights = part * np.sqrt((w ** 2) @ (va[sees] ** 2).sum(1))
+                score = 2.0 ** -22 * abs(scale) * np.sqrt((qi ** 2) @ (ka[sees] ** 2).T).max(1)
+                of_scores = 2 * score * np.linalg.norm(w @ np.abs(v[sees]), axis=1)
+                slack[b, i, at] = of_sums + of_weights + of_scores
+    return out, slack
+
+
+def rows_off(got, ref, slack, dtype):
+    """Worst row of got against ref: the 2-norm of the error over what it may be,
+    half as much again as the norm that rounding ref to the output's type leaves,
+    the slack, and half a unit of fp16's smallest in every value."""
+    own = np.linalg.norm(to_values(ref, dtype) - ref, axis=-1)
+    off = np.linalg.norm(got - ref, axis=-1)
+    return (off / (1.5 * own + slack + 2.0 ** -25 * np.sqrt(ref.shape[-1]))).max()
+
+
+def to_values(x, dtype):
+    """x rounded to f16 / bf16, in binary64."""
+    return to_bits(x, dtype)[1]
