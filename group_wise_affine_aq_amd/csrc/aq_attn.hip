@@ -485,13 +485,13 @@ struct Wave {
   }
 
   // the operand of value n of group g: the lane's 8 tokens
-  static __device__ __forceinline__ u32x4v value_operand(const Values &v, int g, int n) {
+  static __device__ __forceinline__ u32x4v value_operand(const Values &v, int g, int n, uint32_t halves) {
     u32x4v a;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const uint32_t *x = v.c[2 * w][g], *y = v.c[2 * w + 1][g];
       if constexpr (BITS == 16) {
-        a[w] = __builtin_amdgcn_perm(y[n >> 1], x[n >> 1], n & 1 ? 0x07060302u : 0x05040100u);
+        a[w] = __builtin_amdgcn_perm(y[n >> 1], x[n >> 1], halves + (n & 1) * 0x02020202u);
       } else if constexpr (BITS == 8) {
         const uint32_t k = n & 3;
         a[w] = __builtin_amdgcn_perm(y[n >> 2], x[n >> 2], 0x0C000C00u | k | (4 + k) << 16);
@@ -678,10 +678,16 @@ struct Wave {
     }
   }
 
-  // o += weights x values, the weights in two parts
-  __device__ __forceinline__ void gather(const Values &v, const Scales &vs, const float (&p)[NT][8]) {
+  // o += weights x values, the weights in two parts.  SOME: only in the columns
+  // that see `sees` tokens, from the halves of the values that `keep` has
+  template <bool SOME = false>
+  __device__ __forceinline__ void gather(const Values &v, const Scales &vs, const float (&p)[NT][8],
+                                         int sees = 0, u32x4v keep = {}) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
+      // (opaque, or the operands of all passes are made, and kept, ahead of them)
+      uint32_t halves = 0x05040100u;
+      if constexpr (SOME) asm volatile("" : "+s"(halves));
       u32x4v w[NT], w2[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -722,11 +728,20 @@ struct Wave {
       }
 #pragma unroll
       for (int n = 0; n < VN; ++n) {
-        const u32x4v a = value_operand(v, g, n);
+        u32x4v a = value_operand(v, g, n, halves);
+        if constexpr (SOME) a &= keep;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          o[nt][g][n] = mfma<BF>(a, w[nt], o[nt][g][n]);
-          o[nt][g][n] = mfma<BF>(a, w2[nt], o[nt][g][n]);
+          if constexpr (SOME) {
+            f32x4v y = {0.f, 0.f, 0.f, 0.f};
+            y = mfma<BF>(a, w[nt], y);
+            y = mfma<BF>(a, w2[nt], y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[nt][g][n][i] += vis[nt] == sees ? y[i] : 0.f;
+          } else {
+            o[nt][g][n] = mfma<BF>(a, w[nt], o[nt][g][n]);
+            o[nt][g][n] = mfma<BF>(a, w2[nt], o[nt][g][n]);
+          }
         }
       }
     }
@@ -780,19 +795,18 @@ struct Wave {
   }
 
   // 16 bits: the values themselves may be infinite or NaN, and a lane's values
-  // serve every column, so such a tile is taken once per query token, the
-  // values past that token's sight and the other columns' weights zero
-  __device__ __forceinline__ void edge_pass(Values &v, const float (&p)[NT][8], float (&w)[NT][8],
-                                            int sees, int token, const bool *on, int h) const {
+  // serve every column, so such a tile is taken once per query token: the
+  // values past that token's sight are zero, and what the products give the
+  // other columns (0 * NaN among it) is dropped, not weighed with 0
+  __device__ __forceinline__ void edge_gather(const Values &v, const Scales &vs, const float (&p)[NT][8],
+                                              int sees, int token, const bool *on, int h) {
+    u32x4v keep;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int at = token + 16 * (j >> 2) + 4 * h + (j & 3);
-      const bool seen = on[j >> 2] && at < sees;
-#pragma unroll
-      for (int x = 0; x < VW; ++x) v.c[j][0][x] = seen ? v.c[j][0][x] : 0u;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) w[nt][j] = vis[nt] == sees ? p[nt][j] : 0.f;
+    for (int w = 0; w < 4; ++w) {
+      const int at = token + 16 * (w >> 1) + 4 * h + 2 * (w & 1);
+      keep[w] = on[w >> 1] && at + 1 < sees ? 0xFFFFFFFFu : (on[w >> 1] && at < sees ? 0x0000FFFFu : 0u);
     }
+    gather<true>(v, vs, p, sees, keep);
   }
 
   // tiles first, first + NW, ... below end of a sequence: one wave's part
@@ -875,24 +889,10 @@ struct Wave {
           take_scales(g, strip, 2, lane);
           if (edge) edge_values(g, token, on, lane >> 4);
           gather(v, g, t);
+        } else if (edge) {
+          for (int i = 0; i < p.L; ++i) edge_gather(v, g, t, len - p.L + 1 + i, token, on, lane >> 4);
         } else {
-          const int passes = edge ? p.L : 1;
-          for (int i = 0; i < passes; ++i) {
-            float w[NT][8];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int j = 0; j < 8; ++j) w[nt][j] = t[nt][j];
-            if (edge) {
-              if (i) {
-                locate(tile, on);
-                load_values(v, p, rows, on, lane);
-              }
-              edge_pass(v, t, w, len - p.L + 1 + i, token, on, lane >> 4);
-            }
-            gather(v, g, w);
-          }
-          if (edge && !last) locate(tile + 1, on_next);
+          gather(v, g, t);
         }
         __builtin_amdgcn_sched_barrier(0);
         load_values(v, p, rows, on_next, lane);

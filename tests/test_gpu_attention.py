@@ -47,3 +47,39 @@ def test_heads_of_256_with_40_rows(aq):
 def test_heads_of_128_with_25_rows_of_16_bits(aq, dtype):
     """The form that holds the most registers."""
     _compare(aq, [100, 37, 6, 0], 5, 2, 128, 0, 16, 16, 5, dtype)
+
+
+# ---- what a row does not see ------------------------------------------------------------
+def _set_value(cache, table, b, t, head, bits16, d=slice(None)):
+    """The value row of token t of sequence b, one head, as 16-bit patterns."""
+    page = cache.shape[2]
+    cache.parts["v"][0][table[b, t // page], head, t % page, d] = bits16
+
+
+@pytest.mark.parametrize("what", ["nan", "inf"])
+@pytest.mark.parametrize("L,per,dim", [(3, 2, 64), (8, 2, 128), (5, 5, 128), (3, 1, 256), (8, 5, 64)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_newer_values_stay_with_the_rows_that_see_them(aq, dtype, L, per, dim, what):
+    """16-bit pages, several new tokens, one and two tiles of columns: a value
+    of the newest or second newest token that is not finite leaves the rows of
+    the tokens before it as they are."""
+    lengths, heads = [100, 37, L + 1], 2
+    cache, table = _build(lengths, heads, dim, 0, 16, 16, dtype, seed=L + dim)
+    qb, q = _queries(51, (3, L, per * heads, dim), dtype)
+    clean = _attend(aq, cache, table, lengths, qb, dtype, 0)
+    _check(clean, q, cache, table, lengths, dtype)
+    bad = {"nan": 0x7FFF, "inf": {"f16": 0x7C00, "bf16": 0x7F80}[dtype]}[what]
+    for back in (1, 2):  # the newest token, the second newest
+        dirty, _ = _build(lengths, heads, dim, 0, 16, 16, dtype, seed=L + dim)
+        for b, n in enumerate(lengths):
+            _set_value(dirty, table, b, n - back, 1, bad, slice(0, dim, 3))
+        out = _attend(aq, dirty, table, lengths, qb, dtype, 0)
+        got, want = out_to_f64(out), out_to_f64(clean)
+        rest = np.arange(dim) % 3 != 0
+        # the other head, and the tokens before: untouched
+        assert np.array_equal(got[:, :, :per], want[:, :, :per])
+        assert np.array_equal(got[:, :L - back, per:], want[:, :L - back, per:])
+        # where it is seen, it is seen
+        seen = got[:, L - back:, per:]
+        assert not np.isfinite(seen[..., ~rest]).any()
+        assert np.array_equal(seen[..., rest], want[:, L - back:, per:][..., rest])
