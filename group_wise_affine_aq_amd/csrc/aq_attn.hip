@@ -37,10 +37,14 @@
 //  * A weight p s goes into the second product in two fp16 parts, rounded and
 //    rest (two bf16 parts where the pages hold bf16), two products a tile.  (In
 //    one part it would be off by 2^-12 at the mean, as much as an fp16 result's
-//    own rounding: 1.1 to 1.7 times the error.)  Weights are kept 2^6 (8 bits)
-//    or 2^2 (4 bits) times too large, as far as the largest possible scale of a
-//    group allows (131008 / 255, / 15), which keeps small ones out of fp16's
-//    subnormals; l has the same factor.
+//    own rounding: 1.1 to 1.7 times the error.)  Weights are as large as fp16
+//    allows beside the scales of their tile: the exponent m that they are taken
+//    from is not the largest score but up to 30 less, so that the largest weight
+//    times the largest scale lies between 2^11 and 2^16, and down to 2^-35 of
+//    that everything counts; o, l and the biases' sums have the same factor.
+//    (With the factor that any scale allows, 2^6 at 8 bits, weights below 2^-25
+//    were lost at scales of 0.02: of thousands of tokens beside one that takes
+//    all but 2^-12 of the softmax, what they add to the result.)
 //  * bits = 16: the pages' values are the operands.
 //
 // Work division.  The tokens of all units -- a unit is one sequence, one key
@@ -74,6 +78,7 @@ typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x2v __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 32;         // tokens a wave takes at a time
 constexpr int NW = 4;             // waves of a workgroup
@@ -366,7 +371,6 @@ struct Wave {
   static constexpr int SW = (NG * 4 + 1) / 2;    // words of 4 tokens' scales
   static constexpr int NR = NT * D / 4;          // result registers
   static constexpr float UNIT = BITS == 4 ? 0x1p20f : 0x1p24f;  // 1 / what a code of 1 enters as
-  static constexpr float UP = BITS == 8 ? 6.f : (BITS == 4 ? 2.f : 0.f);
 
   struct Keys { uint32_t c[2][KW]; };
   struct Values { uint32_t c[8][NG][VW]; };
@@ -384,6 +388,7 @@ struct Wave {
   u32x4v q[NT][KS];
   float qsum[NT][NG], C[NT];
   int vis[NT];      // tokens the column sees
+  // sums of 2^(t - m) over the scores t, alone and times biases and values
   float m[NT], l[NT], bacc[NT][NG];
   f32x4v o[NT][NG][VN];
 
@@ -452,6 +457,32 @@ struct Wave {
       }
     }
   }
+  // How large, in powers of two, a weight may be: times the tile's largest
+  // scale of values it stays within fp16 (a scale of exponent field e is below
+  // 2^(e - 14); infinities and NaN count as the next field).  Scales of tokens
+  // that nobody sees do not count.  16 bits: the weight alone; bf16 needs no
+  // such care.
+  static __device__ __forceinline__ float room(const Raw &r, bool edge, int token, const bool *on,
+                                               int len, int lane) {
+    if constexpr (!QUANT) return BF ? 4.f : 15.f;
+    u16x2v most = {0, 0};
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        uint32_t w = r.w[sub][i] & 0x7FFF7FFFu;
+        if (edge) w = on[sub] && token + 16 * sub + (lane & 15) < len ? w : 0u;
+        most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2v, w));
+      }
+    int top = most[0] > most[1] ? most[0] : most[1];
+    auto larger = [](int a, int b) { return a > b ? a : b; };
+    top = larger(top, __builtin_amdgcn_update_dpp(0, top, 0x128, 0xF, 0xF, false));  // row_ror:8
+    top = larger(top, __builtin_amdgcn_update_dpp(0, top, 0x124, 0xF, 0xF, false));
+    top = larger(top, __builtin_amdgcn_update_dpp(0, top, 0x122, 0xF, 0xF, false));
+    top = larger(top, __builtin_amdgcn_update_dpp(0, top, 0x121, 0xF, 0xF, false));
+    return (float)(30 - (__builtin_amdgcn_readlane(top, 32) >> 10));  // (the lanes of V's scales)
+  }
+
   // arrays a and a + 1 for the lane's four tokens of each 16
   static __device__ __forceinline__ void take_scales(Scales &g, const char *strip, int a, int lane) {
 #pragma unroll
@@ -648,18 +679,22 @@ struct Wave {
     }
   }
 
-  // weights of the scores t against the new maximum; rescales o, l, bacc
-  __device__ __forceinline__ void weigh(float (&t)[NT][8]) {
+  // The weights 2^(t - m) of the scores t, at most 2^up each: where one would be
+  // larger, m moves up to 4 short of that, so that it seldom moves again, and
+  // what was summed is rescaled.  (Scores past 2^23 have no room for up: their
+  // weights are 1 at most.)
+  __device__ __forceinline__ void weigh(float (&t)[NT][8], float up) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float top = t[nt][0];
 #pragma unroll
       for (int j = 1; j < 8; ++j) top = __builtin_fmaxf(top, t[nt][j]);
-      top = __builtin_fmaxf(quarters_max(top), m[nt]);
-      const float base = top == kNegInf ? 0.f : top;
-      if (__ballot(top > m[nt])) {
-        const float keep = exp2_fast(m[nt] - base);
-        m[nt] = top;
+      top = quarters_max(top);
+      const bool over = top - m[nt] > up;
+      if (__ballot(over)) {
+        const float to = over ? (__builtin_fabsf(top) < 0x1p23f ? top - (up - 4.f) : top) : m[nt];
+        const float keep = exp2_fast(m[nt] - (to == kNegInf ? 0.f : to));
+        m[nt] = to;
         l[nt] *= keep;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -670,9 +705,10 @@ struct Wave {
             for (int i = 0; i < 4; ++i) o[nt][g][n][i] *= keep;
         }
       }
+      const float base = m[nt] == kNegInf ? 0.f : m[nt];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        t[nt][j] = exp2_fast(t[nt][j] - (base - UP));
+        t[nt][j] = exp2_fast(t[nt][j] - base);
         l[nt] += t[nt][j];
       }
     }
@@ -874,6 +910,7 @@ struct Wave {
           share_scales(raw, strip, lane, none);
           take_scales(g, strip, 0, lane);
         }
+        const float up = room(raw, edge, token, on, len, lane);
         scores(k, g, t);
         // after the last tile fetches of no bytes: loads without a branch let
         // the waits count only what they need
@@ -884,7 +921,7 @@ struct Wave {
         if constexpr (QUANT) load_scales(raw, from, rows);
         load_keys(k, p, rows, on_next, lane);
         if (edge) edge_scores(t, token, on, lane >> 4);
-        weigh(t);
+        weigh(t, up);
         if constexpr (QUANT) {
           take_scales(g, strip, 2, lane);
           if (edge) edge_values(g, token, on, lane >> 4);

@@ -83,3 +83,54 @@ def test_newer_values_stay_with_the_rows_that_see_them(aq, dtype, L, per, dim, w
         seen = got[:, L - back:, per:]
         assert not np.isfinite(seen[..., ~rest]).any()
         assert np.array_equal(seen[..., rest], want[:, L - back:, per:][..., rest])
+
+
+# ---- weights and scales far from one ----------------------------------------------------
+def _one_head(bits, dtype, G, dim, k, v, page=16):
+    """A cache of one sequence and one head with the rows k and v [n, dim]."""
+    n = k.shape[0]
+    cache = kv_ref.Cache(-(-n // page), 1, page, dim, G or 32, bits, dtype)
+    slots = np.arange(n)
+    for name, x in (("k", k), ("v", v)):
+        xb, xv = kv_ref.to_bits(x, dtype)
+        if bits == 16:
+            cache.parts[name][0][slots // page, 0, slots % page] = xb
+        else:
+            for part, got in zip(cache.parts[name], oracle.quantize(xv.astype(np.float32), G, bits)):
+                part[slots // page, 0, slots % page] = got
+    return cache, np.arange(-(-n // page), dtype=np.int32)[None]
+
+
+@pytest.mark.parametrize("ahead", [9, 18])
+@pytest.mark.parametrize("bits,G,dim,dtype", [(4, 32, 64, "bf16"), (8, 64, 128, "bf16"), (8, 128, 256, "bf16"),
+                                              (16, 0, 128, "f16"), (16, 0, 64, "bf16")])
+def test_many_small_weights_beside_one_large(aq, bits, G, dim, dtype, ahead):
+    """One token whose value is 0 takes nearly all of the softmax, e^18 times
+    the weight of each other: the result is what the others add."""
+    n = 2500
+    rng = np.random.default_rng(71)
+    qb, q = _queries(72, (1, 1, 4, dim), dtype)
+    k = 0.02 * rng.standard_normal((n, dim))
+    v = rng.random((n, dim))
+    q[0, 0, :] = q[0, 0, 0]  # all heads look the same way
+    qb[0, 0, :] = qb[0, 0, 0]
+    k[700] = q[0, 0, 0] * ahead / (dim ** -0.5 * (q[0, 0, 0] ** 2).sum())
+    v[700] = 0
+    cache, table = _one_head(bits, dtype, G, dim, k, v)
+    _check(_attend(aq, cache, table, [n], qb, dtype, G), q, cache, table, [n], dtype)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("size", [3e-4, 3e-3, 300.0, 6e4])
+def test_scales_of_any_size(aq, bits, size):
+    """Scales of values, given and not made by the quantizer, up to fp16's
+    largest and down among its subnormals; scores that spread over e^10."""
+    n, dim, G = 300, 128, 64
+    rng = np.random.default_rng(73)
+    qb, q = _queries(74, (1, 2, 4, dim), "bf16", 3.0)
+    cache, table = _one_head(bits, "bf16", G, dim, rng.standard_normal((n, dim)), np.ones((n, dim)))
+    codes, scales, biases = cache.parts["v"]
+    codes[:] = rng.integers(0, 1 << 32, codes.shape, dtype=np.uint32)
+    scales[:] = (size * rng.uniform(0.01, 1, scales.shape)).astype(np.float16).view(np.uint16)
+    biases[:] = (size * rng.uniform(-1, 1, biases.shape)).astype(np.float16).view(np.uint16)
+    _check(_attend(aq, cache, table, [n], qb, "bf16", G), q, cache, table, [n], "bf16")
