@@ -714,7 +714,10 @@ struct Wave {
     }
   }
 
-  // o += weights x values, the weights in two parts.  SOME: only in the columns
+  // o += weights x values, the weights in two parts.  At 16 bits the first is
+  // rounded down and the second is the least positive number at least, so that
+  // an infinite value stays what it is (0 * inf or inf - inf would be NaN; a
+  // weight not seen adds the least number times a value of 0).  SOME: only in the columns
   // that see `sees` tokens, from the halves of the values that `keep` has
   template <bool SOME = false>
   __device__ __forceinline__ void gather(const Values &v, const Scales &vs, const float (&p)[NT][8],
@@ -749,15 +752,18 @@ struct Wave {
         } else {
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
+            const float a = p[nt][j], b = p[nt][j + 1];
             if constexpr (BF) {
-              const uint32_t r = pack_bf16(p[nt][j], p[nt][j + 1]);
-              w[nt][j >> 1] = r;
-              w2[nt][j >> 1] = pack_bf16(p[nt][j] - __builtin_bit_cast(float, r << 16),
-                                         p[nt][j + 1] - __builtin_bit_cast(float, r & 0xFFFF0000u));
+              const uint32_t ua = __builtin_bit_cast(uint32_t, a), ub = __builtin_bit_cast(uint32_t, b);
+              w[nt][j >> 1] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+              const float ra = a - __builtin_bit_cast(float, ua & 0xFFFF0000u);
+              const float rb = b - __builtin_bit_cast(float, ub & 0xFFFF0000u);
+              w2[nt][j >> 1] = pack_bf16(__builtin_fmaxf(ra, 0x1p-126f), __builtin_fmaxf(rb, 0x1p-126f));
             } else {
-              const uint32_t r = pack_f16(p[nt][j], p[nt][j + 1]);
+              const uint32_t r = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
               w[nt][j >> 1] = r;
-              w2[nt][j >> 1] = pack_f16(p[nt][j] - half_at(r, 0), p[nt][j + 1] - half_at(r, 1));
+              w2[nt][j >> 1] = pack_f16(__builtin_fmaxf(a - half_at(r, 0), 0x1p-24f),
+                                        __builtin_fmaxf(b - half_at(r, 1), 0x1p-24f));
             }
           }
         }

@@ -85,6 +85,26 @@ def test_newer_values_stay_with_the_rows_that_see_them(aq, dtype, L, per, dim, w
         assert np.array_equal(seen[..., rest], want[:, L - back:, per:][..., rest])
 
 
+@pytest.mark.parametrize("dim,per,L", [(64, 4, 1), (128, 4, 1), (128, 5, 5), (256, 4, 2), (64, 9, 4)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_infinite_values(aq, dtype, dim, per, L):
+    """16-bit pages: an infinite value makes infinities of its sign in the rows
+    that see it, however its weight is rounded; both signs in one place, NaN."""
+    lengths, heads = [333, 40], 2
+    cache, table = _build(lengths, heads, dim, 0, 16, 16, dtype, seed=81)
+    qb, q = _queries(82, (2, L, per * heads, dim), dtype)
+    clean = out_to_f64(_attend(aq, cache, table, lengths, qb, dtype, 0))
+    inf = {"f16": 0x7C00, "bf16": 0x7F80}[dtype]
+    for b, t, d, bits16 in ((0, 3, 5, inf), (0, 200, 6, inf | 0x8000), (0, 332 - L, 7, inf), (1, 20, 5, inf),
+                            (0, 100, 9, inf), (0, 101, 9, inf | 0x8000)):
+        _set_value(cache, table, b, t, 0, bits16, d)
+    got = out_to_f64(_attend(aq, cache, table, lengths, qb, dtype, 0))
+    want = clean.copy()
+    want[0, :, :per, 5], want[0, :, :per, 6], want[0, :, :per, 7] = np.inf, -np.inf, np.inf
+    want[0, :, :per, 9], want[1, :, :per, 5] = np.nan, np.inf
+    assert np.array_equal(got, want, equal_nan=True)
+
+
 # ---- weights and scales far from one ----------------------------------------------------
 def _one_head(bits, dtype, G, dim, k, v, page=16):
     """A cache of one sequence and one head with the rows k and v [n, dim]."""
