@@ -618,15 +618,18 @@ struct Wave {
             }
           }
       }
-      // a group's sum, as the score of keys whose codes are all 1
-      constexpr uint32_t kOnes = BITS == 8 ? 0x00010001u : 0x00100010u;
+      // a group's sum, in the units of the scores of codes: a product with ones
+      // (not with codes of 1, whose exponent is written as 2^-14: at 8 bits the
+      // matrix cores lost all of the sum below 2^-14 of the largest query, and
+      // the biases of keys, by which it is multiplied, may be large)
+      constexpr uint32_t kOnes = 0x3C003C00u;
       const u32x4v ones = {kOnes, kOnes, kOnes, kOnes};
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         f32x4v sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < NKS; ++k) sum = mfma<BF>(ones, q[nt][g * NKS + k], sum);
-        qsum[nt][g] = sum[0];
+        qsum[nt][g] = sum[0] * (1.f / UNIT);
       }
     }
   }

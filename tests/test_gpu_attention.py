@@ -154,3 +154,18 @@ def test_scales_of_any_size(aq, bits, size):
     scales[:] = (size * rng.uniform(0.01, 1, scales.shape)).astype(np.float16).view(np.uint16)
     biases[:] = (size * rng.uniform(-1, 1, biases.shape)).astype(np.float16).view(np.uint16)
     _check(_attend(aq, cache, table, [n], qb, "bf16", G), q, cache, table, [n], "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("bits,G,dim", [(4, 64, 128), (8, 32, 64), (8, 64, 128), (8, 128, 256)])
+def test_keys_far_from_zero(aq, bits, G, dim, dtype):
+    """Keys that lie 100 to either side of zero, queries whose groups add up to
+    little: the scores are what remains when the biases' large parts cancel."""
+    n = 200
+    rng = np.random.default_rng(91)
+    x = 3 * rng.standard_normal((1, 2, 4, dim // G, G))
+    x[..., -1] = -x[..., :-1].sum(-1)
+    qb, q = kv_ref.to_bits(x.reshape(1, 2, 4, dim), dtype)
+    k = rng.standard_normal((n, dim)) + np.where(rng.random((n, dim // G)) < 0.5, 100, -100).repeat(G, 1)
+    cache, table = _one_head(bits, dtype, G, dim, k, rng.standard_normal((n, dim)))
+    _check(_attend(aq, cache, table, [n], qb, dtype, G), q, cache, table, [n], dtype)
