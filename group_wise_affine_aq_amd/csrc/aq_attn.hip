@@ -314,7 +314,7 @@ struct Line {
     for (int b = lo + 1; b < hi; ++b) idle |= clamped_length(p, b) == 0;
     chunk = p.chunk;
     uint32_t total = count(p, lane);
-    if (chunk == kTile && rows * p.B <= most) {
+    if (chunk == kTile && rows * p.B <= most && total) {  // (no chunks of no tokens)
       const uint32_t even = (total + NW * most - 1) / (NW * most) * NW;
 #pragma unroll 1
       for (uint32_t more = 0; more <= 20 && chunk == kTile; more += NW) {

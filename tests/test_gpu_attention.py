@@ -169,3 +169,28 @@ def test_keys_far_from_zero(aq, bits, G, dim, dtype):
     k = rng.standard_normal((n, dim)) + np.where(rng.random((n, dim // G)) < 0.5, 100, -100).repeat(G, 1)
     cache, table = _one_head(bits, dtype, G, dim, k, rng.standard_normal((n, dim)))
     _check(_attend(aq, cache, table, [n], qb, dtype, G), q, cache, table, [n], dtype)
+
+
+# ---- no tokens at all -------------------------------------------------------------------
+@pytest.mark.parametrize("B", [1, 3, 70, 300])
+@pytest.mark.parametrize("pages", [4, 40])  # up to 128 tokens, and more
+@pytest.mark.parametrize("per,dim,bits,G", [(4, 64, 8, 32), (16, 256, 4, 64), (4, 128, 16, 0)])
+def test_every_sequence_empty(aq, per, dim, bits, G, pages, B):
+    """As a graph is captured before any token is there: zero rows, and the
+    workspace serves the next call, with tables joined either way."""
+    import torch
+    cache = kv_ref.Cache(8, 1, 32, dim, G or 32, bits, "f16")
+    cache.poison()
+    table = torch.full((B, pages), -1, dtype=torch.int32, device="cuda")
+    lengths = torch.zeros(B, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    parts = cache.device()
+    for L in (1, 5):
+        q = torch.ones((B, L, per, dim), dtype=torch.float16, device="cuda")
+        out = torch.full_like(q, 7.0)
+        aq.aq_paged_attention(q, *parts, table, lengths, G, bits, out=out, workspace=ws)
+        assert not out.any()
+    full = [700, 0, 31]
+    cache, table = _build(full, 1, dim, G, bits, 32, "f16", seed=95)
+    qb, q = _queries(96, (3, 1, per, dim), "f16")
+    _check(_attend(aq, cache, table, full, qb, "f16", G, workspace=ws), q, cache, table, full, "f16")
