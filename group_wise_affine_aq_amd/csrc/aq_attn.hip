@@ -604,9 +604,11 @@ struct Wave {
         }
         top = quarters_max(top);
         int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
-        e = e < -100 ? -100 : (e > 100 ? 100 : e);
+        e = e < -100 ? -100 : (e > 127 ? 127 : e);
         const float down = __builtin_ldexpf(1.f, 8 - e);
-        C[nt] = __builtin_ldexpf(log2s * UNIT, e - 8);
+        // (a factor past binary32's range may be any smaller one: scores that
+        // differ at all are then more than 2^20 apart either way)
+        C[nt] = __builtin_amdgcn_fmed3f(__builtin_ldexpf(log2s * UNIT, e - 8), -0x1p127f, 0x1p127f);
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll

@@ -194,3 +194,24 @@ def test_every_sequence_empty(aq, per, dim, bits, G, pages, B):
     cache, table = _build(full, 1, dim, G, bits, 32, "f16", seed=95)
     qb, q = _queries(96, (3, 1, per, dim), "f16")
     _check(_attend(aq, cache, table, full, qb, "f16", G, workspace=ws), q, cache, table, full, "f16")
+
+
+# ---- queries of any size ----------------------------------------------------------------
+@pytest.mark.parametrize("size", [1e8, 1e28, 3e33, 1e36])
+@pytest.mark.parametrize("per", [4, 20])
+@pytest.mark.parametrize("bits,G", [(4, 32), (8, 64), (16, 0)])
+def test_large_queries(aq, bits, G, per, size):
+    """bf16 queries far past fp16's range, scores within binary32's: one token
+    takes all.  In every other head ordinary queries."""
+    n, dim = 200, 128
+    rng = np.random.default_rng(97)
+    x = rng.standard_normal((1, 1, per, dim))
+    x[:, :, ::2] *= size
+    qb, q = kv_ref.to_bits(x, "bf16")
+    cache, table = _one_head(bits, "bf16", G, dim, rng.standard_normal((n, dim)), rng.standard_normal((n, dim)))
+    got = out_to_f64(_attend(aq, cache, table, [n], qb, "bf16", G))
+    ref, slack = kv_ref.attention_rows(q, cache, table, [n], dim ** -0.5)
+    # (the formula's weights of 0 and 1 leave no room for errors of the scores)
+    slack[:, :, ::2] = 2.0 ** -14 * np.linalg.norm(ref[:, :, ::2], axis=-1)
+    assert np.isfinite(got).all()
+    assert kv_ref.rows_off(got, ref, slack, "bf16") <= 1
