@@ -17,6 +17,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 __all__ = [
     "AQError", "lib_path", "load_library", "aq_status_string", "aq_version", "aq_codes_words",
@@ -53,6 +54,8 @@ class _KVCache(ctypes.Structure):
                 + [(n, ctypes.c_int32) for n in ("page_size", "kv_heads", "head_dim", "group_size",
                                                  "bits", "dtype")])
 
+
+_pack_kv_cache = struct.Struct("@6Pq6i").pack  # (a third of the time that the structure takes)
 
 _lib = None
 
@@ -519,42 +522,43 @@ def _rows(t, name):
     return t.data_ptr(), (stride if n > 1 else h * d)
 
 
-def _array(t, dtype, count, name):
-    """Device address of a contiguous array of `count` elements (None: any number)."""
+def _array(t, dtype, shape, name):
+    """Device address of a contiguous array of that shape (None: any)."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, {dtype} expected")
     if not (t.is_cuda and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous device tensor")
-    if count is not None and t.numel() != count:
-        raise ValueError(f"{name}: {t.numel()} elements, {count} expected")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} expected")
     return t.data_ptr()
 
 
 def _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits):
+    """(the bytes of a _KVCache, kv_heads, head_dim)"""
     torch = _torch()
-    pages, heads, page, words = k_codes.shape
-    rows = pages * heads * page
+    codes = k_codes.shape
+    pages, heads, page, words = codes
     if bits == 16:
         code = _dtype_code(k_codes)
         if code == AQ_F32:
             raise TypeError("a 16-bit cache holds float16 or bfloat16")
-        kind, count = k_codes.dtype, rows * words
-        return _KVCache(_array(k_codes, kind, count, "k_codes"), None, None,
-                        _array(v_codes, kind, count, "v_codes"), None, None,
-                        pages, page, heads, words, 0, 16, code)
+        kind = k_codes.dtype
+        return _pack_kv_cache(_array(k_codes, kind, None, "k_codes"), 0, 0,
+                              _array(v_codes, kind, codes, "v_codes"), 0, 0,
+                              pages, page, heads, words, 0, 16, code), heads, words
     if bits != 4 and bits != 8:
         raise AQError(-2 if 2 <= bits <= 8 else -1, "aq_kv_cache")
     dim = words * 32 // bits
     if group_size < 1 or dim % group_size or k_scales is None or v_scales is None:
         raise AQError(-1, "aq_kv_cache")
-    word, half, count, groups = torch.int32, torch.float16, rows * words, rows * (dim // group_size)
-    return _KVCache(_array(k_codes, word, count, "k_codes"),
-                    _array(k_scales, half, groups, "k_scales"),
-                    None if k_biases is None else _array(k_biases, half, groups, "k_biases"),
-                    _array(v_codes, word, count, "v_codes"),
-                    _array(v_scales, half, groups, "v_scales"),
-                    None if v_biases is None else _array(v_biases, half, groups, "v_biases"),
-                    pages, page, heads, dim, group_size, bits, 0)
+    word, half, groups = torch.int32, torch.float16, (pages, heads, page, dim // group_size)
+    return _pack_kv_cache(_array(k_codes, word, None, "k_codes"),
+                          _array(k_scales, half, groups, "k_scales"),
+                          0 if k_biases is None else _array(k_biases, half, groups, "k_biases"),
+                          _array(v_codes, word, codes, "v_codes"),
+                          _array(v_scales, half, groups, "v_scales"),
+                          0 if v_biases is None else _array(v_biases, half, groups, "v_biases"),
+                          pages, page, heads, dim, group_size, bits, 0), heads, dim
 
 
 def aq_kv_append(k, v, slots, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases,
@@ -562,15 +566,16 @@ def aq_kv_append(k, v, slots, k_codes, k_scales, k_biases, v_codes, v_scales, v_
     """Quantize k, v [T, kv_heads, head_dim] (fp16/bf16; tokens may be strided) into the cache at
     slots int64 [T] = page * page_size + place (outside the cache: not written)."""
     lib = load_library()
-    cache = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
+    cache, heads, dim = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases,
+                                  group_size, bits)
     T = slots.numel()
-    shape = (T, cache.kv_heads, cache.head_dim)
+    shape = (T, heads, dim)
     if k.shape != shape or v.shape != shape or k.dtype is not v.dtype:
         raise ValueError(f"aq_kv_append: k and v must be {shape} of one dtype")
     kp, ks = _rows(k, "k")
     vp, vs = _rows(v, "v")
     st = lib.aq_kv_append(kp, vp, _dtype_code(k), T, ks, vs,
-                          _array(slots, _torch_module.int64, None, "slots"), ctypes.byref(cache),
+                          _array(slots, _torch_module.int64, None, "slots"), cache,
                           _queue(stream, slots))
     if st != AQ_OK:
         raise AQError(st, "aq_kv_append")
@@ -581,9 +586,10 @@ def aq_kv_read(slots, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, 
     """Rows of the cache at slots int64 [T] -> (k, v) [T, kv_heads, head_dim] in out_dtype
     (default fp16); a slot outside the cache gives zeros."""
     lib = load_library()
-    cache = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
+    cache, H, D = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size,
+                            bits)
     torch = _torch_module
-    T, H, D = slots.numel(), cache.kv_heads, cache.head_dim
+    T = slots.numel()
     if k is None and v is None:
         with _its(stream):
             k = torch.empty((T, H, D), dtype=out_dtype or torch.float16, device=slots.device)
@@ -599,7 +605,7 @@ def aq_kv_read(slots, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, 
         if k.shape != (T, H, D) or v.shape != (T, H, D):
             raise ValueError(f"aq_kv_read: k and v must be {(T, H, D)}")
         kp, vp = _array(k, k.dtype, None, "k"), _array(v, k.dtype, None, "v")
-    st = lib.aq_kv_read(_array(slots, torch.int64, None, "slots"), T, ctypes.byref(cache), kp, vp,
+    st = lib.aq_kv_read(_array(slots, torch.int64, None, "slots"), T, cache, kp, vp,
                         _dtype_code(k), _queue(stream, slots))
     if st != AQ_OK:
         raise AQError(st, "aq_kv_read")
@@ -625,7 +631,8 @@ def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_bias
     aq_paged_attention_workspace bytes, zeroed once before its first use; without one each call
     makes and clears its own."""
     lib = load_library()
-    cache = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
+    cache, heads, dim = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases,
+                                  group_size, bits)
     torch = _torch_module
     shape, strides = q.shape, q.stride()
     if len(shape) == 3:
@@ -639,15 +646,15 @@ def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_bias
             step = outer
         elif B > 1 and outer != L * step:
             raise ValueError("q: all tokens must lie at one distance")
-    if D != cache.head_dim:
-        raise ValueError(f"q: head_dim {D}, the cache has {cache.head_dim}")
+    if D != dim:
+        raise ValueError(f"q: head_dim {D}, the cache has {dim}")
     if last != 1 or (Hq > 1 and inner != D) or not q.is_cuda:
         raise ValueError("q: a device tensor, heads and head_dim contiguous")
     if B * L == 1:
         step = Hq * D
     rows, max_pages = page_table.shape
-    if rows != B:
-        raise ValueError(f"page_table must be [{B}, max_pages]")
+    if rows != B or lengths.numel() != B:
+        raise ValueError(f"page_table must be [{B}, max_pages], lengths [{B}]")
     if out is None:
         with _its(stream):
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -657,13 +664,13 @@ def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_bias
             raise ValueError("out must have q's shape and dtype")
         op = _array(out, q.dtype, None, "out")
     if workspace is None:
-        need = lib.aq_paged_attention_workspace(B, L, Hq, cache.kv_heads, D)
+        need = lib.aq_paged_attention_workspace(B, L, Hq, heads, D)
         with _its(stream):
             workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
     int32 = torch.int32
-    st = lib.aq_paged_attention(q.data_ptr(), _dtype_code(q), B, L, Hq, step, ctypes.byref(cache),
+    st = lib.aq_paged_attention(q.data_ptr(), _dtype_code(q), B, L, Hq, step, cache,
                                 _array(page_table, int32, None, "page_table"), max_pages,
-                                _array(lengths, int32, B, "lengths"),
+                                _array(lengths, int32, None, "lengths"),
                                 D ** -0.5 if scale is None else scale, op,
                                 _array(workspace, workspace.dtype, None, "workspace"),
                                 workspace.nbytes, _queue(stream, q))

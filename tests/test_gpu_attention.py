@@ -215,3 +215,21 @@ def test_large_queries(aq, bits, G, per, size):
     slack[:, :, ::2] = 2.0 ** -14 * np.linalg.norm(ref[:, :, ::2], axis=-1)
     assert np.isfinite(got).all()
     assert kv_ref.rows_off(got, ref, slack, "bf16") <= 1
+
+
+# ---- arguments --------------------------------------------------------------------------
+@pytest.mark.parametrize("bits", [8, 16])
+def test_arrays_of_one_cache_have_its_shape(aq, bits):
+    """As many elements in another shape are another cache's."""
+    import torch
+    parts = kv_ref.Cache(4, 2, 16, 64, 32, bits).device()
+    slots = torch.zeros(1, dtype=torch.int64, device="cuda")
+    aq.aq_kv_read(slots, *parts, 32, bits)
+    for i, t in enumerate(parts):
+        if t is not None:
+            pages, heads, page, last = t.shape
+            for other in ((heads, pages, page, last), (pages * heads, 1, page, last), (pages, heads, page * last)):
+                wrong = list(parts)
+                wrong[i] = t.view(other)
+                with pytest.raises(ValueError):
+                    aq.aq_kv_read(slots, *wrong, 32, bits)
