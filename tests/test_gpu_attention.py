@@ -8,7 +8,7 @@ import pytest
 import kv_ref
 import oracle
 from gpu_util import out_to_f64
-from test_gpu_kv import _attend, _build, _dev16, aq  # noqa: F401  (aq: the module's fixture)
+from test_gpu_kv import CASES, LONG, _attend, _build, aq  # noqa: F401  (aq: the module's fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -233,3 +233,24 @@ def test_arrays_of_one_cache_have_its_shape(aq, bits):
                 wrong[i] = t.view(other)
                 with pytest.raises(ValueError):
                     aq.aq_kv_read(slots, *wrong, 32, bits)
+
+
+# ---- every form, within bounds that refuse other results --------------------------------
+# bits, head size, group size, rows a key head (query heads, new tokens): one tile of
+# columns, two, several slices
+FORMS = [(bits, dim, G, per, L) for bits in (4, 8) for dim in (64, 128, 256) for G in (32, 64, 128)
+         if G <= dim for per, L in ((3, 1), (5, 5))]
+FORMS += [(16, dim, 0, per, L) for dim in (64, 128, 256) for per, L in ((3, 1), (5, 5))]
+FORMS += [(8, 128, 128, 9, 8), (4, 64, 32, 33, 2), (8, 256, 128, 2, 8), (16, 128, 0, 9, 8)]
+FORM_LENGTHS = [1, 31, 33, 129, 0, 400, 16]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("bits,dim,G,per,L", FORMS)
+def test_every_form(aq, bits, dim, G, per, L, dtype):
+    _compare(aq, FORM_LENGTHS, per, 2, dim, G, bits, 32, L, dtype, seed=dim + L)
+
+
+@pytest.mark.parametrize("lengths,per,heads,dim,G,bits,page,L,dtype", CASES + LONG)
+def test_rows_of_long_and_short_sequences(aq, lengths, per, heads, dim, G, bits, page, L, dtype):
+    _compare(aq, lengths, per, heads, dim, G, bits, page, L, dtype)
