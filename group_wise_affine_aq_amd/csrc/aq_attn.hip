@@ -60,8 +60,8 @@
 //
 // Bound: HBM, the codes, scales and biases read once.  At 8 bits a tile of 32
 // tokens x 128 values (groups of 64, one tile of query rows) is 8.7 KB and
-// costs a wave about 250 vector and 24 matrix instructions (4 bits: 4.6 KB,
-// 290); eight waves a CU could take 35 bytes a clock at that rate where HBM
+// costs a wave about 245 vector and 24 matrix instructions (4 bits: 4.6 KB,
+// 320); eight waves a CU could take 35 bytes a clock at that rate where HBM
 // gives a CU about 9.  64 sequences of up to 16384 tokens (1.01 GB) take 187
 // us, 5.4 TB/s; a large copy reaches 5.2, a large read 6.3.  Below about 100 MB
 // what surrounds the stream shows: lengths, page ids and first codes are three
@@ -369,7 +369,6 @@ struct Wave {
   static constexpr int VB = VN * BITS / 8;       // bytes
   static constexpr int VW = VB < 4 ? 1 : VB / 4; // words
   static constexpr int SW = (NG * 4 + 1) / 2;    // words of 4 tokens' scales
-  static constexpr int NR = NT * D / 4;          // result registers
   static constexpr float UNIT = BITS == 4 ? 0x1p20f : 0x1p24f;  // 1 / what a code of 1 enters as
 
   struct Keys { uint32_t c[2][KW]; };
@@ -1303,8 +1302,9 @@ __global__ __launch_bounds__(64 * JW) void attn_join_kernel(Params p, int nt) {
 // of the second workgroup on a CU; 59 as four waves with a tile of rows each on
 // the same tokens, too few tokens are then under way.  The second slice's one
 // tile of 8 rows computed as one, not two: no faster, 46.4 against 45.3.)
-// Heads of 256 have one tile a wave: with two the state does not fit the
-// registers (up to 236 of them in scratch memory at 8 bits).
+// Heads of 256 have one tile a wave: with two the state does not fit the 512
+// registers that a wave can have (8 bits: 40 to 275 of them in scratch memory,
+// with the groups of a row; 16 bits 587).
 constexpr int most_tiles(int D) { return D > 128 ? 1 : 2; }
 void tiles_for(int64_t cols, int D, int &nt, int &slices) {
   const int64_t tiles = (cols + 15) / 16;
@@ -1313,7 +1313,8 @@ void tiles_for(int64_t cols, int D, int &nt, int &slices) {
 }
 
 // Workgroups per CU the kernel is built for: what its registers allow (a lane's
-// scales and biases grow with the groups of a row).  Two where three could be
+// scales and biases grow with the groups of a row), heads of 64 but for 9 to 15
+// registers in scratch memory.  Two where three could be
 // built with fewer loads under way: 16 sequences of up to 4096 tokens, 8 bits,
 // 23.9 against 26.4 us at one step; 16 bits 54 against 60.
 // Heads of 64, quantized, three: 32 sequences of up to 8192 tokens, 4 bits 41.8

@@ -445,9 +445,13 @@ aq_status aq_kv_read(const int64_t *slots, int64_t T, const aq_kv_cache *cache, 
  * q: device, x_dtype AQ_F16 or AQ_BF16 (bits = 16: the cache's dtype), rows
  * [q_heads, head_dim] contiguous, token b*L + i at q + (b*L + i) * q_stride
  * elements (a multiple of 8, at least q_heads * head_dim).  out: device [B, L,
- * q_heads, head_dim] in x_dtype.  page_table: device int32 [B, max_pages].
- * lengths: device int32 [B].  q_heads a multiple of kv_heads.  Scores and
- * softmax statistics are held in binary32.  NULL bias arrays: every bias +0.
+ * q_heads, head_dim] in x_dtype, no part of q's memory.  page_table: device
+ * int32 [B, max_pages].  lengths: device int32 [B].  q_heads a multiple of
+ * kv_heads.  Scores and softmax statistics are held in binary32.  NULL bias
+ * arrays: every bias +0.  Scales may be any finite fp16; one that is infinite
+ * counts as NaN, and so may an infinite bias (aq_kv_append writes neither).
+ * A value of a 16-bit page that is infinite or NaN is what the formula makes
+ * of it in the rows that see its token, and nothing to the others.
  *
  * workspace: device memory of aq_paged_attention_workspace bytes, 16-byte
  * aligned, zeroed once before its first use; every call leaves it fit for the
