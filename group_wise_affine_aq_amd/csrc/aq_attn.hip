@@ -62,11 +62,13 @@
 // tokens x 128 values (groups of 64, one tile of query rows) is 8.7 KB and
 // costs a wave about 245 vector and 24 matrix instructions (4 bits: 4.6 KB,
 // 320); eight waves a CU could take 35 bytes a clock at that rate where HBM
-// gives a CU about 9.  64 sequences of up to 16384 tokens (1.01 GB) take 187
-// us, 5.4 TB/s; a large copy reaches 5.2, a large read 6.3.  Below about 100 MB
+// gives a CU about 9.  64 sequences of up to 16384 tokens (1.01 GB) take 185
+// to 190 us, 5.4 TB/s; a large copy reaches 5.2, a large read 6.3.  Below about 100 MB
 // what surrounds the stream shows: lengths, page ids and first codes are three
 // loads that wait for each other (5 us to the first score), and joining pieces
-// is three more (5 us): 16 sequences of up to 4096 tokens (71 MB) 20.5 us.
+// is three more (5 us): 16 sequences of up to 4096 tokens (71 MB) 19.0 us.
+// (Figures in pairs, here and below, compare two variants at the step at which
+// one was taken, not this code with one.)
 #include "aq_device.hpp"
 #include "aq_internal.hpp"
 
