@@ -1,5 +1,5 @@
 """The compiled kernels: nothing that works lane by lane stands between the end
-of a branch that only some lanes of a wave took and the instruction that turns
+of a branch or loop that only some lanes of a wave took and the instruction that turns
 the others on again.  The compiler has placed copies of live registers there
 (v_accvgpr_write, under register pressure); the lanes that were off lose what
 was copied, thread numbers and addresses among it."""
@@ -27,6 +27,9 @@ def misplaced(lines):
     for i, line in enumerate(lines):
         if "s_cbranch_execz" in line:
             ends.append((kernel, re.search(r"s_cbranch_execz\s+(\.?L\w+)", line).group(1)))
+        elif "s_cbranch_execnz" in line:  # what follows runs when no lane goes back
+            labels[kernel, i] = i
+            ends.append((kernel, i))
         elif line and line[0] in "<.L_":
             name = re.match(r"<?(\.?\w+)>?:", line)
             if name and name.group(1).startswith("_Z"):
@@ -67,6 +70,19 @@ _Z6kernel:
     assert misplaced((text % "v_accvgpr_write_b32 a167, v167").split("\n")) == [
         ("_Z6kernel", ".LBB0_2", ["v_accvgpr_write_b32 a167, v167"])]
     assert not misplaced((text % "s_mov_b32 s97, s5").split("\n"))
+    text = """
+_Z6kernel:
+.LBB0_1:                                ; Loop
+	v_cmp_gt_i32_e32 vcc, 4, v1
+	s_andn2_b64 exec, exec, vcc
+	s_cbranch_execnz .LBB0_1
+	%s
+	s_or_b64 exec, exec, s[2:3]
+	s_endpgm
+"""
+    assert [x[2] for x in misplaced((text % "v_mov_b32_e32 v1, v2").split("\n"))] == [
+        ["v_mov_b32_e32 v1, v2"]]
+    assert not misplaced((text % "s_nop 0").split("\n"))
 
 
 @pytest.mark.skipif(OBJDUMP is None, reason="no llvm-objdump")
