@@ -26,6 +26,8 @@ __all__ = [
     "aq_quantized_matmul", "aq_gather_qmv", "aq_gather_qmm", "aq_gather_quantized_matmul",
     "aq_quantize_fp", "aq_dequantize_fp", "aq_qmv_fp", "aq_matmul_fp", "aq_gather_matmul_fp", "aq_qmv_fp_describe",
     "FP_MODES", "aq_kv_append", "aq_kv_read", "aq_paged_attention", "aq_paged_attention_workspace",
+    "aq_paged_attention_masked", "aq_prompt_attention", "aq_prompt_attention_workspace", "aq_rope",
+    "aq_rope_append", "aq_rope_frequencies", "ROPE_STRETCHES", "aq_kv_weigh", "aq_kv_evict",
 ]
 
 AQ_OK = 0
@@ -103,6 +105,19 @@ def load_library():
         "aq_paged_attention": ([vp, i32, i64, i32, i32, i64, vp, vp, i64, vp, ctypes.c_float, vp,
                                 vp, i64, vp], i32),
         "aq_paged_attention_workspace": ([i64, i32, i32, i32, i32], i64),
+        "aq_paged_attention_masked": ([vp, i32, i64, i32, i32, i64, vp, vp, i64, vp, ctypes.c_float,
+                                       vp, vp, vp, i64, vp], i32),
+        "aq_prompt_attention": ([vp, i32, i64, i32, i64, vp, i64, vp, i64, i64, i32, i32, i64, vp, vp,
+                                 ctypes.c_float, vp, vp, vp, i64, vp], i32),
+        "aq_prompt_attention_workspace": ([i64, i64, i64, i32, i32, i32], i64),
+        "aq_rope": ([vp, i64, i32, vp, i64, i32, i32, i64, i32, vp, vp, i64, vp, i64, vp], i32),
+        "aq_rope_append": ([vp, i64, i32, vp, i64, vp, i64, i32, i64, vp, vp, vp, vp, i64, vp, i64, vp],
+                           i32),
+        "aq_rope_frequencies": ([i32] + [ctypes.c_double] + [i32] + [ctypes.c_double] * 4 + [vp, vp],
+                                i32),
+        "aq_kv_weigh": ([vp, i32, i64, i32, i32, i64, vp, vp, i64, vp, ctypes.c_float, vp, vp, i64, vp],
+                        i32),
+        "aq_kv_evict": ([vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, vp, vp, vp, vp], i32),
         "aq_bench_stream_read": ([vp, i64, i32, i32, vp, vp], i32),
         "aq_bench_read_oneshot": ([vp, i64, i32, i32, vp, vp], i32),
         "aq_bench_mfma_clock": ([i32, i32, vp, vp], i32),
@@ -621,19 +636,8 @@ def aq_paged_attention_workspace(B: int, L: int, q_heads: int, kv_heads: int,
     return n
 
 
-def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, page_table,
-                       lengths, group_size: int, bits: int, scale: float | None = None, out=None,
-                       workspace=None, stream=None):
-    """Attention of the newest L tokens of every sequence over the paged cache: q [B, L, q_heads,
-    head_dim] or [B, q_heads, head_dim] (L = 1; tokens may be strided), page_table int32 [B,
-    max_pages], lengths int32 [B] (cached tokens, the L new ones included) -> out of q's shape.
-    scale: default head_dim ** -0.5.  workspace: a device buffer of
-    aq_paged_attention_workspace bytes, zeroed once before its first use; without one each call
-    makes and clears its own."""
-    lib = load_library()
-    cache, heads, dim = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases,
-                                  group_size, bits)
-    torch = _torch_module
+def _new_tokens(q, dim):
+    """B, L, q_heads, head_dim of the newest tokens' queries, and the tokens' distance in elements."""
     shape, strides = q.shape, q.stride()
     if len(shape) == 3:
         B, Hq, D = shape
@@ -652,6 +656,23 @@ def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_bias
         raise ValueError("q: a device tensor, heads and head_dim contiguous")
     if B * L == 1:
         step = Hq * D
+    return B, L, Hq, D, step
+
+
+def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, page_table,
+                       lengths, group_size: int, bits: int, scale: float | None = None, out=None,
+                       workspace=None, stream=None):
+    """Attention of the newest L tokens of every sequence over the paged cache: q [B, L, q_heads,
+    head_dim] or [B, q_heads, head_dim] (L = 1; tokens may be strided), page_table int32 [B,
+    max_pages], lengths int32 [B] (cached tokens, the L new ones included) -> out of q's shape.
+    scale: default head_dim ** -0.5.  workspace: a device buffer of
+    aq_paged_attention_workspace bytes, zeroed once before its first use; without one each call
+    makes and clears its own."""
+    lib = load_library()
+    cache, heads, dim = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases,
+                                  group_size, bits)
+    torch = _torch_module
+    shape, (B, L, Hq, D, step) = q.shape, _new_tokens(q, dim)
     rows, max_pages = page_table.shape
     if rows != B or lengths.numel() != B:
         raise ValueError(f"page_table must be [{B}, max_pages], lengths [{B}]")
@@ -677,3 +698,264 @@ def aq_paged_attention(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_bias
     if st != AQ_OK:
         raise AQError(st, "aq_paged_attention")
     return out
+
+
+# ---- attention with capped, biased and masked scores ------------------------------------
+_pack_scores = struct.Struct("@fi4P").pack  # aq_attention_scores
+_pack_rotation = struct.Struct("@2P2id").pack  # aq_rotation
+
+
+def _scores(softcap, window, slopes, heads, first, firsts, prefix, prefixes, lse, rows):
+    """The bytes of an aq_attention_scores."""
+    torch = _torch_module
+    if window < 0 or window > 0x7FFFFFFF:
+        raise AQError(-1, "window")
+    return _pack_scores(
+        softcap, window,
+        0 if slopes is None else _array(slopes, torch.float32, (heads,), "slopes"),
+        0 if first is None else _array(first, torch.int32, (firsts,), "first"),
+        0 if prefix is None else _array(prefix, torch.int32, (prefixes,), "prefix"),
+        0 if lse is None else _array(lse, torch.float32, rows, "lse"))
+
+
+def aq_paged_attention_masked(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, page_table,
+                              lengths, group_size: int, bits: int, scale: float | None = None,
+                              softcap: float = 0.0, slopes=None, window: int = 0, first=None, out=None,
+                              lse=None, return_lse: bool = False, workspace=None, stream=None):
+    """aq_paged_attention whose scores are capped (softcap * tanh(s / softcap)), biased by distance
+    (slopes fp32 [q_heads]: s - slope * distance) and masked (window: only that many tokens up to the
+    row's own; first int32 [B]: none before it).  lse fp32 of q's shape without head_dim gets the
+    logarithm of each row's sum of weights.  -> out, or (out, lse) with return_lse."""
+    lib = load_library()
+    cache, heads, dim = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases,
+                                  group_size, bits)
+    torch = _torch_module
+    shape, (B, L, Hq, D, step) = q.shape, _new_tokens(q, dim)
+    rows, max_pages = page_table.shape
+    if rows != B or lengths.numel() != B:
+        raise ValueError(f"page_table must be [{B}, max_pages], lengths [{B}]")
+    with _its(stream):
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        elif out.shape != shape:
+            raise ValueError("out must have q's shape and dtype")
+        if lse is None and return_lse:
+            lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+        if workspace is None:
+            need = lib.aq_paged_attention_workspace(B, L, Hq, heads, D)
+            workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
+    int32 = torch.int32
+    st = lib.aq_paged_attention_masked(
+        q.data_ptr(), _dtype_code(q), B, L, Hq, step, cache,
+        _array(page_table, int32, None, "page_table"), max_pages,
+        _array(lengths, int32, None, "lengths"), D ** -0.5 if scale is None else scale,
+        _scores(softcap, window, slopes, Hq, first, B, None, 0, lse, shape[:-1]),
+        _array(out, q.dtype, None, "out"), _array(workspace, workspace.dtype, None, "workspace"),
+        workspace.nbytes, _queue(stream, q))
+    if st != AQ_OK:
+        raise AQError(st, "aq_paged_attention_masked")
+    return (out, lse) if return_lse else out
+
+
+def aq_prompt_attention_workspace(Tq: int, Tk: int, B: int, q_heads: int, kv_heads: int,
+                                  head_dim: int) -> int:
+    """Bytes of workspace aq_prompt_attention needs for this shape."""
+    n = int(load_library().aq_prompt_attention_workspace(Tq, Tk, B, q_heads, kv_heads, head_dim))
+    if n < 0:
+        raise AQError(-1, "aq_prompt_attention_workspace")
+    return n
+
+
+def aq_prompt_attention(q, k, v, q_starts, k_starts, scale: float | None = None, softcap: float = 0.0,
+                        slopes=None, window: int = 0, first=None, prefix=None, out=None, lse=None,
+                        return_lse: bool = False, workspace=None, stream=None):
+    """Attention of whole prompts: q [Tq, q_heads, head_dim] over k, v [Tk, kv_heads, head_dim]
+    (fp16/bf16, tokens may be strided).  Sequence b has the rows q_starts[b] .. q_starts[b + 1] - 1 of
+    q and k_starts[b] .. k_starts[b + 1] - 1 of k and v (int32 [B + 1]); its queries are its last
+    tokens.  softcap, slopes, window as in aq_paged_attention_masked; first int32 [Tq]: what a row's
+    document begins with; prefix int32 [B]: as many of a sequence's tokens are seen by all of its
+    rows.  lse fp32 [Tq, q_heads].  workspace: a device buffer of aq_prompt_attention_workspace bytes;
+    without one each call makes its own.  -> out, or (out, lse) with return_lse."""
+    lib = load_library()
+    torch = _torch()
+    Tq, Hq, D = q.shape
+    Tk, Hk, _ = k.shape
+    B = q_starts.numel() - 1
+    if k.shape != v.shape or k.shape[2] != D or not q.dtype is k.dtype is v.dtype:
+        raise ValueError("q, k and v must be [tokens, heads, head_dim] of one dtype and head_dim")
+    if k_starts.numel() != B + 1:
+        raise ValueError("q_starts and k_starts must be [B + 1]")
+    qp, qs = _rows(q, "q")
+    kp, ks = _rows(k, "k")
+    vp, vs = _rows(v, "v")
+    with _its(stream):
+        if out is None:
+            out = torch.empty((Tq, Hq, D), dtype=q.dtype, device=q.device)
+        elif out.shape != q.shape:
+            raise ValueError("out must have q's shape and dtype")
+        if lse is None and return_lse:
+            lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            need = lib.aq_prompt_attention_workspace(Tq, Tk, B, Hq, Hk, D)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    int32 = torch.int32
+    st = lib.aq_prompt_attention(
+        qp, _dtype_code(q), Tq, Hq, qs, kp, ks, vp, vs, Tk, Hk, D, B,
+        _array(q_starts, int32, None, "q_starts"), _array(k_starts, int32, None, "k_starts"),
+        D ** -0.5 if scale is None else scale,
+        _scores(softcap, window, slopes, Hq, first, Tq, prefix, B, lse, (Tq, Hq)),
+        _array(out, q.dtype, None, "out"), _array(workspace, workspace.dtype, None, "workspace"),
+        workspace.nbytes, _queue(stream, q))
+    if st != AQ_OK:
+        raise AQError(st, "aq_prompt_attention")
+    return (out, lse) if return_lse else out
+
+
+# ---- rotary positions -------------------------------------------------------------------
+ROPE_STRETCHES = {"plain": 0, "linear": 1, "base": 2, "by_index": 3, "by_turns": 4}
+
+
+def aq_rope_frequencies(rotary: int, base: float = 10000.0, kind: str = "plain", stretch: float = 1.0,
+                        ctx: float = 0.0, low: float = 0.0, high: float = 0.0, device="cuda"):
+    """(frequencies fp32 [rotary / 2] on the device, factor) for aq_rope: base ** (-2 i / rotary),
+    changed for contexts `stretch` times the trained one, ctx, as `kind` says (include/aq.h)."""
+    torch = _torch()
+    freqs, factor = torch.empty(max(rotary, 0) // 2, dtype=torch.float32), ctypes.c_float()
+    st = load_library().aq_rope_frequencies(rotary, base, ROPE_STRETCHES[kind], stretch, ctx, low, high,
+                                            freqs.data_ptr(), ctypes.byref(factor))
+    _check(st, "aq_rope_frequencies")
+    return freqs.to(device), factor.value
+
+
+def _rotation(positions, freqs, T, interleaved, factor):
+    """The bytes of an aq_rotation."""
+    torch = _torch_module
+    return _pack_rotation(_array(positions, torch.int32, (T,), "positions"),
+                          _array(freqs, torch.float32, None, "freqs"), 2 * freqs.numel(),
+                          bool(interleaved), factor)
+
+
+def _turned(out, like, name, stream):
+    """out or a new tensor for like's rows, its address and its tokens' distance."""
+    if out is None:
+        with _its(stream):
+            out = _torch_module.empty(like.shape, dtype=like.dtype, device=like.device)
+    elif out.shape != like.shape or out.dtype is not like.dtype:
+        raise ValueError(f"{name} must have the shape and dtype of what is turned")
+    return (out, *_rows(out, name))
+
+
+def aq_rope(q, k, positions, freqs, interleaved: bool = False, factor: float = 1.0, q_out=None,
+            k_out=None, stream=None):
+    """Rotary positions of q [T, q_heads, head_dim] and k [T, kv_heads, head_dim] (fp16/bf16, tokens may
+    be strided; one of them may be None): the first 2 * len(freqs) values of every head are turned by
+    the angles positions[t] * freqs[i], as pairs i, len(freqs) + i or (interleaved) 2 i, 2 i + 1, and
+    scaled by factor.  q_out may be q, k_out k.  -> (q, k) turned."""
+    lib = load_library()
+    _torch()
+    if q is None and k is None:
+        raise ValueError("aq_rope: nothing to turn")
+    some = k if q is None else q
+    T, _, D = some.shape
+    if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != D or k.dtype is not q.dtype):
+        raise ValueError("aq_rope: q and k must be [T, heads, head_dim] of one dtype")
+    qp = qs = qo = qos = kp = ks = ko = kos = Hq = Hk = 0
+    if q is not None:
+        Hq, (qp, qs), (q_out, qo, qos) = q.shape[1], _rows(q, "q"), _turned(q_out, q, "q_out", stream)
+    if k is not None:
+        Hk, (kp, ks), (k_out, ko, kos) = k.shape[1], _rows(k, "k"), _turned(k_out, k, "k_out", stream)
+    st = lib.aq_rope(qp, qs, Hq, kp, ks, Hk, _dtype_code(some), T, D,
+                     _rotation(positions, freqs, T, interleaved, factor), qo, qos, ko, kos,
+                     _queue(stream, some))
+    if st != AQ_OK:
+        raise AQError(st, "aq_rope")
+    return q_out if q is not None else None, k_out if k is not None else None
+
+
+def aq_rope_append(q, k, v, positions, freqs, slots, k_codes, k_scales, k_biases, v_codes, v_scales,
+                   v_biases, group_size: int, bits: int, interleaved: bool = False, factor: float = 1.0,
+                   q_out=None, k_out=None, stream=None):
+    """aq_rope and aq_kv_append in one launch: q [T, q_heads, head_dim] turned (None: no queries), k
+    turned and written with v [T, kv_heads, head_dim] into the cache at slots int64 [T].  k_out: a
+    tensor that gets the turned keys too.  -> q turned."""
+    lib = load_library()
+    cache, heads, dim = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases,
+                                  group_size, bits)
+    T = slots.numel()
+    shape = (T, heads, dim)
+    if k.shape != shape or v.shape != shape or k.dtype is not v.dtype:
+        raise ValueError(f"aq_rope_append: k and v must be {shape} of one dtype")
+    kp, ks = _rows(k, "k")
+    vp, vs = _rows(v, "v")
+    qp = qs = qo = qos = ko = kos = Hq = 0
+    if q is not None:
+        if q.shape[0] != T or q.shape[2] != dim or q.dtype is not k.dtype:
+            raise ValueError(f"aq_rope_append: q must be [{T}, q_heads, {dim}] of k's dtype")
+        Hq, (qp, qs), (q_out, qo, qos) = q.shape[1], _rows(q, "q"), _turned(q_out, q, "q_out", stream)
+    if k_out is not None:
+        k_out, ko, kos = _turned(k_out, k, "k_out", stream)
+    st = lib.aq_rope_append(qp, qs, Hq, kp, ks, vp, vs, _dtype_code(k), T,
+                            _rotation(positions, freqs, T, interleaved, factor),
+                            _array(slots, _torch_module.int64, None, "slots"), cache, qo, qos, ko, kos,
+                            _queue(stream, slots))
+    if st != AQ_OK:
+        raise AQError(st, "aq_rope_append")
+    return q_out if q is not None else None
+
+
+# ---- keeping a cache within a budget ----------------------------------------------------
+def aq_kv_weigh(q, lse, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, page_table, lengths,
+                weights, group_size: int, bits: int, scale: float | None = None, softcap: float = 0.0,
+                slopes=None, window: int = 0, first=None, stream=None):
+    """Adds to weights (fp32 [B, tokens]) what each cached token gets of the attention of q, [B, L,
+    q_heads, head_dim] or [B, q_heads, head_dim]: the sum over rows and heads of exp(score - lse), lse
+    and the other arguments those of aq_paged_attention_masked for the same queries."""
+    lib = load_library()
+    cache, _, dim = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
+    torch = _torch_module
+    B, L, Hq, D, step = _new_tokens(q, dim)
+    rows, max_pages = page_table.shape
+    if rows != B or lengths.numel() != B or weights.dim() != 2 or weights.shape[0] != B:
+        raise ValueError(f"page_table must be [{B}, max_pages], lengths [{B}], weights [{B}, tokens]")
+    if lse is None:
+        raise ValueError("aq_kv_weigh needs the attention's lse")
+    int32 = torch.int32
+    st = lib.aq_kv_weigh(q.data_ptr(), _dtype_code(q), B, L, Hq, step, cache,
+                         _array(page_table, int32, None, "page_table"), max_pages,
+                         _array(lengths, int32, None, "lengths"), D ** -0.5 if scale is None else scale,
+                         _scores(softcap, window, slopes, Hq, first, B, None, 0, lse, q.shape[:-1]),
+                         _array(weights, torch.float32, None, "weights"), weights.shape[1],
+                         _queue(stream, q))
+    if st != AQ_OK:
+        raise AQError(st, "aq_kv_weigh")
+
+
+def aq_kv_evict(weights, lengths, page_table, new_table, k_codes, k_scales, k_biases, v_codes, v_scales,
+                v_biases, group_size: int, bits: int, keep: int, sinks: int = 0, recent: int = 0,
+                new_lengths=None, stream=None):
+    """Every sequence back to at most `keep` tokens: its first `sinks`, its last `recent` and those
+    between with the largest weights (fp32 [B, tokens]), in their order, copied to the pages of
+    new_table (int32 [B, pages], other pages than page_table's) -> (kept int32 [B, keep]: the
+    positions they had, -1 behind the last; new lengths int32 [B]; their weights fp32 [B, keep])."""
+    lib = load_library()
+    cache, _, _ = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
+    torch = _torch_module
+    int32, B = torch.int32, lengths.numel()
+    if weights.dim() != 2 or not B == weights.shape[0] == page_table.shape[0] == new_table.shape[0]:
+        raise ValueError(f"weights, page_table and new_table must have a row for each of {B} sequences")
+    if keep < 1:
+        raise AQError(-1, "aq_kv_evict")
+    with _its(stream):
+        kept = torch.empty((B, keep), dtype=int32, device=weights.device)
+        got = torch.empty((B, keep), dtype=torch.float32, device=weights.device)
+        if new_lengths is None:
+            new_lengths = torch.empty(B, dtype=int32, device=weights.device)
+    st = lib.aq_kv_evict(_array(weights, torch.float32, None, "weights"), weights.shape[1],
+                         _array(lengths, int32, None, "lengths"), B,
+                         _array(page_table, int32, None, "page_table"), page_table.shape[1],
+                         _array(new_table, int32, None, "new_table"), new_table.shape[1], cache, keep,
+                         sinks, recent, kept.data_ptr(), got.data_ptr(),
+                         _array(new_lengths, int32, (B,), "new_lengths"), _queue(stream, weights))
+    if st != AQ_OK:
+        raise AQError(st, "aq_kv_evict")
+    return kept, new_lengths, got

@@ -22,7 +22,8 @@ LIB = os.path.join(HERE, "libaq.so")
 ARCH = os.environ.get("AQ_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["aq_api.cpp", "aq_quant.hip", "aq_qmv.hip", "aq_qmvm.hip", "aq_qmm.hip", "aq_fp.hip",
-           "aq_kv.hip", "aq_attn.hip", "aq_bench.hip"]
+           "aq_kv.hip", "aq_attn.hip", "aq_attn_masked.hip", "aq_weigh.hip", "aq_rope.hip", "aq_evict.hip",
+           "aq_prompt.hip", "aq_bench.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CFLAGS = [

@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
 #include <cstdio>
 
 #include "aq.h"
@@ -102,6 +103,53 @@ aq_status check_attention_shape(int64_t B, int L, int q_heads, int kv_heads, int
       B * L * q_heads >= (1 << 24))
     return AQ_ERR_UNSUPPORTED;
   return AQ_OK;
+}
+
+// how scores become weights; `prefix`: whether the call takes one
+aq_status check_scores(const aq_attention_scores *x, bool prefix) {
+  if (!x) return AQ_ERR_INVALID_ARG;
+  if (!(x->softcap == 0.f || (x->softcap >= 1e-30f && x->softcap <= 1e30f)) || x->window < 0 ||
+      (x->prefix && !prefix))
+    return AQ_ERR_INVALID_ARG;
+  if (!aligned16(x->slopes) || !aligned16(x->first) || !aligned16(x->prefix) || !aligned16(x->lse))
+    return AQ_ERR_ALIGNMENT;
+  return AQ_OK;
+}
+
+// queries, their cache and its pages, as the calls on new tokens take them
+aq_status check_new_tokens(const void *q, int x_dtype, int64_t B, int L, int q_heads, int64_t q_stride,
+                           const aq_kv_cache *cache, const int32_t *page_table, int64_t max_pages,
+                           const int32_t *lengths) {
+  aq_status st = check_cache(cache);
+  if (st != AQ_OK) return st;
+  if (!valid_act_dtype(x_dtype) || max_pages < 1) return AQ_ERR_INVALID_ARG;
+  if (cache->bits == 16 && x_dtype != cache->dtype) return AQ_ERR_INVALID_ARG;
+  st = check_attention_shape(B, L, q_heads, cache->kv_heads, cache->head_dim);
+  if (st != AQ_OK) return st;
+  if (q_stride < (int64_t)q_heads * cache->head_dim || q_stride % 8 != 0)
+    return AQ_ERR_INVALID_ARG;
+  if (q_stride > ((int64_t)1 << 62) / (B * L)) return AQ_ERR_UNSUPPORTED;
+  if (max_pages > 0x7FFFFF00 / cache->page_size) return AQ_ERR_UNSUPPORTED;
+  st = check_cache_arrays(cache, false);
+  if (st != AQ_OK) return st;
+  if (!q || !page_table || !lengths) return AQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(page_table) || !aligned16(lengths)) return AQ_ERR_ALIGNMENT;
+  return AQ_OK;
+}
+
+// 16-bit rows of `heads` heads, strides in elements
+aq_status check_rows(int64_t T, int heads, int head_dim, int64_t stride) {
+  if (stride < (int64_t)heads * head_dim || stride % 8 != 0) return AQ_ERR_INVALID_ARG;
+  if (T > 0 && stride > ((int64_t)1 << 62) / T) return AQ_ERR_UNSUPPORTED;
+  return AQ_OK;
+}
+
+bool valid_head_dim(int d) { return d == 64 || d == 128 || d == 256; }
+
+aq_status check_rotation(const aq_rotation *r, int head_dim) {
+  if (!r || r->rotary < 1 || r->rotary > head_dim || !(r->factor - r->factor == 0.0))
+    return AQ_ERR_INVALID_ARG;
+  return r->rotary % 16 == 0 ? AQ_OK : AQ_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -491,28 +539,257 @@ aq_status aq_paged_attention(const void *q, aq_dtype x_dtype, int64_t B, int L, 
                              int64_t q_stride, const aq_kv_cache *cache, const int32_t *page_table,
                              int64_t max_pages, const int32_t *lengths, float scale, void *out,
                              void *workspace, int64_t workspace_bytes, void *stream) {
-  aq_status st = check_cache(cache);
+  aq_status st = check_new_tokens(q, (int)x_dtype, B, L, q_heads, q_stride, cache, page_table,
+                                  max_pages, lengths);
   if (st != AQ_OK) return st;
-  if (!valid_act_dtype(x_dtype) || max_pages < 1) return AQ_ERR_INVALID_ARG;
-  if (cache->bits == 16 && (int)x_dtype != cache->dtype) return AQ_ERR_INVALID_ARG;
-  st = check_attention_shape(B, L, q_heads, cache->kv_heads, cache->head_dim);
-  if (st != AQ_OK) return st;
-  if (q_stride < (int64_t)q_heads * cache->head_dim || q_stride % 8 != 0)
-    return AQ_ERR_INVALID_ARG;
-  if (q_stride > ((int64_t)1 << 62) / (B * L)) return AQ_ERR_UNSUPPORTED;
-  if (max_pages > 0x7FFFFF00 / cache->page_size) return AQ_ERR_UNSUPPORTED;
-  st = check_cache_arrays(cache, false);
-  if (st != AQ_OK) return st;
-  if (!q || !page_table || !lengths || !out || !workspace) return AQ_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(page_table) || !aligned16(lengths) || !aligned16(out) ||
-      !aligned16(workspace))
-    return AQ_ERR_ALIGNMENT;
+  if (!out || !workspace) return AQ_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(workspace)) return AQ_ERR_ALIGNMENT;
   if (workspace_bytes <
       aq::attn_workspace_bytes(B, L, q_heads, cache->kv_heads, cache->head_dim))
     return AQ_ERR_INVALID_ARG;
   const aq::AttnArgs a = {q,     q_stride,     page_table, lengths, out,    workspace,
-                          max_pages, scale, (int)x_dtype, (int)B,     L,       q_heads};
+                          max_pages, scale, (int)x_dtype, (int)B,     L,       q_heads, {}};
   return from_hip(aq::launch_paged_attention(a, *cache, static_cast<hipStream_t>(stream)));
+}
+
+aq_status aq_paged_attention_masked(const void *q, aq_dtype x_dtype, int64_t B, int L, int q_heads,
+                                    int64_t q_stride, const aq_kv_cache *cache,
+                                    const int32_t *page_table, int64_t max_pages,
+                                    const int32_t *lengths, float scale,
+                                    const aq_attention_scores *scores, void *out, void *workspace,
+                                    int64_t workspace_bytes, void *stream) {
+  aq_status st = check_new_tokens(q, (int)x_dtype, B, L, q_heads, q_stride, cache, page_table,
+                                  max_pages, lengths);
+  if (st != AQ_OK) return st;
+  st = check_scores(scores, false);
+  if (st != AQ_OK) return st;
+  if (!out || !workspace) return AQ_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(workspace)) return AQ_ERR_ALIGNMENT;
+  if (workspace_bytes <
+      aq::attn_workspace_bytes(B, L, q_heads, cache->kv_heads, cache->head_dim))
+    return AQ_ERR_INVALID_ARG;
+  const aq::AttnArgs a = {q,     q_stride,     page_table, lengths, out,    workspace,
+                          max_pages, scale, (int)x_dtype, (int)B,     L,       q_heads, *scores};
+  return from_hip(
+      aq::launch_paged_attention_masked(a, *cache, static_cast<hipStream_t>(stream)));
+}
+
+static aq_status check_prompt_shape(int64_t Tq, int64_t Tk, int64_t B, int q_heads, int kv_heads,
+                                    int head_dim) {
+  if (Tq < 0 || Tk < 0 || B < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0)
+    return AQ_ERR_INVALID_ARG;
+  if (!valid_head_dim(head_dim)) return AQ_ERR_UNSUPPORTED;
+  const int64_t most = 1 << 24;
+  if (B >= most || Tq >= most || Tk >= most || q_heads >= most || Tq * q_heads >= most ||
+      Tk * kv_heads >= most || B * kv_heads >= most)
+    return AQ_ERR_UNSUPPORTED;
+  return AQ_OK;
+}
+
+int64_t aq_prompt_attention_workspace(int64_t Tq, int64_t Tk, int64_t B, int q_heads, int kv_heads,
+                                      int head_dim) {
+  if (check_prompt_shape(Tq, Tk, B, q_heads, kv_heads, head_dim) != AQ_OK) return -1;
+  return aq::prompt_workspace_bytes(Tq, Tk, B, q_heads, kv_heads, head_dim);
+}
+
+aq_status aq_prompt_attention(const void *q, aq_dtype x_dtype, int64_t Tq, int q_heads,
+                              int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                              int64_t v_stride, int64_t Tk, int kv_heads, int head_dim, int64_t B,
+                              const int32_t *q_starts, const int32_t *k_starts, float scale,
+                              const aq_attention_scores *scores, void *out, void *workspace,
+                              int64_t workspace_bytes, void *stream) {
+  if (!valid_act_dtype(x_dtype)) return AQ_ERR_INVALID_ARG;
+  aq_status st = check_prompt_shape(Tq, Tk, B, q_heads, kv_heads, head_dim);
+  if (st != AQ_OK) return st;
+  st = check_rows(Tq, q_heads, head_dim, q_stride);
+  if (st == AQ_OK) st = check_rows(Tk, kv_heads, head_dim, k_stride);
+  if (st == AQ_OK) st = check_rows(Tk, kv_heads, head_dim, v_stride);
+  if (st == AQ_OK) st = check_scores(scores, true);
+  if (st != AQ_OK) return st;
+  // (a tile of keys is addressed with 32-bit offsets)
+  if (k_stride > 1 << 23 || v_stride > 1 << 23) return AQ_ERR_UNSUPPORTED;
+  if (Tq == 0) return AQ_OK;
+  if (!q || !out || !q_starts || !k_starts || !workspace || (Tk > 0 && (!k || !v)))
+    return AQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(q_starts) ||
+      !aligned16(k_starts) || !aligned16(workspace))
+    return AQ_ERR_ALIGNMENT;
+  if (workspace_bytes < aq::prompt_workspace_bytes(Tq, Tk, B, q_heads, kv_heads, head_dim))
+    return AQ_ERR_INVALID_ARG;
+  aq::PromptArgs a = {};
+  a.q = static_cast<const uint16_t *>(q);
+  a.k = static_cast<const uint16_t *>(k);
+  a.v = static_cast<const uint16_t *>(v);
+  a.out = static_cast<uint16_t *>(out);
+  a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+  a.Tq = Tq, a.Tk = Tk;
+  a.q_starts = q_starts, a.k_starts = k_starts;
+  a.workspace = workspace;
+  a.scale = scale;
+  a.x_dtype = (int)x_dtype, a.B = (int)B;
+  a.q_heads = q_heads, a.kv_heads = kv_heads, a.head_dim = head_dim;
+  a.scores = *scores;
+  return from_hip(aq::launch_prompt_attention(a, static_cast<hipStream_t>(stream)));
+}
+
+// ---- rotary positions ------------------------------------------------------------------
+
+// the arguments both calls share; `k` only: its place in a cache is checked apart
+static aq_status rope_args(aq::RopeArgs &a, const void *q, int64_t q_stride, int q_heads,
+                           const void *k, int64_t k_stride, int kv_heads, aq_dtype x_dtype,
+                           int64_t T, int head_dim, const aq_rotation *r, void *q_out,
+                           int64_t q_out_stride, void *k_out, int64_t k_out_stride, bool need_k_out) {
+  if (!valid_act_dtype(x_dtype) || T < 0 || q_heads < 0 || kv_heads < 0) return AQ_ERR_INVALID_ARG;
+  if (!valid_head_dim(head_dim)) return head_dim < 1 ? AQ_ERR_INVALID_ARG : AQ_ERR_UNSUPPORTED;
+  aq_status st = check_rotation(r, head_dim);
+  if (st == AQ_OK && q_heads) st = check_rows(T, q_heads, head_dim, q_stride);
+  if (st == AQ_OK && q_heads) st = check_rows(T, q_heads, head_dim, q_out_stride);
+  if (st == AQ_OK && kv_heads) st = check_rows(T, kv_heads, head_dim, k_stride);
+  if (st == AQ_OK && kv_heads && (need_k_out || k_out))
+    st = check_rows(T, kv_heads, head_dim, k_out_stride);
+  if (st != AQ_OK) return st;
+  // (the grid: a workgroup per token at most)
+  if (T > 0x7FFFFFF0) return AQ_ERR_UNSUPPORTED;
+  if (T == 0) return AQ_OK;
+  if (!r->positions || !r->freqs || (q_heads && (!q || !q_out)) ||
+      (kv_heads && (!k || (need_k_out && !k_out))))
+    return AQ_ERR_INVALID_ARG;
+  if (!aligned16(r->positions) || !aligned16(r->freqs) || !aligned16(q) || !aligned16(q_out) ||
+      !aligned16(k) || !aligned16(k_out))
+    return AQ_ERR_ALIGNMENT;
+  a = {};
+  a.q = static_cast<const uint16_t *>(q);
+  a.k = static_cast<const uint16_t *>(k);
+  a.q_out = static_cast<uint16_t *>(q_out);
+  a.k_out = static_cast<uint16_t *>(k_out);
+  a.q_stride = q_stride, a.k_stride = k_stride;
+  a.q_out_stride = q_out_stride, a.k_out_stride = k_out_stride;
+  a.T = T;
+  a.positions = r->positions, a.freqs = r->freqs;
+  a.factor = r->factor;
+  a.q_heads = q_heads, a.kv_heads = kv_heads, a.head_dim = head_dim;
+  a.rotary = r->rotary, a.interleaved = r->interleaved != 0;
+  a.x_dtype = (int)x_dtype;
+  return AQ_OK;
+}
+
+aq_status aq_rope(const void *q, int64_t q_stride, int q_heads, const void *k, int64_t k_stride,
+                  int kv_heads, aq_dtype x_dtype, int64_t T, int head_dim,
+                  const aq_rotation *rotation, void *q_out, int64_t q_out_stride, void *k_out,
+                  int64_t k_out_stride, void *stream) {
+  aq::RopeArgs a;
+  const aq_status st = rope_args(a, q, q_stride, q_heads, k, k_stride, kv_heads, x_dtype, T, head_dim,
+                                 rotation, q_out, q_out_stride, k_out, k_out_stride, true);
+  if (st != AQ_OK || T == 0 || (q_heads == 0 && kv_heads == 0)) return st;
+  return from_hip(aq::launch_rope(a, nullptr, static_cast<hipStream_t>(stream)));
+}
+
+aq_status aq_rope_append(const void *q, int64_t q_stride, int q_heads, const void *k,
+                         int64_t k_stride, const void *v, int64_t v_stride, aq_dtype x_dtype,
+                         int64_t T, const aq_rotation *rotation, const int64_t *slots,
+                         const aq_kv_cache *cache, void *q_out, int64_t q_out_stride, void *k_out,
+                         int64_t k_out_stride, void *stream) {
+  aq_status st = check_cache(cache);
+  if (st != AQ_OK) return st;
+  if (cache->bits == 16 && (int)x_dtype != cache->dtype) return AQ_ERR_INVALID_ARG;
+  st = check_cache_arrays(cache, true);
+  if (st != AQ_OK) return st;
+  aq::RopeArgs a;
+  st = rope_args(a, q, q_stride, q_heads, k, k_stride, cache->kv_heads, x_dtype, T, cache->head_dim,
+                 rotation, q_out, q_out_stride, k_out, k_out_stride, false);
+  if (st == AQ_OK) st = check_rows(T, cache->kv_heads, cache->head_dim, v_stride);
+  if (st != AQ_OK || T == 0) return st;
+  if (!v || !slots) return AQ_ERR_INVALID_ARG;
+  if (!aligned16(v) || !aligned16(slots)) return AQ_ERR_ALIGNMENT;
+  a.v = static_cast<const uint16_t *>(v);
+  a.v_stride = v_stride;
+  a.slots = slots;
+  return from_hip(aq::launch_rope(a, cache, static_cast<hipStream_t>(stream)));
+}
+
+aq_status aq_rope_frequencies(int rotary, double base, aq_rope_stretch kind, double stretch,
+                              double ctx, double low, double high, float *freqs, float *factor) {
+  const double pi = 3.14159265358979323846;
+  const bool blend = kind == AQ_ROPE_BY_INDEX || kind == AQ_ROPE_BY_TURNS;
+  if (!freqs || rotary < 4 || rotary % 2 != 0 || !(base > 1.0) || !std::isfinite(base))
+    return AQ_ERR_INVALID_ARG;
+  if (kind < AQ_ROPE_PLAIN || kind > AQ_ROPE_BY_TURNS) return AQ_ERR_INVALID_ARG;
+  if (kind != AQ_ROPE_PLAIN && !(stretch >= 1.0 && std::isfinite(stretch))) return AQ_ERR_INVALID_ARG;
+  if (blend && !(ctx >= 1.0 && std::isfinite(ctx) && low > 0.0 && low < high && std::isfinite(high)))
+    return AQ_ERR_INVALID_ARG;
+  if (kind == AQ_ROPE_BASE) base *= std::pow(stretch, (double)rotary / (rotary - 2));
+  double a = 0.0, b = 1.0;
+  if (kind == AQ_ROPE_BY_INDEX) {
+    auto index = [&](double turns) { return rotary * std::log(ctx / (2 * pi * turns)) / (2 * std::log(base)); };
+    a = std::fmax(std::floor(index(high)), 0.0);
+    b = std::fmin(std::ceil(index(low)), rotary - 1.0);
+  }
+  for (int i = 0; i < rotary / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / rotary);
+    double slow = 0.0;  // how much of f / stretch
+    if (kind == AQ_ROPE_LINEAR) slow = 1.0;
+    if (kind == AQ_ROPE_BY_INDEX) slow = std::fmin(std::fmax((i - a) / std::fmax(b - a, 0.001), 0.0), 1.0);
+    if (kind == AQ_ROPE_BY_TURNS)
+      slow = 1.0 - std::fmin(std::fmax((ctx * f / (2 * pi) - low) / (high - low), 0.0), 1.0);
+    freqs[i] = (float)(slow > 0.0 ? slow * (f / stretch) + (1.0 - slow) * f : f);
+  }
+  if (factor)
+    *factor = kind == AQ_ROPE_BY_INDEX && stretch > 1.0 ? (float)(0.1 * std::log(stretch) + 1.0) : 1.f;
+  return AQ_OK;
+}
+
+// ---- keeping a cache within a budget ---------------------------------------------------
+
+aq_status aq_kv_weigh(const void *q, aq_dtype x_dtype, int64_t B, int L, int q_heads,
+                      int64_t q_stride, const aq_kv_cache *cache, const int32_t *page_table,
+                      int64_t max_pages, const int32_t *lengths, float scale,
+                      const aq_attention_scores *scores, float *weights, int64_t weights_stride,
+                      void *stream) {
+  aq_status st = check_new_tokens(q, (int)x_dtype, B, L, q_heads, q_stride, cache, page_table,
+                                  max_pages, lengths);
+  if (st != AQ_OK) return st;
+  st = check_scores(scores, false);
+  if (st != AQ_OK) return st;
+  if (!scores->lse || !weights || weights_stride < 1 || weights_stride % 4 != 0)
+    return AQ_ERR_INVALID_ARG;
+  if (!aligned16(weights)) return AQ_ERR_ALIGNMENT;
+  // (128 tokens at a time, counted in 32 bits)
+  if (weights_stride > ((int64_t)1 << 62) / B || (max_pages * cache->page_size / 128 + 1) * B > 0x7FFFFFFF)
+    return AQ_ERR_UNSUPPORTED;
+  const aq::AttnArgs a = {q,     q_stride,     page_table, lengths, nullptr, nullptr,
+                          max_pages, scale, (int)x_dtype, (int)B,     L,       q_heads, *scores};
+  return from_hip(
+      aq::launch_kv_weigh(a, *cache, weights, weights_stride, static_cast<hipStream_t>(stream)));
+}
+
+aq_status aq_kv_evict(const float *weights, int64_t weights_stride, const int32_t *lengths,
+                      int64_t B, const int32_t *page_table, int64_t max_pages,
+                      const int32_t *new_table, int64_t new_max_pages, const aq_kv_cache *cache,
+                      int64_t keep, int64_t sinks, int64_t recent, int32_t *kept,
+                      float *new_weights, int32_t *new_lengths, void *stream) {
+  aq_status st = check_cache(cache);
+  if (st != AQ_OK) return st;
+  if (B < 1 || max_pages < 1 || new_max_pages < 1 || weights_stride < 1 || keep < 1 || sinks < 0 ||
+      recent < 0 || sinks > keep || recent > keep - sinks)
+    return AQ_ERR_INVALID_ARG;
+  const int64_t most = (int64_t)1 << 30;
+  if (B >= (1 << 24) || keep > most || B * keep >= 2 * most || weights_stride > most ||
+      max_pages > 0x7FFFFF00 / cache->page_size || new_max_pages > 0x7FFFFF00 / cache->page_size ||
+      (keep / 64 + 1) * B > 0x7FFFFFFF / cache->kv_heads)
+    return AQ_ERR_UNSUPPORTED;
+  if (keep > new_max_pages * cache->page_size) return AQ_ERR_INVALID_ARG;
+  st = check_cache_arrays(cache, false);
+  if (st != AQ_OK) return st;
+  if (!weights || !lengths || !page_table || !new_table || !kept || !new_weights || !new_lengths)
+    return AQ_ERR_INVALID_ARG;
+  if (!aligned16(weights) || !aligned16(lengths) || !aligned16(page_table) || !aligned16(new_table) ||
+      !aligned16(kept) || !aligned16(new_weights) || !aligned16(new_lengths))
+    return AQ_ERR_ALIGNMENT;
+  const aq::EvictArgs a = {weights,     weights_stride, lengths, page_table,
+                           new_table,   max_pages,      new_max_pages,
+                           kept,        new_weights,    new_lengths,
+                           (int)B,      (int)keep,      (int)sinks, (int)recent};
+  return from_hip(aq::launch_kv_evict(a, *cache, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

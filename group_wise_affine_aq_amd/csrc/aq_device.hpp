@@ -90,6 +90,15 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
+// the natural logarithm of l 2^m, l >= 0 (0: -inf).  l's exponent joins m first:
+// m lies several powers of two below the largest score, l as many above 1, and
+// log2 l by itself would have the rounding of their size, not of the result's.
+__device__ __forceinline__ float log_scaled(float m, float l) {
+  const float whole = m + (float)__builtin_amdgcn_frexp_expf(l);
+  const float r = (whole + __builtin_log2f(__builtin_amdgcn_frexp_mantf(l))) * 0.693147180559945309f;
+  return l == 0.f ? -__builtin_inff() : r;
+}
+
 }  // namespace aq
 
 namespace aq {

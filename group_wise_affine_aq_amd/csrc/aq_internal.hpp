@@ -113,6 +113,7 @@ hipError_t launch_kv_append(const void *k, const void *v, int x_dtype, int64_t T
                             hipStream_t s);
 hipError_t launch_kv_read(const int64_t *slots, int64_t T, const KvCache &c, void *k, void *v,
                           int out_dtype, hipStream_t s);
+using Scores = aq_attention_scores;
 struct AttnArgs {
   const void *q;
   int64_t q_stride;
@@ -124,8 +125,55 @@ struct AttnArgs {
   float scale;
   int x_dtype;
   int B, L, q_heads;
+  Scores scores;
 };
 int64_t attn_workspace_bytes(int64_t B, int L, int q_heads, int kv_heads, int head_dim);
 hipError_t launch_paged_attention(const AttnArgs &a, const KvCache &c, hipStream_t s);
+hipError_t launch_paged_attention_masked(const AttnArgs &a, const KvCache &c, hipStream_t s);
+
+// rotary positions: queries and keys turned; with a cache keys and values are
+// written into it as aq_kv_append does
+struct RopeArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t *q_out, *k_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride, T;
+  const int32_t *positions;
+  const float *freqs;
+  const int64_t *slots;
+  double factor;
+  int q_heads, kv_heads, head_dim, rotary, interleaved, x_dtype;
+};
+hipError_t launch_rope(const RopeArgs &a, const KvCache *c, hipStream_t s);
+
+// what each cached token gathers of new tokens' attention (a.scores.lse is read)
+hipError_t launch_kv_weigh(const AttnArgs &a, const KvCache &c, float *weights, int64_t stride,
+                           hipStream_t s);
+
+// the tokens of each sequence that gathered most, moved to other pages
+struct EvictArgs {
+  const float *weights;
+  int64_t stride;
+  const int32_t *lengths, *table, *new_table;
+  int64_t max_pages, new_max_pages;
+  int32_t *kept;
+  float *new_weights;
+  int32_t *new_lengths;
+  int B, keep, sinks, recent;
+};
+hipError_t launch_kv_evict(const EvictArgs &a, const KvCache &c, hipStream_t s);
+
+// attention of whole prompts over 16-bit rows
+struct PromptArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t *out;
+  int64_t q_stride, k_stride, v_stride, Tq, Tk;
+  const int32_t *q_starts, *k_starts;
+  void *workspace;
+  float scale;
+  int x_dtype, B, q_heads, kv_heads, head_dim;
+  Scores scores;
+};
+int64_t prompt_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int q_heads, int kv_heads, int head_dim);
+hipError_t launch_prompt_attention(const PromptArgs &a, hipStream_t s);
 
 }  // namespace aq

@@ -1,0 +1,576 @@
+// aq_prompt.hip -- attention of whole prompts over 16-bit rows of keys and
+// values (gfx950).
+//
+//   out = sum_t p_t v_t,  p = softmax_t(score(q . k_t))
+//
+// in one pass over the keys with the running maximum and sum of the softmax.
+//
+// The query rows of one key head and sequence -- its tokens times the heads of
+// the group, token by token -- are cut into tiles of 32 NW; a workgroup of NW
+// waves takes one, 32 rows a wave, and walks over the keys that any of them
+// sees, KT at a time.  Keys and values of a tile go through LDS once and serve
+// all waves; while they are worked on, the next tile's are on their way to
+// registers and are then written to the other half of LDS: one barrier a tile.
+//
+// Matrix layout (v_mfma_f32_32x32x16).  S^T = K q^T: a lane has one row of
+// queries (lane % 32) and, with h = lane / 32, the tokens 8 i + 4 h .. + 3 of
+// each 32.  So a row's maximum and sum stay in two lanes, and the 16 tokens of
+// one k-step of the second product, O^T = V^T p^T, are taken in the order in
+// which the lanes hold them: weights are rounded and packed where they are.  V
+// enters as columns by transposing reads of LDS (4 tokens x 16 values each).
+// 16-byte pieces of a row lie in LDS at their number xor the row's, keys and
+// values in different ways, so that neither read meets a bank twice.
+//
+// Weights are 2^(t - m): m is not the largest score but up to kUp less, so
+// that the largest weight lies near 2^kUp, fp16's range below it serves the
+// small ones (2^-39 of the largest), and m, which only moves when a weight
+// would pass 2^kUp, seldom does; then everything summed is rescaled.
+//
+// Values that are not finite: 0 * inf is NaN, and a row that does not see a
+// token must not see its value.  A thread that brings values to LDS looks at
+// them; the products of a tile that holds an infinity or a NaN are made of its
+// finite values, and what is not finite is counted, by sign, with a product of
+// ones over the tokens that the row sees.
+#include "aq_device.hpp"
+#include "aq_internal.hpp"
+
+namespace aq {
+namespace {
+
+typedef _Float16 f16x8v __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
+typedef float f32x16v __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
+typedef short s16x4v __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4v lds_s16x4;
+typedef __attribute__((address_space(3))) u32x4v lds_u32x4;
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __amdgpu_buffer_rsrc_t Span;
+
+constexpr float kNegInf = -__builtin_inff();
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kUp = 15.f;  // 2^15 is within fp16's range
+constexpr int kMaxParts = 64;
+
+struct Params {
+  PromptArgs a;
+  float C;         // |scale| log2 e
+  uint32_t flip;   // sign of the scale, for pairs of queries
+  float cap2, inv_cap2;
+  int window, group;
+  int tiles;       // of query rows, at most, of all sequences
+  int parts;       // of every tile's keys
+  float *piece;    // parts > 1: per tile, head and part: rows of D results, then m and l
+};
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float as_float(uint32_t u) { return __builtin_bit_cast(float, u); }
+
+// the value of lane ^ 32
+__device__ __forceinline__ float other_half(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t x = r[0], y = r[1];
+  return as_float(threadIdx.x & 32 ? x : y);
+}
+
+template <bool BF>
+__device__ __forceinline__ f32x16v mfma(u32x4v a, u32x4v b, f32x16v c) {
+  if constexpr (BF)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8v, a), __builtin_bit_cast(bf16x8v, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8v, a), __builtin_bit_cast(f16x8v, b), c, 0, 0, 0);
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  if constexpr (BF)
+    return __builtin_bit_cast(uint32_t, bf16x2v{(__bf16)a, (__bf16)b});
+  else
+    return __builtin_bit_cast(uint32_t, half2v{(_Float16)a, (_Float16)b});
+}
+
+// rows of one sequence: first and number, of queries and of keys
+struct Sequence { int q0, n, k0, len; };
+__device__ __forceinline__ Sequence sequence(const PromptArgs &a, int b) {
+  auto clamp = [](int x, int lo, int64_t hi) { return x < lo ? lo : (x > hi ? (int)hi : x); };
+  Sequence s;
+  s.q0 = clamp(a.q_starts[b], 0, a.Tq);
+  s.n = clamp(a.q_starts[b + 1], s.q0, a.Tq) - s.q0;
+  s.k0 = clamp(a.k_starts[b], 0, a.Tk);
+  s.len = clamp(a.k_starts[b + 1], s.k0, a.Tk) - s.k0;
+  return s;
+}
+
+// The tile `at` of all sequences' tiles of R rows -> its sequence, and its number there,
+// the last tiles, which see the most keys, first.  False past the last.
+template <int R>
+__device__ __forceinline__ bool find_tile(const PromptArgs &a, int group, int at, int &b, int &tile) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    const int mine = b0 + lane < a.B ? (sequence(a, b0 + lane).n * group + R - 1) / R : 0;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int x = __shfl_up(upto, d);
+      upto += lane >= d ? x : 0;
+    }
+    const uint64_t past = __ballot(at < before + upto);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      b = uniform(b0 + l);
+      const int own = __builtin_amdgcn_readlane(mine, l);
+      tile = uniform(own - 1 - (at - before - (__builtin_amdgcn_readlane(upto, l) - own)));
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return false;
+}
+
+// a piece: results of R rows, then their m, then their l
+template <int D>
+constexpr int piece_floats(int R) { return R * (D + 2); }
+
+template <bool BF, int D, int NW>
+struct Shape {
+  static constexpr int R = 32 * NW, THREADS = 64 * NW;
+  static constexpr int KT = D > 128 ? 32 : 64;  // keys of a tile
+  static constexpr int X = KT / 32, KK = KT / 16;
+  static constexpr int CH = D / 8;            // 16-byte pieces of a row
+  static constexpr int RB = D * 2;            // bytes of a row
+  static constexpr int EACH = KT * CH / THREADS;  // pieces a thread brings of each
+  static constexpr int KS = D / 16, DB = D / 32;
+  static constexpr int TILE = KT * RB;        // bytes of keys, or values
+  static constexpr int LDS = 4 * TILE;
+  static __device__ __forceinline__ int key_piece(int row, int c) { return row * RB + (c ^ (row & (CH < 16 ? CH - 1 : 15))) * 16; }
+  static __device__ __forceinline__ int value_piece(int row, int c) { return row * RB + (c ^ (2 * row & (CH < 16 ? CH - 1 : 15))) * 16; }
+};
+
+// whether any of 8 16-bit values is infinite or NaN
+template <bool BF>
+__device__ __forceinline__ bool odd_value(u32x4v w) {
+  constexpr uint32_t kTop = BF ? 0x7F807F80u : 0x7C007C00u;
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = ~w[i] & kTop;  // a half of zero: all of its exponent's bits are set
+    odd |= (x & 0xFFFFu) == 0 || (x >> 16) == 0;
+  }
+  return odd;
+}
+// the values that are finite (0 for the others); those that are of a kind (0 +inf, 1 -inf,
+// 2 NaN), as ones
+template <bool BF>
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+  constexpr uint32_t kTop = BF ? 0x7F80u : 0x7C00u;
+  return ((w & kTop) == kTop ? 0u : w & 0xFFFFu) | ((w >> 16 & kTop) == kTop ? 0u : w & 0xFFFF0000u);
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t kind_pair(uint32_t w, int kind) {
+  constexpr uint32_t kTop = BF ? 0x7F80u : 0x7C00u, kOne = BF ? 0x3F80u : 0x3C00u;
+  auto is = [&](uint32_t x) {
+    return kind == 2 ? (x & 0x7FFFu) > kTop : x == (kind ? kTop | 0x8000u : kTop);
+  };
+  return (is(w & 0xFFFFu) ? kOne : 0u) | (is(w >> 16) ? kOne << 16 : 0u);
+}
+
+template <bool BF, int D, int NW>
+__global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_kernel(Params p) {
+  using S = Shape<BF, D, NW>;
+  constexpr int KT = S::KT, X = S::X, KK = S::KK, KS = S::KS, DB = S::DB, EACH = S::EACH;
+  __shared__ __align__(16) char lds[S::LDS];
+  __shared__ int range[NW][2], odd_tile[2][NW];
+  const PromptArgs &a = p.a;
+  const int head = blockIdx.x % (unsigned)a.kv_heads;
+  const int unit = blockIdx.x / (unsigned)a.kv_heads;
+  int b, tile;
+  if (!find_tile<S::R>(a, p.group, unit, b, tile)) return;
+  Sequence seq = sequence(a, b);
+  seq.q0 = uniform(seq.q0), seq.n = uniform(seq.n), seq.k0 = uniform(seq.k0), seq.len = uniform(seq.len);
+
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
+  const int rows = seq.n * p.group, row = tile * S::R + wave * 32 + (lane & 31);
+  const bool active = row < rows;
+  const int token = (active ? row : 0) / p.group, qh = head * p.group + ((active ? row : 0) - token * p.group);
+  const int pos = seq.len - seq.n + token;
+  // what the row sees: lo <= t < hi
+  int lo = 0, hi = 0;
+  {
+    const int first = a.scores.first ? a.scores.first[seq.q0 + token] : 0;
+    const int prefix = a.scores.prefix ? a.scores.prefix[b] : 0;
+    const int since = pos - p.window + 1;
+    lo = first > since ? first : since;
+    lo = lo < 0 ? 0 : lo;
+    hi = pos + 1 > prefix ? pos + 1 : prefix;
+    hi = hi < seq.len ? hi : seq.len;
+    if (!active || hi < lo) hi = lo = 0;
+  }
+  const bool sees = hi > lo;
+  // over the wave: the first and last key of any row, and the keys that all rows see
+  int least = sees ? lo : 0x7FFFFFFF, most = hi, from = active ? lo : 0, upto = active ? hi : 0x7FFFFFFF;
+  if (active && !sees) from = 0x7FFFFFFF;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_xor(least, d), y = __shfl_xor(most, d), z = __shfl_xor(from, d), w = __shfl_xor(upto, d);
+    least = x < least ? x : least, most = y > most ? y : most;
+    from = z > from ? z : from, upto = w < upto ? w : upto;
+  }
+  least = uniform(least), most = uniform(most), from = uniform(from), upto = uniform(upto);
+  if (lane == 0) range[wave][0] = least, range[wave][1] = most;
+  __syncthreads();
+  int begin = 0x7FFFFFFF, end = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    begin = range[w][0] < begin ? range[w][0] : begin;
+    end = range[w][1] > end ? range[w][1] : end;
+  }
+  // tiles of keys, of which this workgroup has a part
+  int t0 = uniform(begin < end ? begin / KT : 0), t1 = uniform(begin < end ? (end + KT - 1) / KT : 0);
+  if (p.parts > 1) {
+    const int64_t all = t1 - t0;
+    const int first = t0;
+    t0 = first + (int)(all * blockIdx.y / p.parts);
+    t1 = first + (int)(all * (blockIdx.y + 1) / p.parts);
+  }
+
+  // queries: the lane's row as the second operand, 8 values of each 16
+  u32x4v q[KS];
+  {
+    const uint16_t *src = a.q + (int64_t)(seq.q0 + token) * a.q_stride + (int64_t)qh * D + 8 * h;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      q[s] = *reinterpret_cast<const u32x4v *>(src + 16 * s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[s][i] ^= p.flip;
+    }
+  }
+  const float slope = a.scores.slopes ? a.scores.slopes[qh] * kLog2e : 0.f;
+
+  // keys and values of a tile, on their way
+  u32x4v next_k[EACH], next_v[EACH];
+  auto bring = [&](int tile) {
+    const int row0 = tile * KT, left = seq.len - row0;
+    auto fetch = [&](u32x4v *to, const uint16_t *x, int64_t stride) {
+      const uint64_t at = reinterpret_cast<uint64_t>(x + ((int64_t)seq.k0 + row0) * stride + (int64_t)head * D);
+      const uint32_t alo = uniform((int)(uint32_t)at), ahi = uniform((int)(uint32_t)(at >> 32));
+      // (rows past the sequence read as zeros, without a memory access)
+      const int there = left < KT ? left : KT, bytes = there > 0 ? (int)((there - 1) * stride * 2) + S::RB : 0;
+      const Span span = __builtin_amdgcn_make_buffer_rsrc(
+          reinterpret_cast<void *>(((uint64_t)ahi << 32) | alo), 0, uniform(bytes), 0x00020000);
+#pragma unroll
+      for (int e = 0; e < EACH; ++e) {
+        const int i = e * S::THREADS + (int)threadIdx.x, r = i / S::CH, c = i % S::CH;
+        to[e] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(span, r * (int)stride * 2 + c * 16, 0, 0));
+      }
+    };
+    fetch(next_k, a.k, a.k_stride);
+    fetch(next_v, a.v, a.v_stride);
+  };
+  lds_char *const mem = (lds_char *)lds;
+  auto put = [&](int half) {
+    bool odd = false;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+      const int i = e * S::THREADS + (int)threadIdx.x, r = i / S::CH, c = i % S::CH;
+      *(lds_u32x4 *)(mem + half * 2 * S::TILE + S::key_piece(r, c)) = next_k[e];
+      *(lds_u32x4 *)(mem + (half * 2 + 1) * S::TILE + S::value_piece(r, c)) = next_v[e];
+      odd |= odd_value<BF>(next_v[e]);
+    }
+    odd_tile[half][wave] = __ballot(odd) != 0;
+  };
+
+  f32x16v o[DB];
+#pragma unroll
+  for (int i = 0; i < DB; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
+  float m = kNegInf, l = 0.f;
+
+  if (t0 < t1) {
+    bring(t0);
+    put(0);
+  }
+  __syncthreads();
+  for (int t = t0; t < t1; ++t) {
+    const int half = (t - t0) & 1;
+    if (t + 1 < t1) bring(t + 1);
+    const int key0 = t * KT;
+    if (key0 < most && key0 + KT > least) {
+      const lds_char *const keys = mem + half * 2 * S::TILE, *const values = keys + S::TILE;
+      f32x16v s[X];
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[x][j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const u32x4v frag = *(const lds_u32x4 *)(keys + S::key_piece(32 * x + (lane & 31), 2 * k + h));
+          s[x] = mfma<BF>(frag, q[k], s[x]);
+        }
+      }
+      // scores in powers of two
+      if (p.cap2 != 0.f) {
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            // tanh y = 1 - 2 / (e^2y + 1)
+            const float e = exp2_fast(s[x][j] * (p.C * p.inv_cap2 * 2.f * kLog2e));
+            s[x][j] = __builtin_fmaf(-2.f * p.cap2, __builtin_amdgcn_rcpf(1.f + e), p.cap2);
+          }
+      } else {
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) s[x][j] *= p.C;
+      }
+      if (a.scores.slopes) {
+        const float away = (float)(pos - key0 - 4 * h);
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            s[x][j] = __builtin_fmaf(-slope, __builtin_fabsf(away - (float)(32 * x + 8 * (j >> 2) + (j & 3))), s[x][j]);
+      }
+      const bool edge = key0 < from || key0 + KT > upto;
+      if (edge) {
+        const int rel = key0 + 4 * h - lo;
+        const uint32_t span = (uint32_t)(hi - lo);
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            s[x][j] = (uint32_t)(rel + 32 * x + 8 * (j >> 2) + (j & 3)) < span ? s[x][j] : kNegInf;
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int x = 0; x < X; ++x)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = __builtin_fmaxf(top, s[x][j]);
+      top = __builtin_fmaxf(top, other_half(top));
+      const bool over = top - m > kUp;
+      if (__ballot(over)) {
+        // (scores past 2^23 have no room for kUp: their weights are 1 at most)
+        const float to = over ? (__builtin_fabsf(top) < 0x1p23f ? top - (kUp - 4.f) : top) : m;
+        // (not 0: an infinite sum stays what it is)
+        const float keep = __builtin_fmaxf(exp2_fast(m - (to == kNegInf ? 0.f : to)), 0x1p-126f);
+        m = to;
+        l *= keep;
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[i][j] *= keep;
+      }
+      const float base = m == kNegInf ? 0.f : m;
+      u32x4v w[KK];
+#pragma unroll
+      for (int x = 0; x < X; ++x)
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float e0 = exp2_fast(s[x][j] - base), e1 = exp2_fast(s[x][j + 1] - base);
+          l += e0 + e1;
+          w[2 * x + (j >> 3)][(j & 7) >> 1] = pack<BF>(e0, e1);
+        }
+
+      // the values: 4 tokens x 16 values a group of 16 lanes
+      const int vr = 4 * h + ((lane & 15) >> 2), vc = (lane >> 4 & 1) * 16 + (lane & 3) * 4;
+      auto value_operand = [&](int i, int k, int past = 0) {
+        const int d = 32 * i + vc, r = 16 * k + vr + past;
+        const s16x4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(values + S::value_piece(r, d >> 3) + (d & 7) * 2));
+        const s16x4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(values + S::value_piece(r + 8, d >> 3) + (d & 7) * 2));
+        const u32x2v u = __builtin_bit_cast(u32x2v, x), v = __builtin_bit_cast(u32x2v, y);
+        return u32x4v{u[0], u[1], v[0], v[1]};
+      };
+      int odd = 0;
+#pragma unroll
+      for (int x = 0; x < NW; ++x) odd |= odd_tile[half][x];
+      if (!uniform(odd)) {
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+          for (int k = 0; k < KK; ++k) o[i] = mfma<BF>(value_operand(i, k), w[k], o[i]);
+      } else {
+        // ones over the tokens that the row sees
+        constexpr uint32_t kOne = BF ? 0x3F80u : 0x3C00u;
+        u32x4v seen[KK];
+        const int rel = key0 + 4 * h - lo;
+        const uint32_t span = (uint32_t)(hi - lo);
+#pragma unroll
+        for (int k = 0; k < KK; ++k)
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            const int at = rel + 16 * k + 8 * (j >> 2) + (j & 3);
+            seen[k][j >> 1] = ((uint32_t)at < span ? kOne : 0u) | ((uint32_t)(at + 1) < span ? kOne << 16 : 0u);
+          }
+#pragma unroll
+        for (int i = 0; i < DB; ++i) {
+          // (opaque, or all operands are made, and kept, ahead of their products)
+          int past = 0;
+          asm volatile("" : "+s"(past));
+#pragma unroll
+          for (int k = 0; k < KK; ++k) {
+            u32x4v v = value_operand(i, k, past);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = finite_pair<BF>(v[j]);
+            o[i] = mfma<BF>(v, w[k], o[i]);
+          }
+#pragma unroll 1
+          for (int kind = 0; kind < 3; ++kind) {
+            f32x16v count;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) count[j] = 0.f;
+            asm volatile("" : "+s"(past));
+#pragma unroll
+            for (int k = 0; k < KK; ++k) {
+              u32x4v v = value_operand(i, k, past);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[j] = kind_pair<BF>(v[j], kind);
+              count = mfma<BF>(v, seen[k], count);
+            }
+            const float add = kind == 0 ? -kNegInf : (kind == 1 ? kNegInf : __builtin_nanf(""));
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[i][j] += count[j] > 0.f ? add : 0.f;
+          }
+        }
+      }
+    }
+    if (t + 1 < t1) put(half ^ 1);
+    __syncthreads();
+  }
+
+  l += other_half(l);
+  if (p.parts > 1) {
+    float *piece = p.piece + (((int64_t)unit * a.kv_heads + head) * p.parts + blockIdx.y) * piece_floats<D>(S::R);
+    const int r = wave * 32 + (lane & 31);
+    if (!active) return;
+    piece[S::R * D + r] = m;
+    piece[S::R * (D + 1) + r] = l;
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; j += 4)
+        *reinterpret_cast<float4 *>(piece + r * D + 32 * i + 2 * j + 4 * h) =
+            make_float4(o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]);
+    return;
+  }
+  if (!active) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t *out = a.out + ((int64_t)(seq.q0 + token) * a.q_heads + qh) * D;
+#pragma unroll
+  for (int i = 0; i < DB; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; j += 4)
+      *reinterpret_cast<uint2 *>(out + 32 * i + 2 * j + 4 * h) =
+          make_uint2(pack<BF>(o[i][j] * inv, o[i][j + 1] * inv), pack<BF>(o[i][j + 2] * inv, o[i][j + 3] * inv));
+  if (a.scores.lse && h == 0)
+    a.scores.lse[(int64_t)(seq.q0 + token) * a.q_heads + qh] = log_scaled(m, l);
+}
+
+// Joins the parts of a tile's keys: four values of a row a thread, the parts in order
+template <bool BF, int D, int R>
+__global__ __launch_bounds__(256) void prompt_join_kernel(Params p) {
+  const PromptArgs &a = p.a;
+  const int head = blockIdx.x % (unsigned)a.kv_heads, unit = blockIdx.x / (unsigned)a.kv_heads;
+  int b, tile;
+  if (!find_tile<R>(a, p.group, unit, b, tile)) return;
+  const Sequence seq = sequence(a, b);
+  const int item = blockIdx.y * 256 + threadIdx.x, r = item / (D / 4), d = item % (D / 4) * 4;
+  const int row = tile * R + r;
+  if (r >= R || row >= seq.n * p.group) return;
+  const float *piece = p.piece + ((int64_t)unit * a.kv_heads + head) * p.parts * piece_floats<D>(R);
+  float m = kNegInf, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < p.parts; i0 += 8) {
+    float4 v[8];
+    float pm[8], pl[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float *src = piece + (int64_t)(i0 + x < p.parts ? i0 + x : i0) * piece_floats<D>(R);
+      v[x] = *reinterpret_cast<const float4 *>(src + r * D + d);
+      pm[x] = src[R * D + r];
+      pl[x] = src[R * (D + 1) + r];
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      if (i0 + x < p.parts) {
+        const float top = __builtin_fmaxf(m, pm[x]), base = top == kNegInf ? 0.f : top;
+        const float f = __builtin_fmaxf(exp2_fast(m - base), 0x1p-126f), g = __builtin_fmaxf(exp2_fast(pm[x] - base), 0x1p-126f);
+        m = top;
+        l = l * f + pl[x] * g;
+        acc.x = acc.x * f + v[x].x * g, acc.y = acc.y * f + v[x].y * g;
+        acc.z = acc.z * f + v[x].z * g, acc.w = acc.w * f + v[x].w * g;
+      }
+  }
+  const int token = row / p.group, qh = head * p.group + row - token * p.group;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t at = (int64_t)(seq.q0 + token) * a.q_heads + qh;
+  *reinterpret_cast<uint2 *>(a.out + at * D + d) =
+      make_uint2(pack<BF>(acc.x * inv, acc.y * inv), pack<BF>(acc.z * inv, acc.w * inv));
+  if (a.scores.lse && d == 0)
+    a.scores.lse[at] = log_scaled(m, l);
+}
+
+// How a call is cut: waves of a workgroup, tiles of rows at most, and parts of every tile's keys
+struct Cut { int waves, tiles, parts; };
+Cut cut_for(int64_t Tq, int64_t Tk, int64_t B, int q_heads, int kv_heads, int D) {
+  const int group = q_heads / kv_heads, large = D > 128 ? 4 : 8;
+  Cut c;
+  c.waves = Tq * group <= 64 * B ? 2 : large;
+  const int R = 32 * c.waves;
+  c.tiles = (int)(Tq * group / R + B);
+  // parts of at least 8 tiles of keys, as long as the chip is not full and pieces fit 64 MiB
+  const int64_t wgs = (int64_t)c.tiles * kv_heads, room = ((int64_t)64 << 20) / ((int64_t)R * (D + 2) * 4);
+  int64_t parts = (int64_t)device_cus() * (c.waves == 2 ? 4 : 1) / wgs;
+  const int64_t keys = (Tk + B - 1) / B / (8 * (D > 128 ? 32 : 64));
+  if (parts > keys) parts = keys;
+  if (parts > room / wgs) parts = room / wgs;
+  if (parts > kMaxParts) parts = kMaxParts;
+  c.parts = parts < 2 ? 1 : (int)parts;
+  return c;
+}
+
+template <bool BF, int D, int NW>
+hipError_t launch(const Params &p, hipStream_t s) {
+  using S = Shape<BF, D, NW>;
+  const unsigned wgs = (unsigned)p.tiles * (unsigned)p.a.kv_heads;
+  hipLaunchKernelGGL((prompt_kernel<BF, D, NW>), dim3(wgs, p.parts), dim3(S::THREADS), 0, s, p);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || p.parts == 1) return err;
+  hipLaunchKernelGGL((prompt_join_kernel<BF, D, S::R>), dim3(wgs, S::R * D / 4 / 256), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t prompt_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int q_heads, int kv_heads, int D) {
+  const Cut c = cut_for(Tq, Tk, B, q_heads, kv_heads, D);
+  return c.parts == 1 ? 16 : (int64_t)c.tiles * kv_heads * c.parts * 32 * c.waves * (D + 2) * 4;
+}
+
+hipError_t launch_prompt_attention(const PromptArgs &a, hipStream_t s) {
+  Params p;
+  p.a = a;
+  p.C = __builtin_fabsf(a.scale) * kLog2e;
+  p.flip = a.scale < 0.f ? 0x80008000u : 0u;
+  p.cap2 = a.scores.softcap * kLog2e;
+  p.inv_cap2 = a.scores.softcap != 0.f ? 1.f / p.cap2 : 0.f;
+  p.window = a.scores.window > 0 && a.scores.window < (1 << 25) ? a.scores.window : 1 << 25;
+  p.group = a.q_heads / a.kv_heads;
+  const Cut c = cut_for(a.Tq, a.Tk, a.B, a.q_heads, a.kv_heads, a.head_dim);
+  p.tiles = c.tiles;
+  p.parts = c.parts;
+  p.piece = reinterpret_cast<float *>(a.workspace);
+#define AQ_W(B, D)                                                     \
+  if (a.head_dim == D)                                                 \
+    return c.waves == 2 ? launch<B, D, 2>(p, s) : launch<B, D, (D > 128 ? 4 : 8)>(p, s);
+#define AQ_D(B) AQ_W(B, 64) AQ_W(B, 128) AQ_W(B, 256)
+  if (a.x_dtype == X_BF16) { AQ_D(true) } else { AQ_D(false) }
+#undef AQ_D
+#undef AQ_W
+  return hipErrorInvalidValue;
+}
+
+}  // namespace aq

@@ -471,6 +471,206 @@ aq_status aq_paged_attention(const void *q, aq_dtype x_dtype, int64_t B, int L, 
  * -1 on bad arguments.  May query the current device's compute-unit count. */
 int64_t aq_paged_attention_workspace(int64_t B, int L, int q_heads, int kv_heads, int head_dim);
 
+/* ---- attention with capped, biased and masked scores ----------------------
+ *
+ * How scores become weights, for the calls below.  The score of a row (one
+ * query head of one token at position `pos` of its sequence) and the token at
+ * position t is, in this order,
+ *
+ *   s = scale * q . k[t]
+ *   s = softcap * tanh(s / softcap)     unless softcap is 0
+ *   s = s - slopes[head] * |pos - t|    unless slopes is NULL
+ *
+ * and the row sees the token t when all of these hold:
+ *
+ *   t < the sequence's length
+ *   t <= pos, or t < prefix[sequence]   (prefix NULL: t <= pos)
+ *   pos - t < window                    (window 0: any)
+ *   t >= first[...]                     (first NULL: any; the document that
+ *                                        the row belongs to begins there)
+ *
+ * What a row does not see has no part in it, whatever it holds (infinite and
+ * NaN values too).  A row that sees no token is zero.  lse, where it is given,
+ * gets log(sum_t exp(s_t)) of each row, -inf for a row that sees no token.
+ *
+ * softcap: 0, or from 1e-30 to 1e30.  window >= 0.  slopes: device float
+ * [q_heads].  All pointers are device memory, 16-byte aligned. */
+typedef struct aq_attention_scores {
+  float softcap;
+  int32_t window;
+  const float *slopes;
+  const int32_t *first;
+  const int32_t *prefix;
+  float *lse;
+} aq_attention_scores;
+
+/* aq_paged_attention with such scores: the newest L (1..8) tokens of each
+ * sequence over the paged cache, token i of sequence b at position
+ * lengths[b] - L + i.  first: device int32 [B], one per sequence; prefix: NULL
+ * (AQ_ERR_INVALID_ARG otherwise: new tokens come after any prefix); lse: float
+ * [B, L, q_heads] or NULL.  Tokens ahead of what any of a sequence's rows sees
+ * are not read.  Everything else, the workspace too, as in aq_paged_attention;
+ * with all of `scores` zero the results are its own. */
+aq_status aq_paged_attention_masked(const void *q, aq_dtype x_dtype, int64_t B, int L, int q_heads,
+                                    int64_t q_stride, const aq_kv_cache *cache,
+                                    const int32_t *page_table, int64_t max_pages,
+                                    const int32_t *lengths, float scale,
+                                    const aq_attention_scores *scores, void *out, void *workspace,
+                                    int64_t workspace_bytes, void *stream);
+
+/* Attention of whole prompts, or of any number of new tokens, over keys and
+ * values that are rows of 16 bits (a projection's, or a cache's read back):
+ * sequence b's queries are the rows q_starts[b] .. q_starts[b + 1] - 1 of q,
+ * its keys and values the rows k_starts[b] .. k_starts[b + 1] - 1 of k and v,
+ * the queries' own among them as the last: query i of n is at position
+ * (keys - n) + i.  first: device int32 [Tq], one per row of q; prefix: device
+ * int32 [B]; lse: float [Tq, q_heads] or NULL.
+ *
+ * q [Tq, q_heads, head_dim], k and v [Tk, kv_heads, head_dim]: device, x_dtype
+ * AQ_F16 or AQ_BF16, heads and head_dim contiguous, tokens the strides apart
+ * in elements (multiples of 8, at least heads * head_dim).  q_starts, k_starts:
+ * device int32 [B + 1], ascending, from 0 to at most Tq and Tk (they are
+ * clamped to that); rows of q behind the last sequence are left as they are in
+ * out and lse.  out: device [Tq, q_heads, head_dim], no part of q, k or v.
+ * q_heads a multiple of kv_heads; head_dim 64, 128 or 256.  A weight is rounded
+ * to x_dtype once before it meets the values; scores, statistics and sums are
+ * binary32.  Results are the same bits every time.
+ *
+ * workspace: device memory of aq_prompt_attention_workspace bytes, 16-byte
+ * aligned, no initial content needed; calls that may run at the same time need
+ * workspaces of their own.  Tq = 0 does nothing.  AQ_ERR_UNSUPPORTED for Tq *
+ * q_heads, Tk * kv_heads or B * kv_heads >= 2^24, and for tokens of k or v more
+ * than 2^23 elements apart. */
+aq_status aq_prompt_attention(const void *q, aq_dtype x_dtype, int64_t Tq, int q_heads,
+                              int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                              int64_t v_stride, int64_t Tk, int kv_heads, int head_dim, int64_t B,
+                              const int32_t *q_starts, const int32_t *k_starts, float scale,
+                              const aq_attention_scores *scores, void *out, void *workspace,
+                              int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace aq_prompt_attention needs for this shape (at most 64 MiB);
+ * -1 on bad arguments.  May query the current device's compute-unit count. */
+int64_t aq_prompt_attention_workspace(int64_t Tq, int64_t Tk, int64_t B, int q_heads, int kv_heads,
+                                      int head_dim);
+
+/* ---- rotary positions ------------------------------------------------------
+ *
+ * The first `rotary` values of a head are rotary / 2 pairs; the pair i of a
+ * token at position p is turned by the angle p * freqs[i]:
+ *
+ *   (x, y) -> (x c - y s, y c + x s),  c = cos(angle) * factor, s = sin(angle) * factor
+ *
+ * interleaved 0: pair i is the values i and rotary / 2 + i; 1: the values 2 i
+ * and 2 i + 1.  The values from `rotary` on stay as they are.  The angle, its
+ * sine and cosine and their product with the factor are binary64 and rounded
+ * to binary32 once; each product and sum of the turn is rounded to binary32,
+ * the result to the 16-bit type.  Any int32 position, far and negative ones
+ * too; frequencies up to 2^20.  rotary: a multiple of 16, from 16 to head_dim; head_dim 64, 128 or 256
+ * (AQ_ERR_UNSUPPORTED otherwise); factor finite. */
+typedef struct aq_rotation {
+  const int32_t *positions; /* device [T] */
+  const float *freqs;       /* device [rotary / 2] */
+  int32_t rotary;
+  int32_t interleaved;
+  double factor;
+} aq_rotation;
+
+/* Turn the rows of q [T, q_heads, head_dim] into q_out and those of k [T,
+ * kv_heads, head_dim] into k_out.  Rows are 16-bit (AQ_F16 or AQ_BF16), heads
+ * and head_dim contiguous, tokens the strides apart in elements (multiples of
+ * 8, at least heads * head_dim).  q_out may be q itself (with its stride) and
+ * k_out k; other overlaps are the caller's mistake.  q_heads = 0 or kv_heads =
+ * 0 leaves that side out (its pointers may be NULL).  T = 0 does nothing. */
+aq_status aq_rope(const void *q, int64_t q_stride, int q_heads, const void *k, int64_t k_stride,
+                  int kv_heads, aq_dtype x_dtype, int64_t T, int head_dim,
+                  const aq_rotation *rotation, void *q_out, int64_t q_out_stride, void *k_out,
+                  int64_t k_out_stride, void *stream);
+
+/* aq_rope and aq_kv_append in one launch: q turned into q_out, k turned,
+ * rounded to x_dtype and written with v into the cache at slots.  The cache
+ * gets bit for bit what aq_rope and then aq_kv_append would write.  k_out, if
+ * not NULL, gets the turned keys as well (for attention over the rows
+ * themselves).  q_heads = 0 leaves the queries out.  Arguments as in those. */
+aq_status aq_rope_append(const void *q, int64_t q_stride, int q_heads, const void *k,
+                         int64_t k_stride, const void *v, int64_t v_stride, aq_dtype x_dtype,
+                         int64_t T, const aq_rotation *rotation, const int64_t *slots,
+                         const aq_kv_cache *cache, void *q_out, int64_t q_out_stride, void *k_out,
+                         int64_t k_out_stride, void *stream);
+
+/* How frequencies are changed for contexts longer than a model was trained on
+ * (s = stretch, ctx = the trained context, f = base^(-2 i / rotary)):
+ *   AQ_ROPE_PLAIN      f
+ *   AQ_ROPE_LINEAR     f / s (positions interpolated)
+ *   AQ_ROPE_BASE       f with base * s^(rotary / (rotary - 2))
+ *   AQ_ROPE_BY_INDEX   f / s for pairs that turn less than `low` times in ctx,
+ *                      f for those that turn more than `high` times, between
+ *                      them a blend that is linear in the pair's index: with
+ *                      d(r) = rotary ln(ctx / (2 pi r)) / (2 ln base), a =
+ *                      max(floor d(high), 0), b = min(ceil d(low), rotary - 1),
+ *                      the part g = clamp((i - a) / max(b - a, 0.001), 0, 1) of
+ *                      f / s and 1 - g of f; factor 0.1 ln s + 1 for s > 1
+ *   AQ_ROPE_BY_TURNS   the same, linear in the turns r = ctx f / (2 pi): g =
+ *                      1 - clamp((r - low) / (high - low), 0, 1); factor 1 */
+typedef enum aq_rope_stretch {
+  AQ_ROPE_PLAIN = 0,
+  AQ_ROPE_LINEAR = 1,
+  AQ_ROPE_BASE = 2,
+  AQ_ROPE_BY_INDEX = 3,
+  AQ_ROPE_BY_TURNS = 4
+} aq_rope_stretch;
+
+/* Fills freqs, HOST memory of rotary / 2 floats, and *factor (may be NULL) by
+ * that table, computed in binary64.  rotary even and >= 4, base > 1, stretch
+ * >= 1 (not looked at for AQ_ROPE_PLAIN); ctx >= 1 and 0 < low < high for the
+ * last two, AQ_ERR_INVALID_ARG otherwise. */
+aq_status aq_rope_frequencies(int rotary, double base, aq_rope_stretch kind, double stretch,
+                              double ctx, double low, double high, float *freqs, float *factor);
+
+/* ---- keeping a cache within a budget ---------------------------------------
+ *
+ * What each cached token gathers of the attention of new tokens, added to what
+ * it gathered before:
+ *
+ *   weights[b, t] += sum over rows i, h of exp(s - lse[b, i, h])
+ *
+ * for the tokens t < min(length, weights_stride) of sequence b, s and what a row sees as
+ * in aq_paged_attention_masked (softcap, window, slopes, first; prefix NULL).
+ * scores->lse, float [B, L, q_heads], is what that call gave for the same
+ * queries, and is required; a row whose lse is -inf adds nothing.  weights:
+ * device float, sequence b's at weights + b * weights_stride, weights_stride a
+ * multiple of 4.  Only the keys of the cache are read.  The sums are binary32,
+ * in an order that does not depend on timing. */
+aq_status aq_kv_weigh(const void *q, aq_dtype x_dtype, int64_t B, int L, int q_heads,
+                      int64_t q_stride, const aq_kv_cache *cache, const int32_t *page_table,
+                      int64_t max_pages, const int32_t *lengths, float scale,
+                      const aq_attention_scores *scores, float *weights, int64_t weights_stride,
+                      void *stream);
+
+/* Evict what gathered least.  Sequence b (length n = lengths[b], clamped to
+ * [0, min(max_pages * page_size, weights_stride)]) keeps all its tokens if n <=
+ * keep; otherwise the first `sinks`, the last `recent` and, of those between,
+ * the keep - sinks - recent with the largest weights: the lowest positions of
+ * equal ones, NaN below everything.  The kept tokens, in their order, become
+ * the tokens 0, 1, ... of the pages of new_table [B, new_max_pages]; their rows
+ * are copied there as they are.  Outputs: kept int32 [B, keep], the positions
+ * they had, -1 behind the last; new_weights float [B, keep], their weights, 0
+ * behind the last; new_lengths int32 [B].
+ *
+ * The pages of new_table are to be other pages than those of page_table, since
+ * a page may be shared by sequences and tokens move at once; the caller frees
+ * the old ones afterwards.  Rows of a page id outside the cache read as zeros
+ * (codes, scales and biases 0); rows that would go to one are not written.
+ * keep >= 1, sinks and recent >= 0, sinks + recent <= keep <= new_max_pages *
+ * page_size; AQ_ERR_INVALID_ARG otherwise.  lengths and new_lengths may be one
+ * array.  AQ_ERR_UNSUPPORTED for B >= 2^24, B * keep or B * keep * kv_heads / 64 >=
+ * 2^31, keep or weights_stride > 2^30, or tables of more than 2^31 - 256
+ * tokens. */
+aq_status aq_kv_evict(const float *weights, int64_t weights_stride, const int32_t *lengths,
+                      int64_t B, const int32_t *page_table, int64_t max_pages,
+                      const int32_t *new_table, int64_t new_max_pages, const aq_kv_cache *cache,
+                      int64_t keep, int64_t sinks, int64_t recent, int32_t *kept,
+                      float *new_weights, int32_t *new_lengths, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
