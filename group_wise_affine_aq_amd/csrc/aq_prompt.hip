@@ -27,10 +27,10 @@
 // would pass 2^kUp, seldom does; then everything summed is rescaled.
 //
 // Values that are not finite: 0 * inf is NaN, and a row that does not see a
-// token must not see its value.  A thread that brings values to LDS looks at
-// them; the products of a tile that holds an infinity or a NaN are made of its
-// finite values, and what is not finite is counted, by sign, with a product of
-// ones over the tokens that the row sees.
+// token must not see its value, nor lose an infinity to a weight that is
+// rounded to 0.  A thread that brings values to LDS looks at them; those that
+// are not finite become 0 there, and the waves add them, from memory, to the
+// rows that see their token, one token of such a tile after the other.
 #include "aq_device.hpp"
 #include "aq_internal.hpp"
 
@@ -42,6 +42,7 @@ typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
 typedef float f32x16v __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2v __attribute__((ext_vector_type(2)));
 typedef short s16x4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4v lds_s16x4;
 typedef __attribute__((address_space(3))) u32x4v lds_u32x4;
@@ -149,32 +150,28 @@ struct Shape {
   static __device__ __forceinline__ int value_piece(int row, int c) { return row * RB + (c ^ (2 * row & (CH < 16 ? CH - 1 : 15))) * 16; }
 };
 
-// whether any of 8 16-bit values is infinite or NaN
-template <bool BF>
-__device__ __forceinline__ bool odd_value(u32x4v w) {
-  constexpr uint32_t kTop = BF ? 0x7F807F80u : 0x7C007C00u;
-  bool odd = false;
+// the larger magnitude of each half, and whether one is infinite or NaN
+__device__ __forceinline__ uint32_t larger_pair(uint32_t most, u32x4v w) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t x = ~w[i] & kTop;  // a half of zero: all of its exponent's bits are set
-    odd |= (x & 0xFFFFu) == 0 || (x >> 16) == 0;
-  }
-  return odd;
+  for (int i = 0; i < 4; ++i)
+    most = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2v, most),
+                                                                  __builtin_bit_cast(u16x2v, w[i] & 0x7FFF7FFFu)));
+  return most;
 }
-// the values that are finite (0 for the others); those that are of a kind (0 +inf, 1 -inf,
-// 2 NaN), as ones
 template <bool BF>
-__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+__device__ __forceinline__ bool odd_value(uint32_t most) {
   constexpr uint32_t kTop = BF ? 0x7F80u : 0x7C00u;
-  return ((w & kTop) == kTop ? 0u : w & 0xFFFFu) | ((w >> 16 & kTop) == kTop ? 0u : w & 0xFFFF0000u);
+  return (most & 0xFFFFu) >= kTop || (most >> 16) >= kTop;
+}
+// the values that are not finite, or the others, 0 in the places of the rest
+template <bool BF>
+__device__ __forceinline__ uint32_t odd_pair(uint32_t w) {
+  constexpr uint32_t kTop = BF ? 0x7F80u : 0x7C00u;
+  return ((w & kTop) == kTop ? w & 0xFFFFu : 0u) | ((w >> 16 & kTop) == kTop ? w & 0xFFFF0000u : 0u);
 }
 template <bool BF>
-__device__ __forceinline__ uint32_t kind_pair(uint32_t w, int kind) {
-  constexpr uint32_t kTop = BF ? 0x7F80u : 0x7C00u, kOne = BF ? 0x3F80u : 0x3C00u;
-  auto is = [&](uint32_t x) {
-    return kind == 2 ? (x & 0x7FFFu) > kTop : x == (kind ? kTop | 0x8000u : kTop);
-  };
-  return (is(w & 0xFFFFu) ? kOne : 0u) | (is(w >> 16) ? kOne << 16 : 0u);
+__device__ __forceinline__ float half_of(uint32_t w, int i) {
+  return BF ? bf16_to_f32((uint16_t)(w >> (16 * i))) : f16_to_f32((uint16_t)(w >> (16 * i)));
 }
 
 template <bool BF, int D, int NW>
@@ -249,17 +246,21 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
   }
   const float slope = a.scores.slopes ? a.scores.slopes[qh] * kLog2e : 0.f;
 
+  // the rows of a tile of keys or values; those past the sequence read as zeros,
+  // without a memory access
+  auto rows_of = [&](const uint16_t *x, int64_t stride, int tile) {
+    const int left = seq.len - tile * KT, there = left < KT ? left : KT;
+    const uint64_t at = reinterpret_cast<uint64_t>(x + ((int64_t)seq.k0 + tile * KT) * stride + (int64_t)head * D);
+    const uint32_t alo = uniform((int)(uint32_t)at), ahi = uniform((int)(uint32_t)(at >> 32));
+    const int bytes = there > 0 ? (int)((there - 1) * stride * 2) + S::RB : 0;
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(((uint64_t)ahi << 32) | alo), 0,
+                                             uniform(bytes), 0x00020000);
+  };
   // keys and values of a tile, on their way
   u32x4v next_k[EACH], next_v[EACH];
   auto bring = [&](int tile) {
-    const int row0 = tile * KT, left = seq.len - row0;
     auto fetch = [&](u32x4v *to, const uint16_t *x, int64_t stride) {
-      const uint64_t at = reinterpret_cast<uint64_t>(x + ((int64_t)seq.k0 + row0) * stride + (int64_t)head * D);
-      const uint32_t alo = uniform((int)(uint32_t)at), ahi = uniform((int)(uint32_t)(at >> 32));
-      // (rows past the sequence read as zeros, without a memory access)
-      const int there = left < KT ? left : KT, bytes = there > 0 ? (int)((there - 1) * stride * 2) + S::RB : 0;
-      const Span span = __builtin_amdgcn_make_buffer_rsrc(
-          reinterpret_cast<void *>(((uint64_t)ahi << 32) | alo), 0, uniform(bytes), 0x00020000);
+      const Span span = rows_of(x, stride, tile);
 #pragma unroll
       for (int e = 0; e < EACH; ++e) {
         const int i = e * S::THREADS + (int)threadIdx.x, r = i / S::CH, c = i % S::CH;
@@ -271,16 +272,34 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
   };
   lds_char *const mem = (lds_char *)lds;
   auto put = [&](int half) {
-    bool odd = false;
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) top = larger_pair(top, next_v[e]);
+    const bool any = __ballot(odd_value<BF>(top)) != 0;
+    if (any)
+#pragma unroll
+      for (int e = 0; e < EACH; ++e)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) next_v[e][j] ^= odd_pair<BF>(next_v[e][j]);
+    odd_tile[half][wave] = any;
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
       const int i = e * S::THREADS + (int)threadIdx.x, r = i / S::CH, c = i % S::CH;
       *(lds_u32x4 *)(mem + half * 2 * S::TILE + S::key_piece(r, c)) = next_k[e];
       *(lds_u32x4 *)(mem + (half * 2 + 1) * S::TILE + S::value_piece(r, c)) = next_v[e];
-      odd |= odd_value<BF>(next_v[e]);
     }
-    odd_tile[half][wave] = __ballot(odd) != 0;
   };
+
+  // Where the lane's operands begin, this tile's half of LDS included: the xor
+  // reaches the low four bits of a piece's number, so pieces 16 apart, and rows 8
+  // apart, are at fixed distances.
+  constexpr int NK = KS < 8 ? KS : 8, NV = DB < 4 ? DB : 4;
+  const int vr = 4 * h + ((lane & 15) >> 2), vc = (lane >> 4 & 1) * 16 + (lane & 3) * 4;
+  int at_k[NK], at_v[NV];
+#pragma unroll
+  for (int k = 0; k < NK; ++k) at_k[k] = S::key_piece(lane & 31, 2 * k + h);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) at_v[i] = S::TILE + S::value_piece(vr, (32 * i + vc) >> 3) + (vc & 7) * 2;
 
   f32x16v o[DB];
 #pragma unroll
@@ -299,7 +318,6 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
     if (t + 1 < t1) bring(t + 1);
     const int key0 = t * KT;
     if (key0 < most && key0 + KT > least) {
-      const lds_char *const keys = mem + half * 2 * S::TILE, *const values = keys + S::TILE;
       f32x16v s[X];
 #pragma unroll
       for (int x = 0; x < X; ++x) {
@@ -307,7 +325,7 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
         for (int j = 0; j < 16; ++j) s[x][j] = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          const u32x4v frag = *(const lds_u32x4 *)(keys + S::key_piece(32 * x + (lane & 31), 2 * k + h));
+          const u32x4v frag = *(const lds_u32x4 *)(mem + at_k[k % NK] + (32 * x * S::RB + k / NK * 256));
           s[x] = mfma<BF>(frag, q[k], s[x]);
         }
       }
@@ -376,67 +394,45 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
         }
 
       // the values: 4 tokens x 16 values a group of 16 lanes
-      const int vr = 4 * h + ((lane & 15) >> 2), vc = (lane >> 4 & 1) * 16 + (lane & 3) * 4;
-      auto value_operand = [&](int i, int k, int past = 0) {
-        const int d = 32 * i + vc, r = 16 * k + vr + past;
-        const s16x4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(values + S::value_piece(r, d >> 3) + (d & 7) * 2));
-        const s16x4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(values + S::value_piece(r + 8, d >> 3) + (d & 7) * 2));
+      auto value_operand = [&](int i, int k) {
+        const lds_char *from = mem + at_v[i % NV] + (16 * k * S::RB + i / NV * 256);
+        const s16x4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)from);
+        const s16x4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(from + 8 * S::RB));
         const u32x2v u = __builtin_bit_cast(u32x2v, x), v = __builtin_bit_cast(u32x2v, y);
         return u32x4v{u[0], u[1], v[0], v[1]};
       };
+#pragma unroll
+      for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int k = 0; k < KK; ++k) o[i] = mfma<BF>(value_operand(i, k), w[k], o[i]);
+
       int odd = 0;
 #pragma unroll
       for (int x = 0; x < NW; ++x) odd |= odd_tile[half][x];
-      if (!uniform(odd)) {
-#pragma unroll
-        for (int i = 0; i < DB; ++i)
-#pragma unroll
-          for (int k = 0; k < KK; ++k) o[i] = mfma<BF>(value_operand(i, k), w[k], o[i]);
-      } else {
-        // ones over the tokens that the row sees
-        constexpr uint32_t kOne = BF ? 0x3F80u : 0x3C00u;
-        u32x4v seen[KK];
-        const int rel = key0 + 4 * h - lo;
-        const uint32_t span = (uint32_t)(hi - lo);
-#pragma unroll
-        for (int k = 0; k < KK; ++k)
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            const int at = rel + 16 * k + 8 * (j >> 2) + (j & 3);
-            seen[k][j >> 1] = ((uint32_t)at < span ? kOne : 0u) | ((uint32_t)(at + 1) < span ? kOne << 16 : 0u);
-          }
-#pragma unroll
-        for (int i = 0; i < DB; ++i) {
-          // (opaque, or all operands are made, and kept, ahead of their products)
-          int past = 0;
-          asm volatile("" : "+s"(past));
-#pragma unroll
-          for (int k = 0; k < KK; ++k) {
-            u32x4v v = value_operand(i, k, past);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = finite_pair<BF>(v[j]);
-            o[i] = mfma<BF>(v, w[k], o[i]);
-          }
+      if (uniform(odd)) {
+        const Span span = rows_of(a.v, a.v_stride, t);
 #pragma unroll 1
-          for (int kind = 0; kind < 3; ++kind) {
-            f32x16v count;
+        for (int x = 0; x < KT; ++x) {
+          const bool in = (uint32_t)(key0 + x - lo) < (uint32_t)(hi - lo);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) count[j] = 0.f;
-            asm volatile("" : "+s"(past));
+          for (int i = 0; i < DB; ++i)
 #pragma unroll
-            for (int k = 0; k < KK; ++k) {
-              u32x4v v = value_operand(i, k, past);
+            for (int j = 0; j < 16; j += 4) {
+              const u32x2v v = __builtin_bit_cast(u32x2v, __builtin_amdgcn_raw_buffer_load_b64(
+                  span, x * (int)a.v_stride * 2 + (32 * i + 2 * j + 4 * h) * 2, 0, 0));
 #pragma unroll
-              for (int j = 0; j < 4; ++j) v[j] = kind_pair<BF>(v[j], kind);
-              count = mfma<BF>(v, seen[k], count);
+              for (int y = 0; y < 4; ++y) {
+                const float z = half_of<BF>(odd_pair<BF>(v[y >> 1]), y & 1);
+                o[i][j + y] += in ? z : 0.f;
+              }
             }
-            const float add = kind == 0 ? -kNegInf : (kind == 1 ? kNegInf : __builtin_nanf(""));
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[i][j] += count[j] > 0.f ? add : 0.f;
-          }
         }
       }
     }
+#pragma unroll
+    for (int k = 0; k < NK; ++k) at_k[k] ^= 2 * S::TILE;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) at_v[i] ^= 2 * S::TILE;
     if (t + 1 < t1) put(half ^ 1);
     __syncthreads();
   }
