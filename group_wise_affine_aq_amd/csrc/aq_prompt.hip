@@ -9,8 +9,7 @@
 // the group, token by token -- are cut into tiles of 32 NW; a workgroup of NW
 // waves takes one, 32 rows a wave, and walks over the keys that any of them
 // sees, KT at a time.  Keys and values of a tile go through LDS once and serve
-// all waves; while they are worked on, the next tile's are on their way to
-// registers and are then written to the other half of LDS: one barrier a tile.
+// all waves; while they are worked on, the next tile's are on their way.
 //
 // Matrix layout (v_mfma_f32_32x32x16).  S^T = K q^T: a lane has one row of
 // queries (lane % 32) and, with h = lane / 32, the tokens 8 i + 4 h .. + 3 of
@@ -28,9 +27,11 @@
 //
 // Values that are not finite: 0 * inf is NaN, and a row that does not see a
 // token must not see its value, nor lose an infinity to a weight that is
-// rounded to 0.  A thread that brings values to LDS looks at them; those that
-// are not finite become 0 there, and the waves add them, from memory, to the
-// rows that see their token, one token of such a tile after the other.
+// rounded to 0.  Such a value leaves no finite result in its column of any row
+// of the wave, so a workgroup that ends with one that is not finite starts
+// again, with care: values are looked at on their way to LDS, those that are not
+// finite become 0 there, and the waves add them, from memory, to the rows that
+// see their token, one token of such a tile after the other.
 #include "aq_device.hpp"
 #include "aq_internal.hpp"
 
@@ -58,7 +59,9 @@ struct Params {
   PromptArgs a;
   float C;         // |scale| log2 e
   uint32_t flip;   // sign of the scale, for pairs of queries
-  float cap2, inv_cap2;
+  // caps: cap2 (in powers of two; 0: none), what brings a score s to 2 log2 e times tanh's
+  // argument; where |s| <= small the cap is s times a polynomial in s^2
+  float cap2, twice, small, cap[5];
   int window, group;
   int tiles;       // of query rows, at most, of all sequences
   int parts;       // of every tile's keys
@@ -146,8 +149,10 @@ struct Shape {
   static constexpr int KS = D / 16, DB = D / 32;
   static constexpr int TILE = KT * RB;        // bytes of keys, or values
   static constexpr int LDS = 4 * TILE;
-  static __device__ __forceinline__ int key_piece(int row, int c) { return row * RB + (c ^ (row & (CH < 16 ? CH - 1 : 15))) * 16; }
-  static __device__ __forceinline__ int value_piece(int row, int c) { return row * RB + (c ^ (2 * row & (CH < 16 ? CH - 1 : 15))) * 16; }
+  static __device__ __forceinline__ int key_piece(int row, int c) { return row * RB + (c ^ key_swap(row)) * 16; }
+  static __device__ __forceinline__ int value_swap(int row) { return CH < 16 ? row << 1 & 4 : row << 2 & 12; }
+  static __device__ __forceinline__ int key_swap(int row) { return row & (CH < 16 ? CH - 1 : 15); }
+  static __device__ __forceinline__ int value_piece(int row, int c) { return row * RB + (c ^ value_swap(row)) * 16; }
 };
 
 // the larger magnitude of each half, and whether one is infinite or NaN
@@ -173,6 +178,26 @@ template <bool BF>
 __device__ __forceinline__ float half_of(uint32_t w, int i) {
   return BF ? bf16_to_f32((uint16_t)(w >> (16 * i))) : f16_to_f32((uint16_t)(w >> (16 * i)));
 }
+
+// the largest of a lane's scores, or of their magnitudes
+template <int X>
+__device__ __forceinline__ float largest(const f32x16v (&s)[X], bool magnitude) {
+  float top = magnitude ? __builtin_fabsf(s[0][0]) : s[0][0];
+#pragma unroll
+  for (int x = 0; x < X; ++x)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = __builtin_fmaxf(top, magnitude ? __builtin_fabsf(s[x][j]) : s[x][j]);
+  return top;
+}
+// a score below p.small, capped, is the score times this polynomial in its square
+__device__ __forceinline__ float cap_factor(const Params &p, float s) {
+  const float u = s * s;
+  float f = __builtin_fmaf(u, p.cap[4], p.cap[3]);
+  f = __builtin_fmaf(u, f, p.cap[2]);
+  f = __builtin_fmaf(u, f, p.cap[1]);
+  return __builtin_fmaf(u, f, p.cap[0]);
+}
+__device__ __forceinline__ float small_cap(const Params &p, float s) { return s * cap_factor(p, s); }
 
 template <bool BF, int D, int NW>
 __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_kernel(Params p) {
@@ -256,38 +281,58 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
     return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(((uint64_t)ahi << 32) | alo), 0,
                                              uniform(bytes), 0x00020000);
   };
-  // keys and values of a tile, on their way
-  u32x4v next_k[EACH], next_v[EACH];
-  auto bring = [&](int tile) {
-    auto fetch = [&](u32x4v *to, const uint16_t *x, int64_t stride) {
-      const Span span = rows_of(x, stride, tile);
-#pragma unroll
-      for (int e = 0; e < EACH; ++e) {
-        const int i = e * S::THREADS + (int)threadIdx.x, r = i / S::CH, c = i % S::CH;
-        to[e] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(span, r * (int)stride * 2 + c * 16, 0, 0));
-      }
-    };
-    fetch(next_k, a.k, a.k_stride);
-    fetch(next_v, a.v, a.v_stride);
-  };
+  // Keys of tile `due` and values of the one before it (tiles counted from t0) go straight to
+  // LDS, a kilobyte a load, the lanes' pieces in the order in which LDS has them.  The compiler
+  // does not know of these loads: arrived() waits for them.
+  const int tiles = t1 - t0;
+  int due = 0;
   lds_char *const mem = (lds_char *)lds;
-  auto put = [&](int half) {
-    uint32_t top = 0;
+  int from_k[EACH], from_v[EACH];
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) top = larger_pair(top, next_v[e]);
-    const bool any = __ballot(odd_value<BF>(top)) != 0;
-    if (any)
-#pragma unroll
-      for (int e = 0; e < EACH; ++e)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) next_v[e][j] ^= odd_pair<BF>(next_v[e][j]);
-    odd_tile[half][wave] = any;
+  for (int e = 0; e < EACH; ++e) {
+    const int at = (wave * EACH + e) * 64 + lane, r = at / S::CH, c = at % S::CH;
+    from_k[e] = r * (int)a.k_stride * 2 + (c ^ S::key_swap(r)) * 16;
+    from_v[e] = r * (int)a.v_stride * 2 + (c ^ S::value_swap(r)) * 16;
+  }
+  auto fetch = [&](const int *from, const uint16_t *x, int64_t stride, int tile, int to) {
+    const Span span = rows_of(x, stride, t0 + tile);
+    const uint32_t base = (uint32_t)uniform((int)(uint32_t)(uintptr_t)mem + to + wave * (EACH * 1024));
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
-      const int i = e * S::THREADS + (int)threadIdx.x, r = i / S::CH, c = i % S::CH;
-      *(lds_u32x4 *)(mem + half * 2 * S::TILE + S::key_piece(r, c)) = next_k[e];
-      *(lds_u32x4 *)(mem + (half * 2 + 1) * S::TILE + S::value_piece(r, c)) = next_v[e];
+      uint32_t kept;  // (m0, which the compiler may have a use for)
+      asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                   "buffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+                   : "=&s"(kept) : "s"(base + e * 1024), "v"(from[e]), "s"(span) : "memory");
     }
+  };
+  auto arrived = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
+  bool careful = false;  // values are looked at on their way
+  auto bring = [&] {
+    if (due < tiles) fetch(from_k, a.k, a.k_stride, due, (due & 1) * S::TILE);
+    if (due > 0 && due <= tiles) {
+      const int half = (due - 1) & 1, to = (2 + half) * S::TILE;
+      if (!careful) {
+        fetch(from_v, a.v, a.v_stride, due - 1, to);
+      } else {
+        const Span span = rows_of(a.v, a.v_stride, t0 + due - 1);
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+          u32x4v x = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(span, from_v[e], 0, 0));
+          top = larger_pair(top, x);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] ^= odd_pair<BF>(x[j]);
+          *(lds_u32x4 *)(mem + to + ((wave * EACH + e) * 64 + lane) * 16) = x;
+        }
+        odd_tile[half][wave] = __ballot(odd_value<BF>(top)) != 0;
+      }
+    }
+    ++due;
+  };
+  auto barrier = [] {
+    __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   // Where the lane's operands begin, this tile's half of LDS included: the xor
@@ -296,81 +341,164 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
   constexpr int NK = KS < 8 ? KS : 8, NV = DB < 4 ? DB : 4;
   const int vr = 4 * h + ((lane & 15) >> 2), vc = (lane >> 4 & 1) * 16 + (lane & 3) * 4;
   int at_k[NK], at_v[NV];
-#pragma unroll
-  for (int k = 0; k < NK; ++k) at_k[k] = S::key_piece(lane & 31, 2 * k + h);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) at_v[i] = S::TILE + S::value_piece(vr, (32 * i + vc) >> 3) + (vc & 7) * 2;
-
   f32x16v o[DB];
+  float m, l;
+
+  // The first product of tile t, and the second one of the tile before, whose weights are w
+  f32x16v s[X];
+  u32x4v w[KK];
+  bool have = false;  // (w: a tile that no row of the wave sees has none)
+  auto multiply = [&] {
+#pragma unroll
+    for (int x = 0; x < X; ++x)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[x][j] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+        const u32x4v frag = *(const lds_u32x4 *)(mem + at_k[k % NK] + (32 * x * S::RB + k / NK * 256));
+        s[x] = mfma<BF>(frag, q[k], s[x]);
+      }
+  };
+  auto gather = [&](int t) {
+    // the values: 4 tokens x 16 values a group of 16 lanes
+    auto value_operand = [&](int i, int k) {
+      const lds_char *from = mem + at_v[i % NV] + (16 * k * S::RB + i / NV * 256);
+      const s16x4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)from);
+      const s16x4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(from + 8 * S::RB));
+      const u32x2v u = __builtin_bit_cast(u32x2v, x), v = __builtin_bit_cast(u32x2v, y);
+      return u32x4v{u[0], u[1], v[0], v[1]};
+    };
+#pragma unroll
+    for (int k = 0; k < KK; ++k)
+#pragma unroll
+      for (int i = 0; i < DB; ++i) o[i] = mfma<BF>(value_operand(i, k), w[k], o[i]);
+
+    if (!careful) return;
+    int odd = 0;
+#pragma unroll
+    for (int x = 0; x < NW; ++x) odd |= odd_tile[(t - t0) & 1][x];
+    if (uniform(odd)) {
+      const int key0 = t * KT;
+      const Span span = rows_of(a.v, a.v_stride, t);
+#pragma unroll 1
+      for (int x = 0; x < KT; ++x) {
+        const bool in = (uint32_t)(key0 + x - lo) < (uint32_t)(hi - lo);
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const u32x2v v = __builtin_bit_cast(u32x2v, __builtin_amdgcn_raw_buffer_load_b64(
+                span, x * (int)a.v_stride * 2 + (32 * i + 2 * j + 4 * h) * 2, 0, 0));
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float z = half_of<BF>(odd_pair<BF>(v[y >> 1]), y & 1);
+              o[i][j + y] += in ? z : 0.f;
+            }
+          }
+      }
+    }
+  };
+
+  // Two groups of waves, each with a wave on every SIMD, take turns: while one multiplies the other
+  // has the softmax, half a tile later.  Their phases are counted from 0; the earlier group multiplies
+  // tile t in phase 2 t, the later one in phase 2 t + 1.  The keys of tile t + 1 and the values of t are
+  // brought in the phases 2 t and 2 t + 1: what their place held was last read in phase 2 t - 1.
+  const bool late = NW == 8 && wave >= NW / 2;
+  for (;;) {
 #pragma unroll
   for (int i = 0; i < DB; ++i)
 #pragma unroll
     for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
-  float m = kNegInf, l = 0.f;
-
-  if (t0 < t1) {
-    bring(t0);
-    put(0);
+  m = kNegInf, l = 0.f;
+  have = false;
+#pragma unroll
+  for (int k = 0; k < NK; ++k) at_k[k] = S::key_piece(lane & 31, 2 * k + h);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) at_v[i] = 3 * S::TILE + S::value_piece(vr, (32 * i + vc) >> 3) + (vc & 7) * 2;
+  due = 0;
+  bring();
+  arrived();
+  barrier();
+  if (late) {
+    bring();
+    barrier();
   }
-  __syncthreads();
   for (int t = t0; t < t1; ++t) {
-    const int half = (t - t0) & 1;
-    if (t + 1 < t1) bring(t + 1);
     const int key0 = t * KT;
-    if (key0 < most && key0 + KT > least) {
-      f32x16v s[X];
+    const bool need = key0 < most && key0 + KT > least;
+    if (!late) bring();
+    __builtin_amdgcn_s_setprio(1);
+    if (need) multiply();
+    if (have) gather(t - 1);
+    __builtin_amdgcn_s_setprio(0);
 #pragma unroll
-      for (int x = 0; x < X; ++x) {
+    for (int k = 0; k < NK; ++k) at_k[k] ^= S::TILE;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) s[x][j] = 0.f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const u32x4v frag = *(const lds_u32x4 *)(mem + at_k[k % NK] + (32 * x * S::RB + k / NK * 256));
-          s[x] = mfma<BF>(frag, q[k], s[x]);
-        }
-      }
-      // scores in powers of two
-      if (p.cap2 != 0.f) {
-#pragma unroll
-        for (int x = 0; x < X; ++x)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            // tanh y = 1 - 2 / (e^2y + 1)
-            const float e = exp2_fast(s[x][j] * (p.C * p.inv_cap2 * 2.f * kLog2e));
-            s[x][j] = __builtin_fmaf(-2.f * p.cap2, __builtin_amdgcn_rcpf(1.f + e), p.cap2);
-          }
-      } else {
-#pragma unroll
-        for (int x = 0; x < X; ++x)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) s[x][j] *= p.C;
-      }
-      if (a.scores.slopes) {
-        const float away = (float)(pos - key0 - 4 * h);
-#pragma unroll
-        for (int x = 0; x < X; ++x)
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            s[x][j] = __builtin_fmaf(-slope, __builtin_fabsf(away - (float)(32 * x + 8 * (j >> 2) + (j & 3))), s[x][j]);
-      }
+    for (int i = 0; i < NV; ++i) at_v[i] ^= S::TILE;
+    if (late) arrived();
+    barrier();
+    if (late) bring();
+    if (need) {
+      // Scores in powers of two are t = s C, or its cap.  Three ways there, by what the wave has
+      // (each of s, C and the cap's polynomial fused with the subtraction of m where it can be):
+      // plain scores, capped ones that are small beside the cap, and all others.
       const bool edge = key0 < from || key0 + KT > upto;
-      if (edge) {
-        const int rel = key0 + 4 * h - lo;
-        const uint32_t span = (uint32_t)(hi - lo);
-#pragma unroll
-        for (int x = 0; x < X; ++x)
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            s[x][j] = (uint32_t)(rel + 32 * x + 8 * (j >> 2) + (j & 3)) < span ? s[x][j] : kNegInf;
+      const bool simple = !edge && !a.scores.slopes;
+      float top;
+      int way = 0;
+      if (simple && p.cap2 == 0.f) {
+        top = largest(s, false);
+        way = 1;
+      } else if (simple) {
+        top = largest(s, true);
+        if (__ballot(!(top <= p.small)) == 0) way = 2;
       }
-      float top = s[0][0];
+      if (way == 1) {
+        top *= p.C;
+      } else if (way == 2) {
+        top = small_cap(p, top);
+      } else {
+        if (p.cap2 != 0.f) {
 #pragma unroll
-      for (int x = 0; x < X; ++x)
+          for (int x = 0; x < X; ++x)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) top = __builtin_fmaxf(top, s[x][j]);
-      top = __builtin_fmaxf(top, other_half(top));
-      const bool over = top - m > kUp;
-      if (__ballot(over)) {
+            for (int j = 0; j < 16; ++j) {
+              // tanh y = 1 - 2 / (e^2y + 1)
+              const float e = exp2_fast(s[x][j] * p.twice);
+              s[x][j] = __builtin_fmaf(-2.f * p.cap2, __builtin_amdgcn_rcpf(1.f + e), p.cap2);
+            }
+        } else {
+#pragma unroll
+          for (int x = 0; x < X; ++x)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[x][j] *= p.C;
+        }
+        if (a.scores.slopes) {
+          const float away = (float)(pos - key0 - 4 * h);
+#pragma unroll
+          for (int x = 0; x < X; ++x)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              s[x][j] = __builtin_fmaf(-slope, __builtin_fabsf(away - (float)(32 * x + 8 * (j >> 2) + (j & 3))), s[x][j]);
+        }
+        if (edge) {
+          const int rel = key0 + 4 * h - lo;
+          const uint32_t span = (uint32_t)(hi - lo);
+#pragma unroll
+          for (int x = 0; x < X; ++x)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              s[x][j] = (uint32_t)(rel + 32 * x + 8 * (j >> 2) + (j & 3)) < span ? s[x][j] : kNegInf;
+        }
+        top = largest(s, false);
+      }
+      // (the lane's own half of the row, or what no score of it is above: enough to know that m stays)
+      if (__ballot(top - m > kUp)) {
+        if (way == 2) top = small_cap(p, largest(s, false));
+        top = __builtin_fmaxf(top, other_half(top));
+        const bool over = top - m > kUp;
         // (scores past 2^23 have no room for kUp: their weights are 1 at most)
         const float to = over ? (__builtin_fabsf(top) < 0x1p23f ? top - (kUp - 4.f) : top) : m;
         // (not 0: an infinite sum stays what it is)
@@ -383,58 +511,49 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
           for (int j = 0; j < 16; ++j) o[i][j] *= keep;
       }
       const float base = m == kNegInf ? 0.f : m;
-      u32x4v w[KK];
+      auto weigh = [&](auto score) {
 #pragma unroll
-      for (int x = 0; x < X; ++x)
+        for (int x = 0; x < X; ++x)
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float e0 = exp2_fast(s[x][j] - base), e1 = exp2_fast(s[x][j + 1] - base);
-          l += e0 + e1;
-          w[2 * x + (j >> 3)][(j & 7) >> 1] = pack<BF>(e0, e1);
-        }
-
-      // the values: 4 tokens x 16 values a group of 16 lanes
-      auto value_operand = [&](int i, int k) {
-        const lds_char *from = mem + at_v[i % NV] + (16 * k * S::RB + i / NV * 256);
-        const s16x4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)from);
-        const s16x4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(from + 8 * S::RB));
-        const u32x2v u = __builtin_bit_cast(u32x2v, x), v = __builtin_bit_cast(u32x2v, y);
-        return u32x4v{u[0], u[1], v[0], v[1]};
+          for (int j = 0; j < 16; j += 2) {
+            const float e0 = exp2_fast(score(s[x][j])), e1 = exp2_fast(score(s[x][j + 1]));
+            l += e0;
+            l += e1;
+            w[2 * x + (j >> 3)][(j & 7) >> 1] = pack<BF>(e0, e1);
+          }
       };
-#pragma unroll
-      for (int i = 0; i < DB; ++i)
-#pragma unroll
-        for (int k = 0; k < KK; ++k) o[i] = mfma<BF>(value_operand(i, k), w[k], o[i]);
+      if (way == 1)
+        weigh([&](float y) { return __builtin_fmaf(y, p.C, -base); });
+      else if (way == 2)
+        weigh([&](float y) { return __builtin_fmaf(y, cap_factor(p, y), -base); });
+      else
+        weigh([&](float y) { return y - base; });
 
-      int odd = 0;
-#pragma unroll
-      for (int x = 0; x < NW; ++x) odd |= odd_tile[half][x];
-      if (uniform(odd)) {
-        const Span span = rows_of(a.v, a.v_stride, t);
-#pragma unroll 1
-        for (int x = 0; x < KT; ++x) {
-          const bool in = (uint32_t)(key0 + x - lo) < (uint32_t)(hi - lo);
-#pragma unroll
-          for (int i = 0; i < DB; ++i)
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const u32x2v v = __builtin_bit_cast(u32x2v, __builtin_amdgcn_raw_buffer_load_b64(
-                  span, x * (int)a.v_stride * 2 + (32 * i + 2 * j + 4 * h) * 2, 0, 0));
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const float z = half_of<BF>(odd_pair<BF>(v[y >> 1]), y & 1);
-                o[i][j + y] += in ? z : 0.f;
-              }
-            }
-        }
-      }
     }
+    have = need;
+    if (!late) arrived();
+    barrier();
+  }
+  if (have) gather(t1 - 1);
+  if (NW == 8 && !late) barrier();
+
+  // An infinity or NaN among the values has reached all rows of the waves that multiplied it, by a
+  // weight of 0 too: then once more, with care.
+  if (careful) break;
+  float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < NK; ++k) at_k[k] ^= 2 * S::TILE;
+  for (int i = 0; i < DB; ++i)
 #pragma unroll
-    for (int i = 0; i < NV; ++i) at_v[i] ^= 2 * S::TILE;
-    if (t + 1 < t1) put(half ^ 1);
-    __syncthreads();
+    for (int j = 0; j < 16; ++j) sum = __builtin_fmaf(o[i][j], 0.f, sum);
+  const bool odd = __ballot(sum != 0.f) != 0;
+  odd_tile[0][wave] = odd;
+  barrier();
+  int any = 0;
+#pragma unroll
+  for (int x = 0; x < NW; ++x) any |= odd_tile[0][x];
+  if (!uniform(any)) break;
+  barrier();
+  careful = true;
   }
 
   l += other_half(l);
@@ -528,6 +647,24 @@ Cut cut_for(int64_t Tq, int64_t Tk, int64_t B, int q_heads, int kv_heads, int D)
   return c;
 }
 
+// tanh y / y = sum c_i y^2i within 2^-23 for |y| <= 0.6 (a fit of the least largest relative
+// error), so the cap of a small score costs five operations and no exponential or reciprocal:
+// these take four times as long each, and the softmax is what bounds the kernel.
+void set_cap(Params &p) {
+  constexpr double c[5] = {0.9999999268660705, -0.33332309948977934, 0.13310173306949546,
+                           -0.05210146457599173, 0.015475405965029628};
+  p.twice = 0.f, p.small = -1.f;
+  for (float &x : p.cap) x = 0.f;
+  if (p.cap2 == 0.f) return;
+  const double y = (double)p.C / p.cap2;
+  p.twice = (float)(2 * y * 1.4426950408889634);
+  const double small = 0.6 / y;
+  if (!(small > 1e-3 && small < 1e9)) return;  // (powers of scores within binary32)
+  double f = p.C;
+  for (int i = 0; i < 5; ++i, f *= y * y) p.cap[i] = (float)(c[i] * f);
+  p.small = (float)small;
+}
+
 template <bool BF, int D, int NW>
 hipError_t launch(const Params &p, hipStream_t s) {
   using S = Shape<BF, D, NW>;
@@ -552,7 +689,7 @@ hipError_t launch_prompt_attention(const PromptArgs &a, hipStream_t s) {
   p.C = __builtin_fabsf(a.scale) * kLog2e;
   p.flip = a.scale < 0.f ? 0x80008000u : 0u;
   p.cap2 = a.scores.softcap * kLog2e;
-  p.inv_cap2 = a.scores.softcap != 0.f ? 1.f / p.cap2 : 0.f;
+  set_cap(p);
   p.window = a.scores.window > 0 && a.scores.window < (1 << 25) ? a.scores.window : 1 << 25;
   p.group = a.q_heads / a.kv_heads;
   const Cut c = cut_for(a.Tq, a.Tk, a.B, a.q_heads, a.kv_heads, a.head_dim);
