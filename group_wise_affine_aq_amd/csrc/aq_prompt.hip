@@ -271,15 +271,18 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
   }
   const float slope = a.scores.slopes ? a.scores.slopes[qh] * kLog2e : 0.f;
 
-  // the rows of a tile of keys or values; those past the sequence read as zeros,
+  // the rows of a tile of keys or values (counted from t0); those past the sequence read as zeros,
   // without a memory access
-  auto rows_of = [&](const uint16_t *x, int64_t stride, int tile) {
-    const int left = seq.len - tile * KT, there = left < KT ? left : KT;
-    const uint64_t at = reinterpret_cast<uint64_t>(x + ((int64_t)seq.k0 + tile * KT) * stride + (int64_t)head * D);
+  const int k_step = (int)a.k_stride * 2, v_step = (int)a.v_stride * 2;  // bytes of a token
+  const int64_t row0 = (int64_t)seq.k0 + (int64_t)t0 * KT;
+  const uint64_t k0 = reinterpret_cast<uint64_t>(a.k + row0 * a.k_stride + (int64_t)head * D);
+  const uint64_t v0 = reinterpret_cast<uint64_t>(a.v + row0 * a.v_stride + (int64_t)head * D);
+  auto rows_of = [&](uint64_t base, int step, int tile) {
+    const uint64_t at = base + (uint64_t)(uint32_t)tile * (uint32_t)(step * KT);
     const uint32_t alo = uniform((int)(uint32_t)at), ahi = uniform((int)(uint32_t)(at >> 32));
-    const int bytes = there > 0 ? (int)((there - 1) * stride * 2) + S::RB : 0;
+    const int left = seq.len - (t0 + tile) * KT, there = left < KT ? left : KT;
     return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(((uint64_t)ahi << 32) | alo), 0,
-                                             uniform(bytes), 0x00020000);
+                                             uniform(there > 0 ? (there - 1) * step + S::RB : 0), 0x00020000);
   };
   // Keys of tile `due` and values of the one before it (tiles counted from t0) go straight to
   // LDS, a kilobyte a load, the lanes' pieces in the order in which LDS has them.  The compiler
@@ -291,11 +294,11 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
 #pragma unroll
   for (int e = 0; e < EACH; ++e) {
     const int at = (wave * EACH + e) * 64 + lane, r = at / S::CH, c = at % S::CH;
-    from_k[e] = r * (int)a.k_stride * 2 + (c ^ S::key_swap(r)) * 16;
-    from_v[e] = r * (int)a.v_stride * 2 + (c ^ S::value_swap(r)) * 16;
+    from_k[e] = r * k_step + (c ^ S::key_swap(r)) * 16;
+    from_v[e] = r * v_step + (c ^ S::value_swap(r)) * 16;
   }
-  auto fetch = [&](const int *from, const uint16_t *x, int64_t stride, int tile, int to) {
-    const Span span = rows_of(x, stride, t0 + tile);
+  auto fetch = [&](const int *from, uint64_t first, int step, int tile, int to) {
+    const Span span = rows_of(first, step, tile);
     const uint32_t base = (uint32_t)uniform((int)(uint32_t)(uintptr_t)mem + to + wave * (EACH * 1024));
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
@@ -308,13 +311,13 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
   auto arrived = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
   bool careful = false;  // values are looked at on their way
   auto bring = [&] {
-    if (due < tiles) fetch(from_k, a.k, a.k_stride, due, (due & 1) * S::TILE);
+    if (due < tiles) fetch(from_k, k0, k_step, due, (due & 1) * S::TILE);
     if (due > 0 && due <= tiles) {
       const int half = (due - 1) & 1, to = (2 + half) * S::TILE;
       if (!careful) {
-        fetch(from_v, a.v, a.v_stride, due - 1, to);
+        fetch(from_v, v0, v_step, due - 1, to);
       } else {
-        const Span span = rows_of(a.v, a.v_stride, t0 + due - 1);
+        const Span span = rows_of(v0, v_step, due - 1);
         uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
@@ -361,7 +364,7 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
         s[x] = mfma<BF>(frag, q[k], s[x]);
       }
   };
-  auto gather = [&](int t) {
+  auto gather = [&] {
     // the values: 4 tokens x 16 values a group of 16 lanes
     auto value_operand = [&](int i, int k) {
       const lds_char *from = mem + at_v[i % NV] + (16 * k * S::RB + i / NV * 256);
@@ -374,14 +377,15 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
     for (int k = 0; k < KK; ++k)
 #pragma unroll
       for (int i = 0; i < DB; ++i) o[i] = mfma<BF>(value_operand(i, k), w[k], o[i]);
-
+  };
+  auto gather_odd = [&](int t) {
     if (!careful) return;
     int odd = 0;
 #pragma unroll
     for (int x = 0; x < NW; ++x) odd |= odd_tile[(t - t0) & 1][x];
     if (uniform(odd)) {
       const int key0 = t * KT;
-      const Span span = rows_of(a.v, a.v_stride, t);
+      const Span span = rows_of(v0, v_step, t - t0);
 #pragma unroll 1
       for (int x = 0; x < KT; ++x) {
         const bool in = (uint32_t)(key0 + x - lo) < (uint32_t)(hi - lo);
@@ -390,7 +394,7 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             const u32x2v v = __builtin_bit_cast(u32x2v, __builtin_amdgcn_raw_buffer_load_b64(
-                span, x * (int)a.v_stride * 2 + (32 * i + 2 * j + 4 * h) * 2, 0, 0));
+                span, x * v_step + (32 * i + 2 * j + 4 * h) * 2, 0, 0));
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               const float z = half_of<BF>(odd_pair<BF>(v[y >> 1]), y & 1);
@@ -414,6 +418,11 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
   m = kNegInf, l = 0.f;
   have = false;
 #pragma unroll
+  for (int k = 0; k < KK; ++k) w[k] = u32x4v{0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < EACH; ++e)  // (the values that the first weights of 0 meet)
+    *(lds_u32x4 *)(mem + 3 * S::TILE + ((wave * EACH + e) * 64 + lane) * 16) = u32x4v{0, 0, 0, 0};
+#pragma unroll
   for (int k = 0; k < NK; ++k) at_k[k] = S::key_piece(lane & 31, 2 * k + h);
 #pragma unroll
   for (int i = 0; i < NV; ++i) at_v[i] = 3 * S::TILE + S::value_piece(vr, (32 * i + vc) >> 3) + (vc & 7) * 2;
@@ -430,8 +439,27 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
     const bool need = key0 < most && key0 + KT > least;
     if (!late) bring();
     __builtin_amdgcn_s_setprio(1);
-    if (need) multiply();
-    if (have) gather(t - 1);
+    if (need || have) {
+      // Both products without a branch between them: a wave's first tile finds weights of 0 and
+      // finite values, the one behind its last makes scores that nobody takes.  Operands are fetched ahead of the products that take them: 8 of the keys', then 8 of the
+      // values' (two reads each).  Left to itself the compiler waits for every pair.
+      multiply();
+      gather();
+      constexpr int kProduct = 0x8, kRead = 0x100;
+      __builtin_amdgcn_sched_group_barrier(kRead, 8, 0);
+#pragma unroll
+      for (int i = 0; i < X * KS - 8; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kProduct, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < DB * KK; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kProduct, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(kProduct, 8, 0);
+    }
+    if (have) gather_odd(t - 1);
     __builtin_amdgcn_s_setprio(0);
 #pragma unroll
     for (int k = 0; k < NK; ++k) at_k[k] ^= S::TILE;
@@ -534,7 +562,10 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
     if (!late) arrived();
     barrier();
   }
-  if (have) gather(t1 - 1);
+  if (have) {
+    gather();
+    gather_odd(t1 - 1);
+  }
   if (NW == 8 && !late) barrier();
 
   // An infinity or NaN among the values has reached all rows of the waves that multiplied it, by a
