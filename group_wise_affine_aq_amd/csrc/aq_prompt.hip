@@ -179,6 +179,8 @@ __device__ __forceinline__ float half_of(uint32_t w, int i) {
   return BF ? bf16_to_f32((uint16_t)(w >> (16 * i))) : f16_to_f32((uint16_t)(w >> (16 * i)));
 }
 
+template <int N> struct Count { static constexpr int value = N; };
+
 // the largest of a lane's scores, or of their magnitudes
 template <int X>
 __device__ __forceinline__ float largest(const f32x16v (&s)[X], bool magnitude) {
@@ -351,33 +353,47 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
   f32x16v s[X];
   u32x4v w[KK];
   bool have = false;  // (w: a tile that no row of the wave sees has none)
-  auto multiply = [&] {
+  auto value_operand = [&](int i, int k) {  // 4 tokens x 16 values a group of 16 lanes, twice
+    const lds_char *from = mem + at_v[i % NV] + (16 * k * S::RB + i / NV * 256);
+    const s16x4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)from);
+    const s16x4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(from + 8 * S::RB));
+    const u32x2v u = __builtin_bit_cast(u32x2v, x), v = __builtin_bit_cast(u32x2v, y);
+    return u32x4v{u[0], u[1], v[0], v[1]};
+  };
+  // Operands are fetched kAhead products ahead of theirs, and stay kHold products longer: a read into
+  // registers that a product under way still takes its operand from waits for that product (reads
+  // right behind the product that frees their registers, as the compiler would have them: 66 cycles a
+  // product instead of 34).
+  auto multiply = [&](auto first, auto last) {
+    constexpr int NKEYS = X * KS, FIRST = decltype(first)::value, N = decltype(last)::value - FIRST;
+    constexpr int kAhead = 6, kHold = 2;
+    if constexpr (FIRST == 0)
 #pragma unroll
-    for (int x = 0; x < X; ++x)
+      for (int x = 0; x < X; ++x)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) s[x][j] = 0.f;
+        for (int j = 0; j < 16; ++j) s[x][j] = 0.f;
+    u32x4v f[N];
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int x = 0; x < X; ++x) {
-        const u32x4v frag = *(const lds_u32x4 *)(mem + at_k[k % NK] + (32 * x * S::RB + k / NK * 256));
-        s[x] = mfma<BF>(frag, q[k], s[x]);
+    for (int n = 0; n < N + kAhead; ++n) {
+      if (n < N) {
+        const int i = FIRST + n, j = i - NKEYS;
+        f[n] = i < NKEYS ? *(const lds_u32x4 *)(mem + at_k[i / X % NK] + (32 * (i % X) * S::RB + i / X / NK * 256))
+                         : value_operand(j % DB, j / DB);
       }
+      __builtin_amdgcn_sched_barrier(0);
+      if (n >= kAhead) {
+        const int d = n - kAhead, i = FIRST + d, j = i - NKEYS;
+        if (i < NKEYS)
+          s[i % X] = mfma<BF>(f[d], q[i / X], s[i % X]);
+        else
+          o[j % DB] = mfma<BF>(f[d], w[j / DB], o[j % DB]);
+        if (d >= kHold) asm volatile("" ::"v"(f[d - kHold]));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
-  auto gather = [&] {
-    // the values: 4 tokens x 16 values a group of 16 lanes
-    auto value_operand = [&](int i, int k) {
-      const lds_char *from = mem + at_v[i % NV] + (16 * k * S::RB + i / NV * 256);
-      const s16x4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)from);
-      const s16x4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(from + 8 * S::RB));
-      const u32x2v u = __builtin_bit_cast(u32x2v, x), v = __builtin_bit_cast(u32x2v, y);
-      return u32x4v{u[0], u[1], v[0], v[1]};
-    };
-#pragma unroll
-    for (int k = 0; k < KK; ++k)
-#pragma unroll
-      for (int i = 0; i < DB; ++i) o[i] = mfma<BF>(value_operand(i, k), w[k], o[i]);
-  };
+  constexpr Count<X * KS> keys_end;
+  constexpr Count<X * KS + DB * KK> both_end;
   auto gather_odd = [&](int t) {
     if (!careful) return;
     int odd = 0;
@@ -441,23 +457,8 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
     __builtin_amdgcn_s_setprio(1);
     if (need || have) {
       // Both products without a branch between them: a wave's first tile finds weights of 0 and
-      // finite values, the one behind its last makes scores that nobody takes.  Operands are fetched ahead of the products that take them: 8 of the keys', then 8 of the
-      // values' (two reads each).  Left to itself the compiler waits for every pair.
-      multiply();
-      gather();
-      constexpr int kProduct = 0x8, kRead = 0x100;
-      __builtin_amdgcn_sched_group_barrier(kRead, 8, 0);
-#pragma unroll
-      for (int i = 0; i < X * KS - 8; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kProduct, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < DB * KK; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kProduct, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
-      }
-      __builtin_amdgcn_sched_group_barrier(kProduct, 8, 0);
+      // finite values, the one behind its last makes scores that nobody takes.
+      multiply(Count<0>(), both_end);
     }
     if (have) gather_odd(t - 1);
     __builtin_amdgcn_s_setprio(0);
@@ -563,7 +564,7 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
     barrier();
   }
   if (have) {
-    gather();
+    multiply(keys_end, both_end);
     gather_odd(t1 - 1);
   }
   if (NW == 8 && !late) barrier();
