@@ -61,7 +61,7 @@ struct Params {
   uint32_t flip;   // sign of the scale, for pairs of queries
   // caps: cap2 (in powers of two; 0: none), what brings a score s to 2 log2 e times tanh's
   // argument; where |s| <= small the cap is s times a polynomial in s^2
-  float cap2, twice, small, cap[5];
+  float cap2, twice, small, cap[5], smaller, cap3[3];
   int window, group;
   int tiles;       // of query rows, at most, of all sequences
   int parts;       // of every tile's keys
@@ -199,6 +199,10 @@ __device__ __forceinline__ float cap_factor(const Params &p, float s) {
   f = __builtin_fmaf(u, f, p.cap[1]);
   return __builtin_fmaf(u, f, p.cap[0]);
 }
+__device__ __forceinline__ float cap_factor_3(const Params &p, float s) {  // below p.smaller
+  const float u = s * s;
+  return __builtin_fmaf(u, __builtin_fmaf(u, p.cap3[2], p.cap3[1]), p.cap3[0]);
+}
 __device__ __forceinline__ float small_cap(const Params &p, float s) { return s * cap_factor(p, s); }
 
 template <bool BF, int D, int NW>
@@ -273,23 +277,26 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
   }
   const float slope = a.scores.slopes ? a.scores.slopes[qh] * kLog2e : 0.f;
 
-  // the rows of a tile of keys or values (counted from t0); those past the sequence read as zeros,
-  // without a memory access
+  // the rows of a tile of keys or values (counted from t0); those past the sequence, and all of a tile
+  // past the last, read as zeros, without a memory access
   const int k_step = (int)a.k_stride * 2, v_step = (int)a.v_stride * 2;  // bytes of a token
   const int64_t row0 = (int64_t)seq.k0 + (int64_t)t0 * KT;
-  const uint64_t k0 = reinterpret_cast<uint64_t>(a.k + row0 * a.k_stride + (int64_t)head * D);
-  const uint64_t v0 = reinterpret_cast<uint64_t>(a.v + row0 * a.v_stride + (int64_t)head * D);
+  auto scalar = [](const void *x) {
+    const uint64_t u = reinterpret_cast<uint64_t>(x);
+    return (uint64_t)(uint32_t)uniform((int)(u >> 32)) << 32 | (uint32_t)uniform((int)(uint32_t)u);
+  };
+  const uint64_t k0 = scalar(a.k + row0 * a.k_stride + (int64_t)head * D);
+  const uint64_t v0 = scalar(a.v + row0 * a.v_stride + (int64_t)head * D);
+  const int keys_left = (t1 * KT < seq.len ? t1 * KT : seq.len) - t0 * KT;
   auto rows_of = [&](uint64_t base, int step, int tile) {
     const uint64_t at = base + (uint64_t)(uint32_t)tile * (uint32_t)(step * KT);
-    const uint32_t alo = uniform((int)(uint32_t)at), ahi = uniform((int)(uint32_t)(at >> 32));
-    const int left = seq.len - (t0 + tile) * KT, there = left < KT ? left : KT;
-    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(((uint64_t)ahi << 32) | alo), 0,
-                                             uniform(there > 0 ? (there - 1) * step + S::RB : 0), 0x00020000);
+    const int left = keys_left - tile * KT, there = left < KT ? left : KT;
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(at), 0,
+                                             there > 0 ? (there - 1) * step + S::RB : 0, 0x00020000);
   };
   // Keys of tile `due` and values of the one before it (tiles counted from t0) go straight to
   // LDS, a kilobyte a load, the lanes' pieces in the order in which LDS has them.  The compiler
   // does not know of these loads: arrived() waits for them.
-  const int tiles = t1 - t0;
   int due = 0;
   lds_char *const mem = (lds_char *)lds;
   int from_k[EACH], from_v[EACH];
@@ -301,7 +308,7 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
   }
   auto fetch = [&](const int *from, uint64_t first, int step, int tile, int to) {
     const Span span = rows_of(first, step, tile);
-    const uint32_t base = (uint32_t)uniform((int)(uint32_t)(uintptr_t)mem + to + wave * (EACH * 1024));
+    const uint32_t base = (uint32_t)(uintptr_t)mem + to + wave * (EACH * 1024);
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
       uint32_t kept;  // (m0, which the compiler may have a use for)
@@ -313,8 +320,8 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
   auto arrived = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
   bool careful = false;  // values are looked at on their way
   auto bring = [&] {
-    if (due < tiles) fetch(from_k, k0, k_step, due, (due & 1) * S::TILE);
-    if (due > 0 && due <= tiles) {
+    fetch(from_k, k0, k_step, due, (due & 1) * S::TILE);
+    if (due > 0) {
       const int half = (due - 1) & 1, to = (2 + half) * S::TILE;
       if (!careful) {
         fetch(from_v, v0, v_step, due - 1, to);
@@ -423,8 +430,9 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
 
   // Two groups of waves, each with a wave on every SIMD, take turns: while one multiplies the other
   // has the softmax, half a tile later.  Their phases are counted from 0; the earlier group multiplies
-  // tile t in phase 2 t, the later one in phase 2 t + 1.  The keys of tile t + 1 and the values of t are
-  // brought in the phases 2 t and 2 t + 1: what their place held was last read in phase 2 t - 1.
+  // tile t in phase 2 t, the later one in phase 2 t + 1.  As it begins each asks for its threads' share of
+  // the keys of tile t + 1 and the values of t, whose place was last read in phase 2 t - 1; they are
+  // there at the end of phase 2 t + 1.  (The softmax is the longer half of a tile: nothing else is in it.)
   const bool late = NW == 8 && wave >= NW / 2;
   for (;;) {
 #pragma unroll
@@ -446,14 +454,11 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
   bring();
   arrived();
   barrier();
-  if (late) {
-    bring();
-    barrier();
-  }
+  if (late) barrier();
   for (int t = t0; t < t1; ++t) {
     const int key0 = t * KT;
     const bool need = key0 < most && key0 + KT > least;
-    if (!late) bring();
+    bring();
     __builtin_amdgcn_s_setprio(1);
     if (need || have) {
       // Both products without a branch between them: a wave's first tile finds weights of 0 and
@@ -468,7 +473,6 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
     for (int i = 0; i < NV; ++i) at_v[i] ^= S::TILE;
     if (late) arrived();
     barrier();
-    if (late) bring();
     if (need) {
       // Scores in powers of two are t = s C, or its cap.  Three ways there, by what the wave has
       // (each of s, C and the cap's polynomial fused with the subtraction of m where it can be):
@@ -482,11 +486,11 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
         way = 1;
       } else if (simple) {
         top = largest(s, true);
-        if (__ballot(!(top <= p.small)) == 0) way = 2;
+        if (__ballot(!(top <= p.small)) == 0) way = __ballot(!(top <= p.smaller)) == 0 ? 3 : 2;
       }
       if (way == 1) {
         top *= p.C;
-      } else if (way == 2) {
+      } else if (way) {
         top = small_cap(p, top);
       } else {
         if (p.cap2 != 0.f) {
@@ -525,7 +529,7 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
       }
       // (the lane's own half of the row, or what no score of it is above: enough to know that m stays)
       if (__ballot(top - m > kUp)) {
-        if (way == 2) top = small_cap(p, largest(s, false));
+        if (way > 1) top = small_cap(p, largest(s, false));
         top = __builtin_fmaxf(top, other_half(top));
         const bool over = top - m > kUp;
         // (scores past 2^23 have no room for kUp: their weights are 1 at most)
@@ -555,6 +559,8 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
         weigh([&](float y) { return __builtin_fmaf(y, p.C, -base); });
       else if (way == 2)
         weigh([&](float y) { return __builtin_fmaf(y, cap_factor(p, y), -base); });
+      else if (way == 3)
+        weigh([&](float y) { return __builtin_fmaf(y, cap_factor_3(p, y), -base); });
       else
         weigh([&](float y) { return y - base; });
 
@@ -679,22 +685,29 @@ Cut cut_for(int64_t Tq, int64_t Tk, int64_t B, int q_heads, int kv_heads, int D)
   return c;
 }
 
-// tanh y / y = sum c_i y^2i within 2^-23 for |y| <= 0.6 (a fit of the least largest relative
-// error), so the cap of a small score costs five operations and no exponential or reciprocal:
-// these take four times as long each, and the softmax is what bounds the kernel.
+// tanh y / y = sum c_i y^2i: five terms within 2^-23 for |y| <= 0.6, three within 2^-23 for |y| <= 0.2
+// (fits of the least largest relative error).  So the cap of a small score costs five operations or
+// three and no exponential or reciprocal, which take twice as long each: the softmax is the longer half
+// of a tile (8192 tokens, cap 50: 754 us with them, 718 without).
 void set_cap(Params &p) {
   constexpr double c[5] = {0.9999999268660705, -0.33332309948977934, 0.13310173306949546,
                            -0.05210146457599173, 0.015475405965029628};
-  p.twice = 0.f, p.small = -1.f;
+  constexpr double c3[3] = {0.999999894791025, -0.33328590894235166, 0.1301540743838377};
+  p.twice = 0.f, p.small = p.smaller = -1.f;
   for (float &x : p.cap) x = 0.f;
+  for (float &x : p.cap3) x = 0.f;
   if (p.cap2 == 0.f) return;
   const double y = (double)p.C / p.cap2;
   p.twice = (float)(2 * y * 1.4426950408889634);
   const double small = 0.6 / y;
   if (!(small > 1e-3 && small < 1e9)) return;  // (powers of scores within binary32)
   double f = p.C;
-  for (int i = 0; i < 5; ++i, f *= y * y) p.cap[i] = (float)(c[i] * f);
+  for (int i = 0; i < 5; ++i, f *= y * y) {
+    p.cap[i] = (float)(c[i] * f);
+    if (i < 3) p.cap3[i] = (float)(c3[i] * f);
+  }
   p.small = (float)small;
+  p.smaller = (float)(0.2 / y);
 }
 
 template <bool BF, int D, int NW>
