@@ -199,10 +199,6 @@ __device__ __forceinline__ float cap_factor(const Params &p, float s) {
   f = __builtin_fmaf(u, f, p.cap[1]);
   return __builtin_fmaf(u, f, p.cap[0]);
 }
-__device__ __forceinline__ float cap_factor_3(const Params &p, float s) {  // below p.smaller
-  const float u = s * s;
-  return __builtin_fmaf(u, __builtin_fmaf(u, p.cap3[2], p.cap3[1]), p.cap3[0]);
-}
 __device__ __forceinline__ float small_cap(const Params &p, float s) { return s * cap_factor(p, s); }
 
 template <bool BF, int D, int NW>
@@ -428,11 +424,13 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
     }
   };
 
-  // Two groups of waves, each with a wave on every SIMD, take turns: while one multiplies the other
-  // has the softmax, half a tile later.  Their phases are counted from 0; the earlier group multiplies
-  // tile t in phase 2 t, the later one in phase 2 t + 1.  As it begins each asks for its threads' share of
-  // the keys of tile t + 1 and the values of t, whose place was last read in phase 2 t - 1; they are
-  // there at the end of phase 2 t + 1.  (The softmax is the longer half of a tile: nothing else is in it.)
+  // Two groups of waves, each with a wave on every SIMD, half a tile apart: between two barriers the
+  // earlier one multiplies tile t and has its softmax, the later one has the softmax of tile t - 1 and
+  // multiplies tile t.  So one group's products run beside the other's vector work, as far as the one
+  // is as long as the other; the later group's softmax goes first where both have vector work, since
+  // its products still follow it (8192 tokens capped 647 us without, 607 so).  Behind the barrier
+  // every wave asks for its share of the keys of tile t + 1 and the values of t, whose place was last
+  // read ahead of it.
   const bool late = NW == 8 && wave >= NW / 2;
   for (;;) {
 #pragma unroll
@@ -451,28 +449,30 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
 #pragma unroll
   for (int i = 0; i < NV; ++i) at_v[i] = 3 * S::TILE + S::value_piece(vr, (32 * i + vc) >> 3) + (vc & 7) * 2;
   due = 0;
+  auto next = [&] {
+    arrived();
+    barrier();
+    bring();
+  };
   bring();
-  arrived();
-  barrier();
-  if (late) barrier();
+  next();
   for (int t = t0; t < t1; ++t) {
     const int key0 = t * KT;
     const bool need = key0 < most && key0 + KT > least;
-    bring();
-    __builtin_amdgcn_s_setprio(1);
     if (need || have) {
       // Both products without a branch between them: a wave's first tile finds weights of 0 and
       // finite values, the one behind its last makes scores that nobody takes.
       multiply(Count<0>(), both_end);
     }
     if (have) gather_odd(t - 1);
-    __builtin_amdgcn_s_setprio(0);
 #pragma unroll
     for (int k = 0; k < NK; ++k) at_k[k] ^= S::TILE;
 #pragma unroll
     for (int i = 0; i < NV; ++i) at_v[i] ^= S::TILE;
-    if (late) arrived();
-    barrier();
+    if (late) {
+      next();
+      __builtin_amdgcn_s_setprio(1);
+    }
     if (need) {
       // Scores in powers of two are t = s C, or its cap.  Three ways there, by what the wave has
       // (each of s, C and the cap's polynomial fused with the subtraction of m where it can be):
@@ -544,36 +544,54 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
           for (int j = 0; j < 16; ++j) o[i][j] *= keep;
       }
       const float base = m == kNegInf ? 0.f : m;
-      auto weigh = [&](auto score) {
+      // eight scores at a time, one step of all of them after the other: a result is not there for the
+      // next instruction, and left to itself the compiler would take it in the next but one
+      auto weigh = [&](auto... steps) {
 #pragma unroll
         for (int x = 0; x < X; ++x)
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float e0 = exp2_fast(score(s[x][j])), e1 = exp2_fast(score(s[x][j + 1]));
-            l += e0;
-            l += e1;
-            w[2 * x + (j >> 3)][(j & 7) >> 1] = pack<BF>(e0, e1);
+          for (int j0 = 0; j0 < 16; j0 += 8) {
+            float u[8], f[8];
+            auto all = [&](auto step) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) step(s[x][j0 + j], u[j], f[j]);
+              __builtin_amdgcn_sched_barrier(0);
+            };
+            (all(steps), ...);
+            all([](float, float &, float &e) { e = exp2_fast(e); });
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+              w[2 * x + (j0 >> 3)][j >> 1] = pack<BF>(f[j], f[j + 1]);
+              u[j] = f[j] + f[j + 1];
+            }
+            l += (u[0] + u[2]) + (u[4] + u[6]);
           }
       };
+      auto square = [](float y, float &u, float &) { u = y * y; };
+      auto less_base = [&](float y, float &, float &f) { f = __builtin_fmaf(y, f, -base); };
       if (way == 1)
-        weigh([&](float y) { return __builtin_fmaf(y, p.C, -base); });
+        weigh([&](float y, float &, float &f) { f = __builtin_fmaf(y, p.C, -base); });
       else if (way == 2)
-        weigh([&](float y) { return __builtin_fmaf(y, cap_factor(p, y), -base); });
+        weigh(square, [&](float, float &u, float &f) { f = __builtin_fmaf(u, p.cap[4], p.cap[3]); },
+              [&](float, float &u, float &f) { f = __builtin_fmaf(u, f, p.cap[2]); },
+              [&](float, float &u, float &f) { f = __builtin_fmaf(u, f, p.cap[1]); },
+              [&](float, float &u, float &f) { f = __builtin_fmaf(u, f, p.cap[0]); }, less_base);
       else if (way == 3)
-        weigh([&](float y) { return __builtin_fmaf(y, cap_factor_3(p, y), -base); });
+        weigh(square, [&](float, float &u, float &f) { f = __builtin_fmaf(u, p.cap3[2], p.cap3[1]); },
+              [&](float, float &u, float &f) { f = __builtin_fmaf(u, f, p.cap3[0]); }, less_base);
       else
-        weigh([&](float y) { return y - base; });
+        weigh([&](float y, float &, float &f) { f = y - base; });
 
     }
     have = need;
-    if (!late) arrived();
-    barrier();
+    if (late) __builtin_amdgcn_s_setprio(0);
+    if (!late) next();
   }
   if (have) {
     multiply(keys_end, both_end);
     gather_odd(t1 - 1);
   }
-  if (NW == 8 && !late) barrier();
+  arrived();
 
   // An infinity or NaN among the values has reached all rows of the waves that multiplied it, by a
   // weight of 0 too: then once more, with care.
