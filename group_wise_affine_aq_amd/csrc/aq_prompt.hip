@@ -482,8 +482,9 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
       float top;
       int way = 0;
       if (simple && p.cap2 == 0.f) {
+        // (a score past 2^23 has no room for what its product with C is rounded by)
         top = largest(s, false);
-        way = 1;
+        if (__ballot(!(__builtin_fabsf(top * p.C) < 0x1p23f)) == 0) way = 1;
       } else if (simple) {
         top = largest(s, true);
         if (__ballot(!(top <= p.small)) == 0) way = __ballot(!(top <= p.smaller)) == 0 ? 3 : 2;
@@ -718,7 +719,8 @@ void set_cap(Params &p) {
   const double y = (double)p.C / p.cap2;
   p.twice = (float)(2 * y * 1.4426950408889634);
   const double small = 0.6 / y;
-  if (!(small > 1e-3 && small < 1e9)) return;  // (powers of scores within binary32)
+  // (powers of scores are within binary32, and what is small has room for its rounding)
+  if (!(small > 1e-3 && small < 1e9 && small * p.C < 0x1p22)) return;
   double f = p.C;
   for (int i = 0; i < 5; ++i, f *= y * y) {
     p.cap[i] = (float)(c[i] * f);
