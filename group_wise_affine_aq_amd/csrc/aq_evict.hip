@@ -43,7 +43,9 @@ __device__ __forceinline__ uint32_t lanes_before(uint64_t m) {
 }
 
 __global__ __launch_bounds__(kSelect) void select_kernel(EvictArgs a, KvCache c) {
-  __shared__ uint32_t bins[256], count_gt[kWaves], count_eq[kWaves];
+  constexpr int U = 16;      // tokens of a lane whose weights are fetched at once
+  constexpr int kCopies = 8; // of the counts: equal digits are counted one after the other
+  __shared__ uint32_t bins[kCopies][256 + 4], count_gt[kWaves], count_eq[kWaves];
   __shared__ uint32_t found, left;
   const int b = blockIdx.x, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = clamped(a, c, b);
@@ -62,22 +64,50 @@ __global__ __launch_bounds__(kSelect) void select_kernel(EvictArgs a, KvCache c)
   // candidates: sinks <= i < n - recent, of which `want` are kept
   const int lo = a.sinks, hi = n - a.recent;
   const uint32_t want = (uint32_t)(a.keep - a.sinks - a.recent);
+  // a wave's run of neighbouring tokens, in whole ballots; the keys of a run that is no longer than a
+  // round stay in registers, others are fetched again for every pass
+  const int per = (n + kSelect - 1) / kSelect * 64;
+  const int begin = wave * per < n ? wave * per : n, end = begin + per < n ? begin + per : n;
+  uint32_t keys[U];
+  auto fetch = [&](int i0) {
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * 64 + lane;
+      x[u] = w[i < end ? i : 0];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) keys[u] = key_of(x[u]);
+  };
+  const bool once = per <= U * 64;
+  if (once) fetch(begin);
+
   uint32_t key = 0, mask = 0, rest = want;
   if (want) {
     for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += kSelect) bins[i] = 0;
+      for (int i = threadIdx.x; i < kCopies * 260; i += kSelect) (&bins[0][0])[i] = 0;
       __syncthreads();
-      for (int i = lo + (int)threadIdx.x; i < hi; i += kSelect) {
-        const uint32_t k = key_of(w[i]);
-        if ((k & mask) == key) atomicAdd(&bins[(k >> shift) & 255], 1u);
+      for (int i0 = begin; i0 < end; i0 += U * 64) {
+        if (!once) fetch(i0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * 64 + lane;
+          if (i < end && i >= lo && i < hi && (keys[u] & mask) == key)
+            atomicAdd(&bins[lane & (kCopies - 1)][(keys[u] >> shift) & 255], 1u);
+        }
       }
       __syncthreads();
       if (wave == 0) {
         // from the top: the digit in which the count passes `rest`; lane l has the digits
         // 255 - 4 l down to 252 - 4 l
-        uint32_t own[4], sum = 0;
+        uint32_t own[4] = {0, 0, 0, 0}, sum = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum += own[j] = bins[255 - 4 * lane - j];
+        for (int x = 0; x < kCopies; ++x) {
+          const uint4 four = *reinterpret_cast<const uint4 *>(&bins[x][252 - 4 * lane]);
+          own[0] += four.w, own[1] += four.z, own[2] += four.y, own[3] += four.x;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum += own[j];
         uint32_t upto = sum;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -88,7 +118,9 @@ __global__ __launch_bounds__(kSelect) void select_kernel(EvictArgs a, KvCache c)
         if (lane == __builtin_ctzll(past)) {
           uint32_t before = upto - sum;
           int j = 0;
-          while (j < 3 && before + own[j] < rest) before += own[j++];
+#pragma unroll
+          for (int x = 0; x < 3; ++x)
+            if (j == x && before + own[x] < rest) before += own[x], ++j;
           found = 255 - 4 * lane - j;
           left = rest - before;
         }
@@ -101,39 +133,45 @@ __global__ __launch_bounds__(kSelect) void select_kernel(EvictArgs a, KvCache c)
     }
   }
   // larger keys are kept, and the first `rest` equal ones (none of no candidates)
-  const int per = ((n + kSelect - 1) / kSelect) * 64;  // a wave's run, whole ballots
-  const int begin = wave * per < n ? wave * per : n, end = begin + per < n ? begin + per : n;
-  auto look = [&](int i, uint64_t &gt, uint64_t &eq) {
+  auto look = [&](int i, uint32_t k, uint64_t &gt, uint64_t &eq) {
     const bool in = i < end, edge = i < lo || i >= hi;
-    const uint32_t k = in && !edge ? key_of(w[i]) : 0;
     gt = __ballot(in && (edge || (want && k > key)));
     eq = __ballot(in && !edge && want && k == key);
   };
   uint32_t gts = 0, eqs = 0;
-  for (int i0 = begin; i0 < end; i0 += 64) {
-    uint64_t gt, eq;
-    look(i0 + lane, gt, eq);
-    gts += __builtin_popcountll(gt);
-    eqs += __builtin_popcountll(eq);
+  for (int i0 = begin; i0 < end; i0 += U * 64) {
+    if (!once) fetch(i0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint64_t gt, eq;
+      look(i0 + u * 64 + lane, keys[u], gt, eq);
+      gts += __builtin_popcountll(gt);
+      eqs += __builtin_popcountll(eq);
+    }
   }
   if (lane == 0) count_gt[wave] = gts, count_eq[wave] = eqs;
   __syncthreads();
   uint32_t at = 0, seen = 0;  // kept tokens and equal ones ahead of this run
   for (int x = 0; x < wave; ++x) at += count_gt[x], seen += count_eq[x];
   at += seen < rest ? seen : rest;
-  for (int i0 = begin; i0 < end; i0 += 64) {
-    uint64_t gt, eq;
-    look(i0 + lane, gt, eq);
-    const uint32_t before = lanes_before(eq);
-    const bool in = gt >> lane & 1 || (eq >> lane & 1 && seen + before < rest);
-    const uint64_t all = __ballot(in);
-    if (in) {
-      const uint32_t to = at + lanes_before(all);
-      kept[to] = i0 + lane;
-      got[to] = w[i0 + lane];
+  for (int i0 = begin; i0 < end; i0 += U * 64) {
+    if (!once) fetch(i0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * 64 + lane;
+      uint64_t gt, eq;
+      look(i, keys[u], gt, eq);
+      const uint32_t before = lanes_before(eq);
+      const bool in = gt >> lane & 1 || (eq >> lane & 1 && seen + before < rest);
+      const uint64_t all = __ballot(in);
+      if (in) {
+        const uint32_t to = at + lanes_before(all);
+        kept[to] = i;
+        got[to] = w[i];
+      }
+      at += __builtin_popcountll(all);
+      seen += __builtin_popcountll(eq);
     }
-    at += __builtin_popcountll(all);
-    seen += __builtin_popcountll(eq);
   }
   __syncthreads();
   if (threadIdx.x == 0) a.new_lengths[b] = total;

@@ -20,26 +20,31 @@
 namespace aq {
 namespace {
 
-constexpr int kSpan = 512;         // tokens of a workgroup's strip
-constexpr int kChunk = 4 * kTile;  // tokens of the work line's chunks
+constexpr int WV = 8;       // waves of a workgroup
+constexpr int kSpan = 512;  // tokens of a workgroup's strip
 
-// sum over the 16 lanes of a column's row of lanes, in each of them
-__device__ __forceinline__ float columns_sum(float v) {
-  v += dpp_f<0x128>(v);  // row_ror:8
-  v += dpp_f<0x124>(v);
-  v += dpp_f<0x122>(v);
-  v += dpp_f<0x121>(v);
-  return v;
+// Sums of 8 values over the 16 lanes of a row; a lane gets the sum number lane / 2 % 8.  Partners
+// are lanes that differ in bit 3, then 2, then 1: each time a lane keeps half of what it has, by
+// that bit, and takes its partner's of it.
+__device__ __forceinline__ float columns_sum(const float (&s)[8], int lane) {
+  const bool b3 = lane & 8, b2 = lane & 4, b1 = lane & 2;
+  float x[4], y[2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] = (b3 ? s[j + 4] : s[j]) + dpp_f<0x140>(b3 ? s[j] : s[j + 4]);  // row_mirror
+#pragma unroll
+  for (int j = 0; j < 2; ++j) y[j] = (b2 ? x[j + 2] : x[j]) + dpp_f<0x141>(b2 ? x[j] : x[j + 2]);  // row_half_mirror
+  const float z = (b1 ? y[1] : y[0]) + dpp_f<0x4E>(b1 ? y[0] : y[1]);  // quad_perm [2,3,0,1]
+  return z + dpp_f<0xB1>(z);                                            // quad_perm [1,0,3,2]
 }
 
 template <int BITS, bool BF, int D, int G, int NT>
-__global__ __launch_bounds__(64 * NW, 2) void weigh_kernel(Params p, float *weights, int64_t stride) {
+__global__ __launch_bounds__(64 * WV, 2) void weigh_kernel(Params p, float *weights, int64_t stride) {
   typedef Wave<BITS, BF, D, G, NT, true> W;
   constexpr int STRIP = 128 * W::TB;
-  __shared__ float strips[NW][kSpan];
-  __shared__ __align__(16) char scales[NW][W::QUANT ? STRIP : 16];
+  __shared__ float strips[WV][kSpan];
+  __shared__ __align__(16) char scales[WV][W::QUANT ? STRIP : 16];
   const int wave = uniform(threadIdx.x >> 6);
-  const int heads_at_once = p.kv_heads >= 4 ? 4 : (p.kv_heads >= 2 ? 2 : 1), split = NW / heads_at_once;
+  const int heads_at_once = p.kv_heads >= 8 ? 8 : (p.kv_heads >= 4 ? 4 : (p.kv_heads >= 2 ? 2 : 1)), split = WV / heads_at_once;
   const int head0 = wave % heads_at_once, part = wave / heads_at_once;
 
   Params lp = p;  // the line's units: sequences
@@ -61,15 +66,15 @@ __global__ __launch_bounds__(64 * NW, 2) void weigh_kernel(Params p, float *weig
       len = uniform(clamped_length(p, b));
       chunks = line.chunks(lp, b, len);
     }
-    // chunks c0 .. c1 of sequence b, at most a strip's worth
-    const uint32_t c0 = pos - before;
-    uint32_t n = end - pos < chunks - c0 ? end - pos : chunks - c0;
-    n = n < kSpan / kChunk ? n : kSpan / kChunk;
+    // chunks c0 .. of sequence b, a strip's worth of tiles at a time
+    const uint32_t c0 = pos - before, n = end - pos < chunks - c0 ? end - pos : chunks - c0;
     pos += n;
-    const int base = uniform(first_tile<true>(p, b, len));
-    const int tiles = (len + kTile - 1) / kTile, tile0 = base + (int)c0 * (kChunk / kTile);
-    int tile1 = tile0 + (int)n * (kChunk / kTile);
-    tile1 = tile1 < tiles ? tile1 : tiles;
+    const int base = uniform(first_tile<true>(p, b, len)), per = (int)(line.chunk / kTile);
+    const int tiles = (len + kTile - 1) / kTile;
+    int last_tile = base + (int)(c0 + n) * per;
+    last_tile = last_tile < tiles ? last_tile : tiles;
+    for (int tile0 = base + (int)c0 * per; tile0 < last_tile; tile0 += kSpan / kTile) {
+    const int tile1 = last_tile - tile0 < kSpan / kTile ? last_tile : tile0 + kSpan / kTile;
 
     const int lane = lane_here(), h = lane >> 4;
     __syncthreads();  // the last strips' readers are done
@@ -147,20 +152,15 @@ __global__ __launch_bounds__(64 * NW, 2) void weigh_kernel(Params p, float *weig
             if constexpr (W::QUANT) W::load_scales(raw, from, rows);
             W::load_keys(k, p, rows, on_next, lane);
             if (edge) st.edge_scores(t, token, on, h);
-            float mine8[8];
+            float sum[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              float sum = exp2_fast(t[0][j] - lse[0]);
+              sum[j] = exp2_fast(t[0][j] - lse[0]);
 #pragma unroll
-              for (int nt = 1; nt < NT; ++nt) sum += exp2_fast(t[nt][j] - lse[nt]);
-              mine8[j] = columns_sum(sum);
+              for (int nt = 1; nt < NT; ++nt) sum[j] += exp2_fast(t[nt][j] - lse[nt]);
             }
-            // lane c adds the sum c % 8 of its four-token groups
-            float add = mine8[0];
-#pragma unroll
-            for (int j = 1; j < 8; ++j) add = (lane & 7) == j ? mine8[j] : add;
-            float *to = &strips[wave][token - tile0 * kTile + 16 * (lane >> 2 & 1) + 4 * h + (lane & 3)];
-            *to += add;
+            float *to = &strips[wave][token - tile0 * kTile + 16 * (lane >> 3 & 1) + 4 * h + (lane >> 1 & 3)];
+            *to += columns_sum(sum, lane);
             on[0] = on_next[0];
             on[1] = on_next[1];
           }
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(64 * NW, 2) void weigh_kernel(Params p, float *weig
       }
     __syncthreads();
     const int64_t most_tokens = stride < len ? stride : len;
-    for (int i = threadIdx.x; i < (tile1 - tile0) * kTile; i += 64 * NW) {
+    for (int i = threadIdx.x; i < (tile1 - tile0) * kTile; i += 64 * WV) {
       const int64_t t = (int64_t)tile0 * kTile + i;
       if (t < most_tokens) {
         float sum = 0.f;
@@ -177,6 +177,7 @@ __global__ __launch_bounds__(64 * NW, 2) void weigh_kernel(Params p, float *weig
         for (int x = 0; x < heads_at_once; ++x) sum += strips[q * heads_at_once + x][i];
         weights[b * stride + t] += sum;
       }
+    }
     }
   }
 }
@@ -194,15 +195,16 @@ hipError_t launch_kv_weigh(const AttnArgs &a, const KvCache &c, float *weights, 
   int nt;
   tiles_for(cols, c.head_dim, nt, p.slices);
   const int64_t cap = a.max_pages * c.page_size;
-  // (the line is counted in chunks of 32 bits)
-  if ((cap + kChunk - 1) / kChunk * a.B > 0x7FFFFFFF) return hipErrorInvalidValue;
-  p.chunk = kChunk;
-  int64_t grid = 2 * device_cus();
-  const int64_t most = (cap + kChunk - 1) / kChunk * a.B;
+  // (the line's chunks are counted in 32 bits: where the table could hold more tiles than that they are longer)
+  int64_t chunk = 2 * kTile;
+  while ((cap + chunk - 1) / chunk * a.B > 0x7FFFFFFF) chunk *= 2;
+  p.chunk = (uint32_t)chunk;
+  int64_t grid = device_cus();
+  const int64_t most = (cap + chunk - 1) / chunk * a.B;
   if (most < grid) grid = most;
   hipError_t err = hipErrorInvalidValue;
 #define AQ_KT(B, F, D, G, T)                                                                    \
-  hipLaunchKernelGGL((weigh_kernel<B, F, D, G, T>), dim3((unsigned)grid), dim3(64 * NW), 0, s, p, \
+  hipLaunchKernelGGL((weigh_kernel<B, F, D, G, T>), dim3((unsigned)grid), dim3(64 * WV), 0, s, p, \
                      weights, stride)
 #define AQ_K(B, F, D, G)               \
   do {                                 \
