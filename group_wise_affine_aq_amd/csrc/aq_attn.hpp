@@ -305,17 +305,6 @@ __device__ __forceinline__ float get_piece1(Span from, int at) {
 // and 44.9 with 40 rows a key head; 59.1 and 53.6 at 16 bits; 195 and 196 for
 // 64 sequences, whose parts are long.  4, 10 and 20 tiles measured the same.)
 
-// inclusive sum over the lanes, a row of 16 and then the rows
-__device__ __forceinline__ uint32_t lanes_prefix(uint32_t v) {
-  v += __builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true);   // row_shr:1
-  v += __builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true);   // row_shr:8
-  v += __builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);  // row_bcast:15
-  v += __builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);  // row_bcast:31
-  return v;
-}
-
 template <bool MORE>
 struct Line {
   uint32_t rows;      // units per sequence

@@ -1,10 +1,10 @@
 // aq_evict.hip -- the tokens of each cached sequence that gathered most of the
 // attention, chosen and moved to other pages (gfx950).
 //
-// Choosing.  One workgroup per sequence finds the least key that is kept, the
-// M-th largest of the candidates' weights, by radix: weights become 32-bit keys
-// in their order, and four counts of 8 bits each narrow down the key, each count
-// over the candidates that share the bits found so far.  Then every wave takes
+// Choosing.  One workgroup per sequence finds the least key that is kept by
+// radix: weights become 32-bit keys in their order, those of the first and last
+// tokens the largest there is, and four counts of 8 bits each narrow down the key, each count
+// over the keys that share the bits found so far.  Then every wave takes
 // a run of neighbouring tokens: it counts the larger keys and the equal ones,
 // the counts of the waves before it say where its own kept tokens go and how
 // many equal ones are still to be taken, and a second pass writes positions
@@ -15,6 +15,7 @@
 // head, keys or values, whose new places are neighbours, 16 bytes a thread and
 // several loads under way.  It is bound by HBM; the choice by the latency of
 // its passes.
+#include "aq_device.hpp"
 #include "aq_internal.hpp"
 
 namespace aq {
@@ -23,12 +24,13 @@ namespace {
 constexpr int kSelect = 1024;  // threads that choose
 constexpr int kWaves = kSelect / 64;
 
-// weights in their order, NaN below everything
+// Weights in their order: NaN, below everything, is 1, and no weight is 0 or
+// kAlways (the patterns of NaNs).
+constexpr uint32_t kNever = 0, kAlways = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t key_of(float w) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, w);
-  if (w != w) return 0;
-  if (w == 0.f) return 0x80000000u;  // -0 and +0 are equal
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t u = __builtin_bit_cast(uint32_t, w + 0.f);  // (-0 and +0 are equal)
+  const uint32_t key = u ^ (0x80000000u | (uint32_t)((int)u >> 31));
+  return w == w ? key : 1u;
 }
 
 __device__ __forceinline__ int clamped(const EvictArgs &a, const KvCache &c, int b) {
@@ -45,8 +47,8 @@ __device__ __forceinline__ uint32_t lanes_before(uint64_t m) {
 __global__ __launch_bounds__(kSelect) void select_kernel(EvictArgs a, KvCache c) {
   constexpr int U = 16;      // tokens of a lane whose weights are fetched at once
   constexpr int kCopies = 8; // of the counts: equal digits are counted one after the other
-  __shared__ uint32_t bins[kCopies][256 + 4], count_gt[kWaves], count_eq[kWaves];
-  __shared__ uint32_t found, left;
+  __shared__ __align__(16) uint32_t bins[4][kCopies][256 + 4];  // of every digit
+  __shared__ uint32_t count_gt[kWaves], count_eq[kWaves];
   const int b = blockIdx.x, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = clamped(a, c, b);
   const float *w = a.weights + (int64_t)b * a.stride;
@@ -61,118 +63,95 @@ __global__ __launch_bounds__(kSelect) void select_kernel(EvictArgs a, KvCache c)
     return;
   }
 
-  // candidates: sinks <= i < n - recent, of which `want` are kept
-  const int lo = a.sinks, hi = n - a.recent;
-  const uint32_t want = (uint32_t)(a.keep - a.sinks - a.recent);
   // a wave's run of neighbouring tokens, in whole ballots; the keys of a run that is no longer than a
-  // round stay in registers, others are fetched again for every pass
+  // round stay in registers, others are made again for every pass.  The first and last tokens have the
+  // largest key, places behind the run one below all, so that the `keep` largest are what is kept.
+  const int lo = a.sinks, hi = n - a.recent;
   const int per = (n + kSelect - 1) / kSelect * 64;
   const int begin = wave * per < n ? wave * per : n, end = begin + per < n ? begin + per : n;
-  uint32_t keys[U];
+  float x[U];
+  uint32_t k[U];
   auto fetch = [&](int i0) {
-    float x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * 64 + lane;
       x[u] = w[i < end ? i : 0];
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) keys[u] = key_of(x[u]);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * 64 + lane;
+      k[u] = i < lo || i >= hi ? kAlways : key_of(x[u]);
+      k[u] = i < end ? k[u] : kNever;
+    }
   };
   const bool once = per <= U * 64;
   if (once) fetch(begin);
-
-  uint32_t key = 0, mask = 0, rest = want;
-  if (want) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < kCopies * 260; i += kSelect) (&bins[0][0])[i] = 0;
-      __syncthreads();
-      for (int i0 = begin; i0 < end; i0 += U * 64) {
-        if (!once) fetch(i0);
+  // (rounds of a run, and within one the ballots that it has)
+  auto every = [&](auto visit) {
+    for (int i0 = begin; i0 < end; i0 += U * 64) {
+      if (!once) fetch(i0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = i0 + u * 64 + lane;
-          if (i < end && i >= lo && i < hi && (keys[u] & mask) == key)
-            atomicAdd(&bins[lane & (kCopies - 1)][(keys[u] >> shift) & 255], 1u);
-        }
-      }
-      __syncthreads();
-      if (wave == 0) {
-        // from the top: the digit in which the count passes `rest`; lane l has the digits
-        // 255 - 4 l down to 252 - 4 l
-        uint32_t own[4] = {0, 0, 0, 0}, sum = 0;
-#pragma unroll
-        for (int x = 0; x < kCopies; ++x) {
-          const uint4 four = *reinterpret_cast<const uint4 *>(&bins[x][252 - 4 * lane]);
-          own[0] += four.w, own[1] += four.z, own[2] += four.y, own[3] += four.x;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum += own[j];
-        uint32_t upto = sum;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const uint32_t x = __shfl_up(upto, d);
-          upto += lane >= d ? x : 0;
-        }
-        const uint64_t past = __ballot(upto >= rest);
-        if (lane == __builtin_ctzll(past)) {
-          uint32_t before = upto - sum;
-          int j = 0;
-#pragma unroll
-          for (int x = 0; x < 3; ++x)
-            if (j == x && before + own[x] < rest) before += own[x], ++j;
-          found = 255 - 4 * lane - j;
-          left = rest - before;
-        }
-      }
-      __syncthreads();
-      key |= found << shift;
-      mask |= 255u << shift;
-      rest = left;
-      __syncthreads();
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * 64 < end) visit(i0 + u * 64 + lane, k[u], x[u]);
     }
-  }
-  // larger keys are kept, and the first `rest` equal ones (none of no candidates)
-  auto look = [&](int i, uint32_t k, uint64_t &gt, uint64_t &eq) {
-    const bool in = i < end, edge = i < lo || i >= hi;
-    gt = __ballot(in && (edge || (want && k > key)));
-    eq = __ballot(in && !edge && want && k == key);
   };
-  uint32_t gts = 0, eqs = 0;
-  for (int i0 = begin; i0 < end; i0 += U * 64) {
-    if (!once) fetch(i0);
+
+  uint32_t key = 0, mask = 0, rest = (uint32_t)a.keep;
+  for (int i = threadIdx.x; i < 4 * kCopies * 260; i += kSelect) (&bins[0][0][0])[i] = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int digit = 0; digit < 4; ++digit) {
+    const int shift = 24 - 8 * digit;
+    uint32_t *mine = bins[digit][lane & (kCopies - 1)];
+    every([&](int, uint32_t k, float) {
+      if ((k & mask) == key) atomicAdd(mine + (k >> shift & 255), 1u);
+    });
+    __syncthreads();
+    // every wave finds, from the top, the digit in which the count passes `rest`; lane l has the
+    // digits 255 - 4 l down to 252 - 4 l
+    uint32_t own[4] = {0, 0, 0, 0}, sum = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      uint64_t gt, eq;
-      look(i0 + u * 64 + lane, keys[u], gt, eq);
-      gts += __builtin_popcountll(gt);
-      eqs += __builtin_popcountll(eq);
+    for (int copy = 0; copy < kCopies; ++copy) {
+      const uint4 four = *reinterpret_cast<const uint4 *>(&bins[digit][copy][252 - 4 * lane]);
+      own[0] += four.w, own[1] += four.z, own[2] += four.y, own[3] += four.x;
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum += own[j];
+    const uint32_t upto = lanes_prefix(sum);
+    const int l = __builtin_ctzll(__ballot(upto >= rest));
+    uint32_t before = upto - sum, found = 255u - 4u * (uint32_t)lane;
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (before + own[j] < rest && found == 255u - 4u * (uint32_t)lane - j) before += own[j], --found;
+    key |= (uint32_t)__builtin_amdgcn_readlane((int)found, l) << shift;
+    mask |= 255u << shift;
+    rest -= (uint32_t)__builtin_amdgcn_readlane((int)before, l);
   }
+  // larger keys are kept, and the first `rest` equal ones
+  uint32_t gts = 0, eqs = 0;
+  every([&](int, uint32_t k, float) { gts += k > key, eqs += k == key; });
+  gts = (uint32_t)__builtin_amdgcn_readlane((int)lanes_prefix(gts), 63);
+  eqs = (uint32_t)__builtin_amdgcn_readlane((int)lanes_prefix(eqs), 63);
   if (lane == 0) count_gt[wave] = gts, count_eq[wave] = eqs;
   __syncthreads();
   uint32_t at = 0, seen = 0;  // kept tokens and equal ones ahead of this run
-  for (int x = 0; x < wave; ++x) at += count_gt[x], seen += count_eq[x];
+  for (int i = 0; i < wave; ++i) at += count_gt[i], seen += count_eq[i];
   at += seen < rest ? seen : rest;
-  for (int i0 = begin; i0 < end; i0 += U * 64) {
-    if (!once) fetch(i0);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * 64 + lane;
-      uint64_t gt, eq;
-      look(i, keys[u], gt, eq);
-      const uint32_t before = lanes_before(eq);
-      const bool in = gt >> lane & 1 || (eq >> lane & 1 && seen + before < rest);
-      const uint64_t all = __ballot(in);
-      if (in) {
-        const uint32_t to = at + lanes_before(all);
-        kept[to] = i;
-        got[to] = w[i];
-      }
-      at += __builtin_popcountll(all);
+  every([&](int i, uint32_t k, float w) {
+    bool in = k > key;
+    const uint64_t eq = __ballot(k == key);
+    if (eq && seen < rest) {
+      in = in || (k == key && seen + lanes_before(eq) < rest);
       seen += __builtin_popcountll(eq);
     }
-  }
+    const uint64_t all = __ballot(in);
+    if (in) {
+      const uint32_t to = at + lanes_before(all);
+      kept[to] = i;
+      got[to] = w;
+    }
+    at += __builtin_popcountll(all);
+  });
   __syncthreads();
   if (threadIdx.x == 0) a.new_lengths[b] = total;
 }
