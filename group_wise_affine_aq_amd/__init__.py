@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import struct
 
@@ -705,6 +706,19 @@ _pack_scores = struct.Struct("@fi4P").pack  # aq_attention_scores
 _pack_rotation = struct.Struct("@2P2id").pack  # aq_rotation
 
 
+def _on_its_device(call):
+    """The call with the device of its first tensor as the current one: kernels are launched there."""
+    @functools.wraps(call)
+    def checked(*args, **more):
+        t = args[0] if args and args[0] is not None else (args[1] if len(args) > 1 else None)
+        torch = _torch()
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
+            with torch.cuda.device(t.device):
+                return call(*args, **more)
+        return call(*args, **more)
+    return checked
+
+
 def _scores(softcap, window, slopes, heads, first, firsts, prefix, prefixes, lse, rows):
     """The bytes of an aq_attention_scores."""
     torch = _torch_module
@@ -718,6 +732,7 @@ def _scores(softcap, window, slopes, heads, first, firsts, prefix, prefixes, lse
         0 if lse is None else _array(lse, torch.float32, rows, "lse"))
 
 
+@_on_its_device
 def aq_paged_attention_masked(q, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, page_table,
                               lengths, group_size: int, bits: int, scale: float | None = None,
                               softcap: float = 0.0, slopes=None, window: int = 0, first=None, out=None,
@@ -766,6 +781,7 @@ def aq_prompt_attention_workspace(Tq: int, Tk: int, B: int, q_heads: int, kv_hea
     return n
 
 
+@_on_its_device
 def aq_prompt_attention(q, k, v, q_starts, k_starts, scale: float | None = None, softcap: float = 0.0,
                         slopes=None, window: int = 0, first=None, prefix=None, out=None, lse=None,
                         return_lse: bool = False, workspace=None, stream=None):
@@ -845,6 +861,7 @@ def _turned(out, like, name, stream):
     return (out, *_rows(out, name))
 
 
+@_on_its_device
 def aq_rope(q, k, positions, freqs, interleaved: bool = False, factor: float = 1.0, q_out=None,
             k_out=None, stream=None):
     """Rotary positions of q [T, q_heads, head_dim] and k [T, kv_heads, head_dim] (fp16/bf16, tokens may
@@ -872,6 +889,7 @@ def aq_rope(q, k, positions, freqs, interleaved: bool = False, factor: float = 1
     return q_out if q is not None else None, k_out if k is not None else None
 
 
+@_on_its_device
 def aq_rope_append(q, k, v, positions, freqs, slots, k_codes, k_scales, k_biases, v_codes, v_scales,
                    v_biases, group_size: int, bits: int, interleaved: bool = False, factor: float = 1.0,
                    q_out=None, k_out=None, stream=None):
@@ -904,6 +922,7 @@ def aq_rope_append(q, k, v, positions, freqs, slots, k_codes, k_scales, k_biases
 
 
 # ---- keeping a cache within a budget ----------------------------------------------------
+@_on_its_device
 def aq_kv_weigh(q, lse, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, page_table, lengths,
                 weights, group_size: int, bits: int, scale: float | None = None, softcap: float = 0.0,
                 slopes=None, window: int = 0, first=None, stream=None):
@@ -930,6 +949,7 @@ def aq_kv_weigh(q, lse, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases
         raise AQError(st, "aq_kv_weigh")
 
 
+@_on_its_device
 def aq_kv_evict(weights, lengths, page_table, new_table, k_codes, k_scales, k_biases, v_codes, v_scales,
                 v_biases, group_size: int, bits: int, keep: int, sinks: int = 0, recent: int = 0,
                 new_lengths=None, stream=None):

@@ -716,15 +716,11 @@ struct Wave {
         }
     }
     if constexpr (MORE) {
-      // tanh x = 1 - 2 / (e^2x + 1): off by some 2^-24 of the cap
       if (p.cap2 != 0.f)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float e = exp2_fast(t[nt][j] * (p.inv_cap2 * 2.88539008177792681f));
-            t[nt][j] = __builtin_fmaf(-2.f * p.cap2, __builtin_amdgcn_rcpf(1.f + e), p.cap2);
-          }
+          for (int j = 0; j < 8; ++j) t[nt][j] = capped_score(t[nt][j], p.cap2, p.inv_cap2);
       if (p.slopes)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

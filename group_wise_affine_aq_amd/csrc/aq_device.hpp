@@ -101,6 +101,23 @@ __device__ __forceinline__ uint32_t lanes_prefix(uint32_t v) {
   return v;
 }
 
+// A score t in powers of two, capped: cap2 tanh(t / cap2).  Beside a large cap
+// the exponential's form 1 - 2 / (e^2y + 1) leaves only what its rounding does
+// (2^-23 of the cap); up to |y| = 0.6 the cap is t times a polynomial in y^2,
+// tanh y / y within 2^-23 (a fit of the least largest relative error).
+constexpr double kTanhTerms[5] = {0.9999999268660705, -0.33332309948977934, 0.13310173306949546,
+                                  -0.05210146457599173, 0.015475405965029628};
+__device__ __forceinline__ float capped_score(float t, float cap2, float inv_cap2) {
+  const float y = t * inv_cap2, u = y * y;
+  float f = __builtin_fmaf(u, (float)kTanhTerms[4], (float)kTanhTerms[3]);
+  f = __builtin_fmaf(u, f, (float)kTanhTerms[2]);
+  f = __builtin_fmaf(u, f, (float)kTanhTerms[1]);
+  f = __builtin_fmaf(u, f, (float)kTanhTerms[0]);
+  const float e = __builtin_amdgcn_exp2f(y * 2.88539008177792681f);  // 2 log2 e
+  const float large = __builtin_fmaf(-2.f * cap2, __builtin_amdgcn_rcpf(1.f + e), cap2);
+  return __builtin_fabsf(y) <= 0.6f ? t * f : large;
+}
+
 // the natural logarithm of l 2^m, l >= 0 (0: -inf).  l's exponent joins m first:
 // m lies several powers of two below the largest score, l as many above 1, and
 // log2 l by itself would have the rounding of their size, not of the result's.

@@ -59,9 +59,9 @@ struct Params {
   PromptArgs a;
   float C;         // |scale| log2 e
   uint32_t flip;   // sign of the scale, for pairs of queries
-  // caps: cap2 (in powers of two; 0: none), what brings a score s to 2 log2 e times tanh's
-  // argument; where |s| <= small the cap is s times a polynomial in s^2
-  float cap2, twice, small, cap[5], smaller, cap3[3];
+  // caps: cap2 (in powers of two; 0: none) and its inverse; where |s| <= small (smaller) the cap of a
+  // score s is s times a polynomial of five (three) terms in s^2
+  float cap2, inv_cap2, small, cap[5], smaller, cap3[3];
   int window, group;
   int tiles;       // of query rows, at most, of all sequences
   int parts;       // of every tile's keys
@@ -498,11 +498,7 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
 #pragma unroll
           for (int x = 0; x < X; ++x)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              // tanh y = 1 - 2 / (e^2y + 1)
-              const float e = exp2_fast(s[x][j] * p.twice);
-              s[x][j] = __builtin_fmaf(-2.f * p.cap2, __builtin_amdgcn_rcpf(1.f + e), p.cap2);
-            }
+            for (int j = 0; j < 16; ++j) s[x][j] = capped_score(s[x][j] * p.C, p.cap2, p.inv_cap2);
         } else {
 #pragma unroll
           for (int x = 0; x < X; ++x)
@@ -704,26 +700,23 @@ Cut cut_for(int64_t Tq, int64_t Tk, int64_t B, int q_heads, int kv_heads, int D)
   return c;
 }
 
-// tanh y / y = sum c_i y^2i: five terms within 2^-23 for |y| <= 0.6, three within 2^-23 for |y| <= 0.2
-// (fits of the least largest relative error).  So the cap of a small score costs five operations or
-// three and no exponential or reciprocal, which take twice as long each: the softmax is the longer half
-// of a tile (8192 tokens, cap 50: 754 us with them, 718 without).
+// tanh y / y = sum c_i y^2i: five terms within 2^-23 for |y| <= 0.6, three for |y| <= 0.2 (fits of
+// the least largest relative error).  So the cap of a small score costs five operations or three and no
+// exponential or reciprocal, which take twice as long each: the softmax is the longer half of a tile
+// (8192 tokens, cap 50: 754 us with them, 718 without, at that step).
 void set_cap(Params &p) {
-  constexpr double c[5] = {0.9999999268660705, -0.33332309948977934, 0.13310173306949546,
-                           -0.05210146457599173, 0.015475405965029628};
   constexpr double c3[3] = {0.999999894791025, -0.33328590894235166, 0.1301540743838377};
-  p.twice = 0.f, p.small = p.smaller = -1.f;
+  p.inv_cap2 = 0.f, p.small = p.smaller = -1.f;
   for (float &x : p.cap) x = 0.f;
   for (float &x : p.cap3) x = 0.f;
   if (p.cap2 == 0.f) return;
-  const double y = (double)p.C / p.cap2;
-  p.twice = (float)(2 * y * 1.4426950408889634);
-  const double small = 0.6 / y;
+  p.inv_cap2 = 1.f / p.cap2;
+  const double y = (double)p.C / p.cap2, small = 0.6 / y;
   // (powers of scores are within binary32, and what is small has room for its rounding)
   if (!(small > 1e-3 && small < 1e9 && small * p.C < 0x1p22)) return;
   double f = p.C;
   for (int i = 0; i < 5; ++i, f *= y * y) {
-    p.cap[i] = (float)(c[i] * f);
+    p.cap[i] = (float)(kTanhTerms[i] * f);
     if (i < 3) p.cap3[i] = (float)(c3[i] * f);
   }
   p.small = (float)small;

@@ -152,12 +152,16 @@ __global__ __launch_bounds__(64 * WV, 2) void weigh_kernel(Params p, float *weig
             if constexpr (W::QUANT) W::load_scales(raw, from, rows);
             W::load_keys(k, p, rows, on_next, lane);
             if (edge) st.edge_scores(t, token, on, h);
+            // (what a row does not see gets nothing of it, be its logarithm NaN)
             float sum[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              sum[j] = exp2_fast(t[0][j] - lse[0]);
+              sum[j] = 0.f;
 #pragma unroll
-              for (int nt = 1; nt < NT; ++nt) sum[j] += exp2_fast(t[nt][j] - lse[nt]);
+              for (int nt = 0; nt < NT; ++nt) {
+                const float x = exp2_fast(t[nt][j] - lse[nt]);
+                sum[j] += edge && t[nt][j] == kNegInf ? 0.f : x;
+              }
             }
             float *to = &strips[wave][token - tile0 * kTile + 16 * (lane >> 3 & 1) + 4 * h + (lane >> 1 & 3)];
             *to += columns_sum(sum, lane);

@@ -25,10 +25,14 @@ def scores(q, k, scale, pos, softcap=0.0, slope=None):
 def score_error(q, ka, scale, pos, softcap=0.0, slope=None):
     """How far a score may be off.  The rounding errors of its partial sums add
     like a random walk: 2^-22 of scale times the 2-norm of the products of q and
-    the keys' sizes ka (kv_ref.attention_rows), for the largest token.  The
-    tanh is off by a few 2^-24 of the cap (an exponential, a reciprocal, a
-    product: 2^-21), the bias by a rounding or two of its own size (2^-22)."""
-    off = 2.0 ** -22 * abs(scale) * np.sqrt((q ** 2) @ (ka ** 2).T).max(1) + 2.0 ** -21 * softcap
+    the keys' sizes ka (kv_ref.attention_rows), for the largest token; the cap
+    passes on no more.  The cap itself is off by a few 2^-24 of the capped score
+    (a polynomial, or an exponential, a reciprocal and a product where the score
+    is over half the cap: 2^-21), the bias by a rounding or two of its own size
+    (2^-22)."""
+    off = 2.0 ** -22 * abs(scale) * np.sqrt((q ** 2) @ (ka ** 2).T).max(1)
+    if softcap:
+        off = off + 2.0 ** -21 * np.minimum(softcap, abs(scale) * (np.abs(q) @ ka.T).max(1))
     return off if slope is None else off + 2.0 ** -22 * slope * (pos + len(ka))
 
 
