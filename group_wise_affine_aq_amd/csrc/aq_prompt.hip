@@ -11,6 +11,16 @@
 // sees, KT at a time.  Keys and values of a tile go through LDS once and serve
 // all waves; while they are worked on, the next tile's are on their way.
 //
+// NW is 4, or 2 where a sequence has 64 rows or fewer.  With heads of up to 128
+// two workgroups share a CU, and one's products run beside the other's softmax
+// without any order between them (8192 tokens of 32 heads of 128: 592 us
+// capped, 528 not).  Workgroups of 8 waves in two groups half a tile apart took
+// 577 and 509 there, but 72 -> 83 us for 4 x 1024 tokens, 447 -> 479 us with
+// heads of 64 and 107 -> 117 us with a window of 512.  Heads of 256 leave room
+// for one wave a SIMD: 1165 us, 1336 with 32 keys a tile, whose sums are one
+// chain of products.  Products of the tile before, put between the softmax's
+// steps in one wave, cost more than they hid (647 and 1199 us).
+//
 // Matrix layout (v_mfma_f32_32x32x16).  S^T = K q^T: a lane has one row of
 // queries (lane % 32) and, with h = lane / 32, the tokens 8 i + 4 h .. + 3 of
 // each 32.  So a row's maximum and sum stay in two lanes, and the 16 tokens of
@@ -141,7 +151,7 @@ constexpr int piece_floats(int R) { return R * (D + 2); }
 template <bool BF, int D, int NW>
 struct Shape {
   static constexpr int R = 32 * NW, THREADS = 64 * NW;
-  static constexpr int KT = D > 128 ? 32 : 64;  // keys of a tile
+  static constexpr int KT = D > 128 && NW == 2 ? 32 : 64;  // keys of a tile
   static constexpr int X = KT / 32, KK = KT / 16;
   static constexpr int CH = D / 8;            // 16-byte pieces of a row
   static constexpr int RB = D * 2;            // bytes of a row
@@ -424,14 +434,6 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
     }
   };
 
-  // Two groups of waves, each with a wave on every SIMD, half a tile apart: between two barriers the
-  // earlier one multiplies tile t and has its softmax, the later one has the softmax of tile t - 1 and
-  // multiplies tile t.  So one group's products run beside the other's vector work, as far as the one
-  // is as long as the other; the later group's softmax goes first where both have vector work, since
-  // its products still follow it (8192 tokens capped 647 us without, 607 so).  Behind the barrier
-  // every wave asks for its share of the keys of tile t + 1 and the values of t, whose place was last
-  // read ahead of it.
-  const bool late = NW == 8 && wave >= NW / 2;
   for (;;) {
 #pragma unroll
   for (int i = 0; i < DB; ++i)
@@ -449,13 +451,12 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
 #pragma unroll
   for (int i = 0; i < NV; ++i) at_v[i] = 3 * S::TILE + S::value_piece(vr, (32 * i + vc) >> 3) + (vc & 7) * 2;
   due = 0;
-  auto next = [&] {
-    arrived();
-    barrier();
-    bring();
-  };
+  // Behind a barrier every wave asks for its share of the keys of the next tile but one and the values
+  // of the next, whose place was last read ahead of it.
   bring();
-  next();
+  arrived();
+  barrier();
+  bring();
   for (int t = t0; t < t1; ++t) {
     const int key0 = t * KT;
     const bool need = key0 < most && key0 + KT > least;
@@ -465,14 +466,11 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
       multiply(Count<0>(), both_end);
     }
     if (have) gather_odd(t - 1);
+
 #pragma unroll
     for (int k = 0; k < NK; ++k) at_k[k] ^= S::TILE;
 #pragma unroll
     for (int i = 0; i < NV; ++i) at_v[i] ^= S::TILE;
-    if (late) {
-      next();
-      __builtin_amdgcn_s_setprio(1);
-    }
     if (need) {
       // Scores in powers of two are t = s C, or its cap.  Three ways there, by what the wave has
       // (each of s, C and the cap's polynomial fused with the subtraction of m where it can be):
@@ -581,8 +579,9 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
 
     }
     have = need;
-    if (late) __builtin_amdgcn_s_setprio(0);
-    if (!late) next();
+    arrived();
+    barrier();
+    bring();
   }
   if (have) {
     multiply(keys_end, both_end);
@@ -684,15 +683,15 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(Params p) {
 // How a call is cut: waves of a workgroup, tiles of rows at most, and parts of every tile's keys
 struct Cut { int waves, tiles, parts; };
 Cut cut_for(int64_t Tq, int64_t Tk, int64_t B, int q_heads, int kv_heads, int D) {
-  const int group = q_heads / kv_heads, large = D > 128 ? 4 : 8;
+  const int group = q_heads / kv_heads;
   Cut c;
-  c.waves = Tq * group <= 64 * B ? 2 : large;
+  c.waves = Tq * group <= 64 * B ? 2 : 4;
   const int R = 32 * c.waves;
   c.tiles = (int)(Tq * group / R + B);
-  // parts of at least 8 tiles of keys, as long as the chip is not full and pieces fit 64 MiB
+  // parts of at least 512 keys, as long as the chip is not full and pieces fit 64 MiB
   const int64_t wgs = (int64_t)c.tiles * kv_heads, room = ((int64_t)64 << 20) / ((int64_t)R * (D + 2) * 4);
   int64_t parts = (int64_t)device_cus() * (c.waves == 2 ? 4 : 1) / wgs;
-  const int64_t keys = (Tk + B - 1) / B / (8 * (D > 128 ? 32 : 64));
+  const int64_t keys = (Tk + B - 1) / B / 512;
   if (parts > keys) parts = keys;
   if (parts > room / wgs) parts = room / wgs;
   if (parts > kMaxParts) parts = kMaxParts;
@@ -756,7 +755,7 @@ hipError_t launch_prompt_attention(const PromptArgs &a, hipStream_t s) {
   p.piece = reinterpret_cast<float *>(a.workspace);
 #define AQ_W(B, D)                                                     \
   if (a.head_dim == D)                                                 \
-    return c.waves == 2 ? launch<B, D, 2>(p, s) : launch<B, D, (D > 128 ? 4 : 8)>(p, s);
+    return c.waves == 2 ? launch<B, D, 2>(p, s) : launch<B, D, 4>(p, s);
 #define AQ_D(B) AQ_W(B, 64) AQ_W(B, 128) AQ_W(B, 256)
   if (a.x_dtype == X_BF16) { AQ_D(true) } else { AQ_D(false) }
 #undef AQ_D
