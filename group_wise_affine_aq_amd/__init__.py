@@ -710,9 +710,9 @@ def _on_its_device(call):
     """The call with the device of its first tensor as the current one: kernels are launched there."""
     @functools.wraps(call)
     def checked(*args, **more):
-        t = args[0] if args and args[0] is not None else (args[1] if len(args) > 1 else None)
         torch = _torch()
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
+        t = next((x for x in (*args, *more.values()) if isinstance(x, torch.Tensor)), None)
+        if t is not None and t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
             with torch.cuda.device(t.device):
                 return call(*args, **more)
         return call(*args, **more)

@@ -261,3 +261,30 @@ def test_reference_is_the_formula():
                 assert math.isclose(lse[h], math.log(total), rel_tol=1e-12)
             else:
                 assert not out[h].any() and lse[h] == -math.inf
+
+
+@pytest.mark.parametrize("named", [False, True])
+def test_calls_run_on_the_device_of_their_tensors(monkeypatch, named):
+    """Whether the first tensor is passed by position or by name, or stands behind a None."""
+    import contextlib
+    import torch
+
+    class There(torch.Tensor):
+        is_cuda = property(lambda self: True)
+        device = property(lambda self: "the second")
+        get_device = lambda self: 1  # noqa: E731
+
+    entered = []
+
+    @contextlib.contextmanager
+    def device(x):
+        entered.append(x)
+        yield
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    x = torch.zeros(2).as_subclass(There)
+    call = aq._on_its_device(lambda q, k, stream=None: (q, k))
+    assert (call(q=None, k=x) if named else call(None, x)) == (None, x) and entered == ["the second"]
+    assert (call(k=None, q=x) if named else call(x, None)) == (x, None) and len(entered) == 2
+    assert call(None, None) == (None, None) and len(entered) == 2
