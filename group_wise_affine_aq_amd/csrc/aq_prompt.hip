@@ -13,12 +13,12 @@
 //
 // NW is 4, or 2 where a sequence has 64 rows or fewer.  With heads of up to 128
 // two workgroups share a CU, and one's products run beside the other's softmax
-// without any order between them (8192 tokens of 32 heads of 128: 592 us
-// capped, 528 not).  Workgroups of 8 waves in two groups half a tile apart took
-// 577 and 509 there, but 72 -> 83 us for 4 x 1024 tokens, 447 -> 479 us with
-// heads of 64 and 107 -> 117 us with a window of 512.  Heads of 256 leave room
-// for one wave a SIMD: 1165 us, 1336 with 32 keys a tile, whose sums are one
-// chain of products.  Products of the tile before, put between the softmax's
+// without any order between them (8192 tokens of 32 heads of 128: 568 us
+// capped, 509 not).  Workgroups of 8 waves in two groups half a tile apart, when the
+// former took 592 and 528, took 577 and 509 there, but 72 -> 83 us for 4 x 1024
+// tokens, 447 -> 479 us for 4 x 4096 of heads of 64 and 107 -> 117 us with a
+// window of 512.  Heads of 256 leave room for one wave a SIMD: 1138 us (1336
+// with 32 keys a tile, whose sums are one chain of products, 1165 with 64).  Products of the tile before, put between the softmax's
 // steps in one wave, cost more than they hid (647 and 1199 us).
 //
 // Matrix layout (v_mfma_f32_32x32x16).  S^T = K q^T: a lane has one row of
@@ -487,11 +487,10 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
         top = largest(s, true);
         if (__ballot(!(top <= p.small)) == 0) way = __ballot(!(top <= p.smaller)) == 0 ? 3 : 2;
       }
-      if (way == 1) {
-        top *= p.C;
-      } else if (way) {
-        top = small_cap(p, top);
-      } else {
+      // (an if without an else, in which the scores change where they are: else they are copied for it,
+      // in all ways)
+      if (way) top = way == 1 ? top * p.C : small_cap(p, top);
+      if (!way) {
         if (p.cap2 != 0.f) {
 #pragma unroll
           for (int x = 0; x < X; ++x)

@@ -662,7 +662,7 @@ aq_status aq_kv_weigh(const void *q, aq_dtype x_dtype, int64_t B, int L, int q_h
  * (codes, scales and biases 0); rows that would go to one are not written.
  * keep >= 1, sinks and recent >= 0, sinks + recent <= keep <= new_max_pages *
  * page_size; AQ_ERR_INVALID_ARG otherwise.  lengths and new_lengths may be one
- * array.  AQ_ERR_UNSUPPORTED for B >= 2^24, B * keep or B * keep * kv_heads / 64 >=
+ * array; no other output is part of an input.  AQ_ERR_UNSUPPORTED for B >= 2^24, B * keep or B * keep * kv_heads / 64 >=
  * 2^31, keep or weights_stride > 2^30, or tables of more than 2^31 - 256
  * tokens. */
 aq_status aq_kv_evict(const float *weights, int64_t weights_stride, const int32_t *lengths,
