@@ -267,6 +267,30 @@ def test_odd_values_in_prompts(aq, dtype, D, Hq, H):
     assert np.isfinite(got[:, group:]).all()
 
 
+@pytest.mark.parametrize("n,Hq", [(20, 2), (90, 2)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_long_keys_in_parts(aq, n, Hq, D):
+    """Keys cut into parts for workgroups of two and of four waves; infinite and NaN values in the
+    first, an inner and the last tile of a part, seen by all rows, by some and by none."""
+    past, window = 3000, 2990
+    rng = np.random.default_rng(D + n)
+    k, v = rng.standard_normal((past + n, 1, D)), rng.standard_normal((past + n, 1, D))
+    _check_prompt(aq, [n], [past], Hq, 1, D, "f16", seed=9, k=k, v=v, softcap=30.0)
+    clean, lse0, _ = _prompt(aq, [n], [past], Hq, 1, D, "f16", seed=9, k=k, v=v, window=window)
+    odd = [(0, 1, np.nan), (12, 5, np.inf), (511, 6, -np.inf), (512, 7, np.inf), (1700, 8, np.nan),
+           (past, 9, np.inf), (past + n - 1, 10, -np.inf)]
+    for t, d, x in odd:
+        v[t, 0, d] = x
+    got, lse, _ = _prompt(aq, [n], [past], Hq, 1, D, "f16", seed=9, k=k, v=v, window=window)
+    want = clean.copy()
+    for t, d, x in odd:
+        for row in range(n):
+            if t <= past + row and past + row - t < window:
+                want[row, :, d] = x
+    assert np.array_equal(got, want, equal_nan=True)
+    assert np.array_equal(lse, lse0)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_small_weights_beside_a_large_one(aq, dtype):
     """One token whose value is 0 takes nearly all of the softmax."""
