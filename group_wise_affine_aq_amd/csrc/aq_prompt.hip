@@ -717,6 +717,13 @@ void set_cap(Params &p) {
     p.cap[i] = (float)(kTanhTerms[i] * f);
     if (i < 3) p.cap3[i] = (float)(c3[i] * f);
   }
+  // (the terms hold powers of y up to y^8: where one is no normal number of binary32 it has lost bits,
+  // or all of them, that scores near the cap would need.  With heads of 128 and the usual scale caps of
+  // up to 2000 have normal terms)
+  for (float x : p.cap)
+    if (!(__builtin_fabsf(x) >= 0x1p-126f)) return;
+  for (float x : p.cap3)
+    if (!(__builtin_fabsf(x) >= 0x1p-126f)) return;
   p.small = (float)small;
   p.smaller = (float)(0.2 / y);
 }
