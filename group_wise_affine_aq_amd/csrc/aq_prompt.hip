@@ -30,10 +30,15 @@
 // 16-byte pieces of a row lie in LDS at their number xor the row's, keys and
 // values in different ways, so that neither read meets a bank twice.
 //
-// Weights are 2^(t - m): m is not the largest score but up to kUp less, so
-// that the largest weight lies near 2^kUp, fp16's range below it serves the
-// small ones (2^-39 of the largest), and m, which only moves when a weight
-// would pass 2^kUp, seldom does; then everything summed is rescaled.
+// Weights are 2^(t - m): m is set so that the largest weight is 2^(up - 4) and
+// moves when one would pass 2^up, so that it seldom does; then everything summed
+// is rescaled.  fp16: up = 15, the range below serves the small weights (down
+// to 2^-35 of the largest, at least).  bf16 has binary32's range for weights and
+// values, and a sum of weights of 1 times values near its end would pass it
+// where the result does not: up = -12, so that 4096 tokens of the largest
+// weights and of the type's largest value, 2^128, still have a finite sum (with
+// up = 15 one token of 2^117 had none), and small values lose nothing down to
+// 2^-110.
 //
 // Values that are not finite: 0 * inf is NaN, and a row that does not see a
 // token must not see its value, nor lose an infinity to a weight that is
@@ -62,7 +67,7 @@ typedef __amdgpu_buffer_rsrc_t Span;
 
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr float kUp = 15.f;  // 2^15 is within fp16's range
+template <bool BF> constexpr float kUp = BF ? -12.f : 15.f;  // weights are 2^kUp at most
 constexpr int kMaxParts = 64;
 
 struct Params {
@@ -522,12 +527,13 @@ __global__ __launch_bounds__(64 * NW, D > 128 || NW == 2 ? 1 : 2) void prompt_ke
         top = largest(s, false);
       }
       // (the lane's own half of the row, or what no score of it is above: enough to know that m stays)
-      if (__ballot(top - m > kUp)) {
+      if (__ballot(top - m > kUp<BF>)) {
         if (way > 1) top = small_cap(p, largest(s, false));
         top = __builtin_fmaxf(top, other_half(top));
-        const bool over = top - m > kUp;
-        // (scores past 2^23 have no room for kUp: their weights are 1 at most)
-        const float to = over ? (__builtin_fabsf(top) < 0x1p23f ? top - (kUp - 4.f) : top) : m;
+        const bool over = top - m > kUp<BF>;
+        // (scores past 2^23 have no room for kUp: their weights are 1 at most, and m does not fall after
+        // those that do)
+        const float to = over ? (__builtin_fabsf(top) < 0x1p23f ? top - (kUp<BF> - 4.f) : __builtin_fmaxf(top, m)) : m;
         // (not 0: an infinite sum stays what it is)
         const float keep = __builtin_fmaxf(exp2_fast(m - (to == kNegInf ? 0.f : to)), 0x1p-126f);
         m = to;

@@ -4,10 +4,11 @@ heads among the waves."""
 import numpy as np
 import pytest
 
+import kv_ref
 from gpu_util import to_dev
 from test_gpu_attention import _queries
 from test_gpu_kv import _build, _dev16, aq  # noqa: F401  (aq: the module's fixture)
-from test_gpu_scores import _check_prompt
+from test_gpu_scores import _check_prompt, _prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +74,43 @@ def test_rows_without_a_logarithm_add_nothing(aq):
         aq.aq_kv_weigh(_dev16(qb, "f16"), lse, *parts, tab, lens, w, 32, 8)
         got.append(w)
     assert torch.equal(*got) and abs(float(got[0].sum()) - 3) < 1e-4
+
+
+# ---- values near binary32's ends --------------------------------------------------------
+@pytest.mark.parametrize("n,past,window", [([1], [0], 0), ([150, 1, 33], [30, 0, 200], 0), ([150], [200], 1),
+                                           ([20], [3000], 0), ([90], [3000], 0)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_large_values_of_prompts(aq, D, n, past, window):
+    """bf16 values around 1e36, and of one sign near the type's largest: sums of
+    weights and values stay within binary32 where the result does."""
+    rng = np.random.default_rng(D)
+    keys = sum(n) + sum(past)
+    k, v = rng.standard_normal((keys, 1, D)), rng.standard_normal((keys, 1, D))
+    for x in (v * 1e36, 3.3e38 * (1 - rng.random(v.shape) / 16)):
+        _check_prompt(aq, n, past, 2, 1, D, "bf16", seed=D, k=k, v=x, window=window)
+
+
+@pytest.mark.parametrize("power", [-60, 100, 121])
+def test_results_scale_with_the_values_of_prompts(aq, power):
+    """Values times a power of two give the same results times it."""
+    rng = np.random.default_rng(9)
+    k, v = rng.standard_normal((350, 1, 128)), rng.standard_normal((350, 1, 128))
+    a, b = (_prompt(aq, [150], [200], 2, 1, 128, "bf16", seed=3, k=k, v=x, softcap=20.0)[0]
+            for x in (v, v * 2.0 ** power))
+    assert np.array_equal(a * 2.0 ** power, b)
+
+
+def test_scores_past_where_weights_have_room(aq):
+    """Scores past 2^23 in powers of two that fall by 8 from tile to tile: what
+    was summed is not raised as they fall."""
+    n, D = 700, 64
+    q = np.random.default_rng(4).standard_normal((1, 1, D))  # what _prompt makes of seed 4
+    q0, q1 = (float(x) for x in kv_ref.to_bits(q, "bf16")[1][0, 0, :2])
+    to_power = D ** 0.5 * np.log(2)
+    k = np.zeros((n + 1, 1, D))
+    k[:, 0, 0] = 1.2e7 * to_power / q0
+    k[:, 0, 1] = -8 * to_power / q1 * (np.arange(n + 1) // 64)
+    v = 1e36 * np.random.default_rng(5).standard_normal((n + 1, 1, D))
+    got, lse, _ = _prompt(aq, [1], [n], 1, 1, D, "bf16", seed=4, k=k, v=v)
+    assert np.isfinite(got).all() and np.abs(got).max() <= np.abs(v[:192]).max()
+    assert lse.min() > 2.0 ** 23 * np.log(2)
