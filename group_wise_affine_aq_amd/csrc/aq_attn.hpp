@@ -488,11 +488,13 @@ struct Wave {
   // How large, in powers of two, a weight may be: times the tile's largest
   // scale of values it stays within fp16 (a scale of exponent field e is below
   // 2^(e - 14); infinities and NaN count as the next field).  Scales of tokens
-  // that nobody sees do not count.  16 bits: the weight alone; bf16 needs no
-  // such care.
+  // that nobody sees do not count.  16 bits: the weight alone.  bf16 has
+  // binary32's range for values too: weights stay so small that 4096 of the
+  // largest, times the type's largest value, have a finite sum (at up to 2^4,
+  // 2500 tokens of 2^121 had none).
   static __device__ __forceinline__ float room(const Raw &r, bool edge, int token, const bool *on,
                                                int len, int lane) {
-    if constexpr (!QUANT) return BF ? 4.f : 15.f;
+    if constexpr (!QUANT) return BF ? -12.f : 15.f;
     u16x2v most = {0, 0};
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub)
@@ -735,7 +737,7 @@ struct Wave {
   // The weights 2^(t - m) of the scores t, at most 2^up each: where one would be
   // larger, m moves up to 4 short of that, so that it seldom moves again, and
   // what was summed is rescaled.  (Scores past 2^23 have no room for up: their
-  // weights are 1 at most.)
+  // weights are 1 at most, and m does not fall after those that do.)
   __device__ __forceinline__ void weigh(float (&t)[NT][8], float up) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -745,7 +747,7 @@ struct Wave {
       top = quarters_max(top);
       const bool over = top - m[nt] > up;
       if (__ballot(over)) {
-        const float to = over ? (__builtin_fabsf(top) < 0x1p23f ? top - (up - 4.f) : top) : m[nt];
+        const float to = over ? (__builtin_fabsf(top) < 0x1p23f ? top - (up - 4.f) : __builtin_fmaxf(top, m[nt])) : m[nt];
         const float keep = exp2_fast(m[nt] - (to == kNegInf ? 0.f : to));
         m[nt] = to;
         l[nt] *= keep;

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 import kv_ref
-from gpu_util import to_dev
+from gpu_util import out_to_f64, to_dev
 from test_gpu_attention import _queries
 from test_gpu_kv import _build, _dev16, aq  # noqa: F401  (aq: the module's fixture)
 from test_gpu_scores import _check_prompt, _prompt
@@ -114,3 +114,23 @@ def test_scores_past_where_weights_have_room(aq):
     got, lse, _ = _prompt(aq, [1], [n], 1, 1, D, "bf16", seed=4, k=k, v=v)
     assert np.isfinite(got).all() and np.abs(got).max() <= np.abs(v[:192]).max()
     assert lse.min() > 2.0 ** 23 * np.log(2)
+
+
+@pytest.mark.parametrize("lengths,L,per,dim", [([1, 300, 33], 1, 4, 128), ([2500], 2, 2, 64), ([700], 5, 8, 256)])
+@pytest.mark.parametrize("power", [-60, 100, 121])
+def test_results_scale_with_the_values_of_pages(aq, power, lengths, L, per, dim):
+    """bf16 pages whose values are those of another cache times a power of two: the
+    same results times it, where sums of weights and values pass binary32
+    unless the weights leave room too."""
+    import torch
+    got = []
+    for times in (0, power):
+        cache, table = _build(lengths, 1, dim, 0, 16, 16, "bf16", seed=51, poison=False)
+        v = cache.parts["v"][0]
+        v &= 0x7FFF  # (of one sign)
+        v[:] = np.where(v & 0x7F80, v + (times << 7 & 0xFFFF), v).astype(np.uint16)
+        qb, _ = _queries(52, (len(lengths), L, per, dim), "bf16", 0.3)
+        args = (_dev16(qb, "bf16"), *cache.device(), to_dev(table), to_dev(np.array(lengths, np.int32)), 32, 16)
+        got.append([out_to_f64(aq.aq_paged_attention(*args)), out_to_f64(aq.aq_paged_attention_masked(*args, softcap=9.0))])
+    for a, b in zip(*got):
+        assert np.isfinite(b).all() and np.array_equal(a * 2.0 ** power, b)
