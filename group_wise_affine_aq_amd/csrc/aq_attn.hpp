@@ -492,8 +492,9 @@ struct Wave {
   // binary32's range for values too: weights stay so small that 4096 of the
   // largest, times the type's largest value, have a finite sum (at up to 2^4,
   // 2500 tokens of 2^121 had none).
+  // Tokens since .. len - 1 are those that somebody sees.
   static __device__ __forceinline__ float room(const Raw &r, bool edge, int token, const bool *on,
-                                               int len, int lane) {
+                                               int since, int len, int lane) {
     if constexpr (!QUANT) return BF ? -12.f : 15.f;
     u16x2v most = {0, 0};
 #pragma unroll
@@ -501,7 +502,7 @@ struct Wave {
 #pragma unroll
       for (int i = 0; i < RW; ++i) {
         uint32_t w = r.w[sub][i] & 0x7FFF7FFFu;
-        if (edge) w = on[sub] && token + 16 * sub + (lane & 15) < len ? w : 0u;
+        if (edge) w = on[sub] && (uint32_t)(token + 16 * sub - since + (lane & 15)) < (uint32_t)(len - since) ? w : 0u;
         most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2v, w));
       }
     int top = most[0] > most[1] ? most[0] : most[1];
@@ -912,11 +913,13 @@ struct Wave {
                                       int tile0, int end, char *strip) {
     const int lane = lane_here();
     const int least = len - p.L + 1 + (slice * NT * 16) / p.group;  // what every column sees
-    // MORE: and from where on
-    int first_b = 0, most = 0;
+    // MORE: and from where on; since: what any does
+    int first_b = 0, most = 0, since = 0;
     if constexpr (MORE) {
       const int newest = ((slice + 1) * NT * 16 - 1) / p.group;
       first_b = uniform(first_of(p, b));
+      since = first_seen(p, first_b, least);
+      since = since < len ? since : len;
       most = first_seen(p, first_b, len - p.L + 1 + (newest < p.L ? newest : p.L - 1));
     }
     Keys k;
@@ -979,7 +982,7 @@ struct Wave {
           share_scales(raw, strip, lane, none);
           take_scales(g, strip, 0, lane);
         }
-        const float up = room(raw, edge, token, on, len, lane);
+        const float up = room(raw, edge, token, on, since, len, lane);
         scores(p, k, g, t, token, lane >> 4);
         // after the last tile fetches of no bytes: loads without a branch let
         // the waits count only what they need

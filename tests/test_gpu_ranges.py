@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 import kv_ref
-from gpu_util import out_to_f64, to_dev
+from gpu_util import out_bits, out_to_f64, to_dev
 from test_gpu_attention import _queries
 from test_gpu_kv import _build, _dev16, aq  # noqa: F401  (aq: the module's fixture)
 from test_gpu_scores import _check_prompt, _prompt
@@ -134,3 +134,27 @@ def test_results_scale_with_the_values_of_pages(aq, power, lengths, L, per, dim)
         got.append([out_to_f64(aq.aq_paged_attention(*args)), out_to_f64(aq.aq_paged_attention_masked(*args, softcap=9.0))])
     for a, b in zip(*got):
         assert np.isfinite(b).all() and np.array_equal(a * 2.0 ** power, b)
+
+
+# ---- what a row does not see ------------------------------------------------------------
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("L,per,dim,window", [(1, 4, 128, 20), (4, 5, 64, 20), (3, 2, 256, 33), (8, 8, 128, 5)])
+def test_scales_that_no_row_sees(aq, bits, L, per, dim, window):
+    """Packed pages: scales and biases of tokens before the window, large,
+    infinite or NaN, leave all results as they are to the last bit."""
+    lengths = [100, 70]
+    qb, _ = _queries(61, (2, L, per * 2, dim), "f16")
+    lens, got = to_dev(np.array(lengths, np.int32)), []
+    for odd in (None, 0x7BFF, 0x7C00, 0x7E00):
+        cache, table = _build(lengths, 2, dim, 32, bits, 16, "f16", seed=L + dim)
+        if odd:
+            for b, n in enumerate(lengths):
+                for t in range(max(0, n - L - window - 30), n - L - window + 1):
+                    for part in (1, 2):
+                        cache.parts["k"][part][table[b, t // 16], :, t % 16] = odd
+                        cache.parts["v"][part][table[b, t // 16], :, t % 16] = odd
+        out, lse = aq.aq_paged_attention_masked(_dev16(qb, "f16"), *cache.device(), to_dev(table), lens, 32, bits,
+                                                window=window, return_lse=True)
+        got.append((out_bits(out), out_bits(lse)))
+    for out, lse in got[1:]:
+        assert np.array_equal(out, got[0][0]) and np.array_equal(lse, got[0][1])
