@@ -144,6 +144,10 @@ aq_status check_rows(int64_t T, int heads, int head_dim, int64_t stride) {
   return AQ_OK;
 }
 
+// A launch has fewer than 2^32 threads, so workgroups of 256 are fewer than
+// 2^24: past that it fails, behind what a call launched before it.
+constexpr int64_t kMaxWorkgroups256 = (1 << 24) - 1;
+
 bool valid_head_dim(int d) { return d == 64 || d == 128 || d == 256; }
 
 aq_status check_rotation(const aq_rotation *r, int head_dim) {
@@ -648,8 +652,8 @@ static aq_status rope_args(aq::RopeArgs &a, const void *q, int64_t q_stride, int
   if (st == AQ_OK && kv_heads && (need_k_out || k_out))
     st = check_rows(T, kv_heads, head_dim, k_out_stride);
   if (st != AQ_OK) return st;
-  // (the grid: a workgroup per token at most)
-  if (T > 0x7FFFFFF0) return AQ_ERR_UNSUPPORTED;
+  // (so many tokens go 16 to a workgroup)
+  if (T > kMaxWorkgroups256 * 16) return AQ_ERR_UNSUPPORTED;
   if (T == 0) return AQ_OK;
   if (!r->positions || !r->freqs || (q_heads && (!q || !q_out)) ||
       (kv_heads && (!k || (need_k_out && !k_out))))
@@ -773,9 +777,10 @@ aq_status aq_kv_evict(const float *weights, int64_t weights_stride, const int32_
       recent < 0 || sinks > keep || recent > keep - sinks)
     return AQ_ERR_INVALID_ARG;
   const int64_t most = (int64_t)1 << 30;
-  if (B >= (1 << 24) || keep > most || B * keep >= 2 * most || weights_stride > most ||
+  // (B workgroups of 1024 choose, one for 64 kept tokens and head moves)
+  if (B > kMaxWorkgroups256 / 4 || keep > most || B * keep >= 2 * most || weights_stride > most ||
       max_pages > 0x7FFFFF00 / cache->page_size || new_max_pages > 0x7FFFFF00 / cache->page_size ||
-      (keep / 64 + 1) * B > 0x7FFFFFFF / cache->kv_heads)
+      (keep + 63) / 64 * B > kMaxWorkgroups256 / cache->kv_heads)
     return AQ_ERR_UNSUPPORTED;
   if (keep > new_max_pages * cache->page_size) return AQ_ERR_INVALID_ARG;
   st = check_cache_arrays(cache, false);

@@ -580,7 +580,8 @@ typedef struct aq_rotation {
  * and head_dim contiguous, tokens the strides apart in elements (multiples of
  * 8, at least heads * head_dim).  q_out may be q itself (with its stride) and
  * k_out k; other overlaps are the caller's mistake.  q_heads = 0 or kv_heads =
- * 0 leaves that side out (its pointers may be NULL).  T = 0 does nothing. */
+ * 0 leaves that side out (its pointers may be NULL).  T = 0 does nothing;
+ * AQ_ERR_UNSUPPORTED for T > 2^28 - 16. */
 aq_status aq_rope(const void *q, int64_t q_stride, int q_heads, const void *k, int64_t k_stride,
                   int kv_heads, aq_dtype x_dtype, int64_t T, int head_dim,
                   const aq_rotation *rotation, void *q_out, int64_t q_out_stride, void *k_out,
@@ -662,9 +663,9 @@ aq_status aq_kv_weigh(const void *q, aq_dtype x_dtype, int64_t B, int L, int q_h
  * (codes, scales and biases 0); rows that would go to one are not written.
  * keep >= 1, sinks and recent >= 0, sinks + recent <= keep <= new_max_pages *
  * page_size; AQ_ERR_INVALID_ARG otherwise.  lengths and new_lengths may be one
- * array; no other output is part of an input.  AQ_ERR_UNSUPPORTED for B >= 2^24, B * keep or B * keep * kv_heads / 64 >=
- * 2^31, keep or weights_stride > 2^30, or tables of more than 2^31 - 256
- * tokens. */
+ * array; no other output is part of an input.  AQ_ERR_UNSUPPORTED for B >=
+ * 2^22, B * keep >= 2^31, B * ceil(keep / 64) * kv_heads >= 2^24, keep or
+ * weights_stride > 2^30, or tables of more than 2^31 - 256 tokens. */
 aq_status aq_kv_evict(const float *weights, int64_t weights_stride, const int32_t *lengths,
                       int64_t B, const int32_t *page_table, int64_t max_pages,
                       const int32_t *new_table, int64_t new_max_pages, const aq_kv_cache *cache,

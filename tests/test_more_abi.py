@@ -196,6 +196,18 @@ def test_evict_errors(lib):
         assert evict(lib, c, **bad) == UNSUPPORTED, bad
 
 
+def test_launches_of_more_threads_than_there_are(lib):
+    """2^32 threads or more in one launch: refused before anything is enqueued."""
+    c = cache(kv_heads=1, head_dim=64, group_size=64, bits=4)
+    # moving: B * ceil(keep / 64) * kv_heads workgroups; choosing: B of 1024 threads
+    for bad in (dict(B=1, keep=1 << 30, nmp=1 << 26), dict(B=1 << 14, keep=1 << 16, nmp=1 << 12),
+                dict(B=1 << 22, keep=1, nmp=1, sinks=0, recent=0)):
+        assert evict(lib, c, **bad) == UNSUPPORTED, bad
+    assert evict(lib, cache(kv_heads=16, num_pages=1), B=1 << 20, keep=64, nmp=4) == UNSUPPORTED
+    for T in (1 << 28, 0x7FFFFFF0):
+        assert rope(lib, T=T) == append(lib, cache(), T=T) == UNSUPPORTED, T
+
+
 # ---- frequencies ------------------------------------------------------------------------
 def freqs(*args, **k):
     return aq.aq_rope_frequencies(*args, device="cpu", **k)
