@@ -836,7 +836,7 @@ def aq_rope_frequencies(rotary: int, base: float = 10000.0, kind: str = "plain",
     """(frequencies fp32 [rotary / 2] on the device, factor) for aq_rope: base ** (-2 i / rotary),
     changed for contexts `stretch` times the trained one, ctx, as `kind` says (include/aq.h)."""
     torch = _torch()
-    freqs, factor = torch.empty(max(rotary, 0) // 2, dtype=torch.float32), ctypes.c_float()
+    freqs, factor = torch.empty(max(rotary, 0) // 2, dtype=torch.float32, device="cpu"), ctypes.c_float()
     st = load_library().aq_rope_frequencies(rotary, base, ROPE_STRETCHES[kind], stretch, ctx, low, high,
                                             freqs.data_ptr(), ctypes.byref(factor))
     _check(st, "aq_rope_frequencies")

@@ -236,6 +236,16 @@ def test_frequencies_by_the_formulas(lib):
     assert np.allclose(got, g * f / s + (1 - g) * f, rtol=1e-7) and factor == 1.0
 
 
+def test_frequencies_are_made_on_the_host(lib):
+    """Where tensors are made on another device by default, too: the library
+    fills host memory."""
+    import torch
+    with torch.device("meta"):
+        got, factor = freqs(128, 500000.0, "by_turns", 8.0, 4096.0, 1.0, 4.0)
+    want = freqs(128, 500000.0, "by_turns", 8.0, 4096.0, 1.0, 4.0)
+    assert got.device.type == "cpu" and torch.equal(got, want[0]) and factor == want[1]
+
+
 def test_frequencies_errors(lib):
     for bad in (dict(rotary=2), dict(rotary=7), dict(rotary=-4), dict(base=1.0), dict(base=NAN), dict(base=INF),
                 dict(kind="linear", stretch=0.5), dict(kind="base", stretch=INF),
