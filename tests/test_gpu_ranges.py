@@ -8,7 +8,7 @@ import kv_ref
 from gpu_util import out_bits, out_to_f64, to_dev
 from test_gpu_attention import _queries
 from test_gpu_kv import _build, _dev16, aq  # noqa: F401  (aq: the module's fixture)
-from test_gpu_scores import _check_prompt, _prompt
+from test_gpu_scores import _check_prompt, _paged, _prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -158,3 +158,113 @@ def test_scales_that_no_row_sees(aq, bits, L, per, dim, window):
         got.append((out_bits(out), out_bits(lse)))
     for out, lse in got[1:]:
         assert np.array_equal(out, got[0][0]) and np.array_equal(lse, got[0][1])
+
+
+# ---- shares of the work -----------------------------------------------------------------
+@pytest.mark.parametrize("bits,G", [(4, 64), (8, 64), (16, 0)])
+@pytest.mark.parametrize("heads", [3, 4, 5, 7, 8, 9, 16])
+def test_any_number_of_key_heads(aq, bits, G, heads):
+    """Key heads go to eight, four, two or one of a workgroup's waves, and round
+    again where there are more; strips of 512 tokens are used again."""
+    _paged(aq, [700, 1, 0, 1333], 4, heads, 64, G and 32, bits, 16, 1, "f16", seed=heads, window=1200)
+    _paged(aq, [577, 90], 9, heads, 128, G, bits, 48, 5, "bf16", seed=heads + 1, softcap=20.0, slopes=True)
+
+
+def test_many_tokens_of_many_key_heads(aq):
+    """Chunks of one sequence over the whole chip."""
+    _paged(aq, [20011], 2, 5, 64, 64, 8, 64, 1, "f16", seed=71)
+    _paged(aq, [9001, 12000], 3, 8, 64, 32, 4, 16, 2, "f16", seed=72, first=[17, 2300])
+
+
+# ---- rows past 31 bits ------------------------------------------------------------------
+@pytest.fixture(scope="module")
+def vast():
+    """One array for keys and values (4 bits, 69 GB of codes) of more than 2^31 rows."""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 77 GB of device memory")
+    H, D, G, page = 8, 64, 64, 64
+    pages = (1 << 31) // (H * page) + 9
+    part = [torch.empty((pages, H, page, D // 8), dtype=torch.int32, device="cuda")]
+    part += [torch.empty((pages, H, page, 1), dtype=torch.float16, device="cuda") for _ in range(2)]
+    yield part, pages, H, D, G, page
+    part.clear()
+    torch.cuda.empty_cache()
+
+
+def test_turned_keys_of_more_rows_than_31_bits(aq, vast):
+    import torch
+    part, pages, H, D, G, page = vast
+    T, ids = 150, torch.tensor([pages - 1, 3, pages - 3], device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(81)
+    k = torch.randn((T, H, D), generator=gen, device="cuda").half()
+    positions = torch.randint(0, 1 << 20, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    freqs, _ = aq.aq_rope_frequencies(D)
+    t = torch.arange(T, device="cuda")
+    small = kv_ref.Cache(3, H, page, D, G, 4).device()
+    turned = aq.aq_rope(None, k, positions, freqs)[1]
+    aq.aq_kv_append(turned, turned, t, *small, G, 4)
+    # keys turned and values that are the same rows: both writes leave the same bits
+    far = ids[t // page] * page + t % page
+    out = torch.empty_like(k)
+    aq.aq_rope_append(None, k, turned, positions, freqs, far, *part, *part, G, 4, k_out=out)
+    assert torch.equal(out, turned)
+    at = (t // page, slice(None), t % page)
+    for x, y in zip(part, small):
+        assert torch.equal(x[ids][at].view(torch.int16), y[at].view(torch.int16))
+
+
+def test_rows_that_move_past_31_bits(aq, vast):
+    import torch
+    part, pages, H, D, G, page = vast
+    old = torch.tensor([[pages - 1, 2, pages - 4], [pages - 2, pages - 6, 5]], dtype=torch.int32, device="cuda")
+    new = torch.tensor([[7, pages - 7], [pages - 8, 9]], dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(82)
+    for x in part:
+        y = torch.randint(-2 ** 15, 2 ** 15, (6, *x.shape[1:]), generator=gen, device="cuda")
+        x[old.flatten().long()] = y.to(torch.int16).view(torch.float16) if x.dtype == torch.float16 else y.int()
+    weights = torch.rand((2, 3 * page), generator=gen, device="cuda")
+    lengths = torch.tensor([3 * page - 1, 2 * page + 5], dtype=torch.int32, device="cuda")
+    kept, _, _ = aq.aq_kv_evict(weights, lengths, old, new, *part, *part, G, 4, keep=100, sinks=3, recent=9)
+    to = torch.arange(100, device="cuda")
+    for b in range(2):
+        at = kept[b].long()
+        for x in part:
+            moved = x[new[b].long()][to // page, :, to % page]
+            assert torch.equal(moved.view(torch.int16), x[old[b].long()][at // page, :, at % page].view(torch.int16))
+
+
+# ---- scores that are not finite ---------------------------------------------------------
+def test_infinite_scores(aq):
+    """A score of +inf leaves no sum: the rows that see it are NaN, their
+    logarithms too, and no others; -inf is a weight of 0; a cap bounds both."""
+    import torch
+    n, dim = 90, 64
+    gen = torch.Generator(device="cuda").manual_seed(91)
+    q, k, v = (torch.randn((n, 1, dim), generator=gen, device="cuda").half() for _ in range(3))
+    k[40, 0, 7] = np.inf
+    q[:, 0, 7] = 1.0
+    st = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    pages = torch.arange(6, dtype=torch.int32, device="cuda")[None]
+    cache = kv_ref.Cache(6, 1, 16, dim, 32, 16, "f16").device()
+    aq.aq_kv_append(k, v, torch.arange(n, device="cuda"), *cache, 32, 16)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+
+    def both(q, **more):
+        out, lse = aq.aq_prompt_attention(q, k, v, st, st, return_lse=True, **more)
+        one = aq.aq_paged_attention_masked(q[None, -3:], *cache, pages, lens, 32, 16, return_lse=True, **more)
+        return out, lse, *one
+
+    out, lse, o1, l1 = both(q)
+    sees = torch.arange(n, device="cuda") >= 40
+    assert out[sees].isnan().all() and out[~sees].isfinite().all() and o1.isnan().all()
+    assert lse[sees].isnan().all() and lse[~sees].isfinite().all() and l1.isnan().all()
+    q[:, 0, 7] = -1.0
+    got = both(q)
+    assert all(x.isfinite().all() for x in got)
+    w = torch.zeros((1, 96), device="cuda")
+    aq.aq_kv_weigh(q[None, -3:], got[3], *cache, pages, lens, w, 32, 16)
+    assert w[0, 40] == 0 and abs(float(w.sum()) - 3) < 1e-4
+    for sign in (1.0, -1.0):
+        q[:, 0, 7] = sign
+        assert all(x.isfinite().all() for x in both(q, softcap=5.0))
