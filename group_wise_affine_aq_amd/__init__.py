@@ -928,7 +928,8 @@ def aq_kv_weigh(q, lse, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases
                 slopes=None, window: int = 0, first=None, stream=None):
     """Adds to weights (fp32 [B, tokens]) what each cached token gets of the attention of q, [B, L,
     q_heads, head_dim] or [B, q_heads, head_dim]: the sum over rows and heads of exp(score - lse), lse
-    and the other arguments those of aq_paged_attention_masked for the same queries."""
+    and the other arguments those of aq_paged_attention_masked for the same queries.  Rows of weights
+    are a multiple of 4 long; tokens past their end are left out."""
     lib = load_library()
     cache, _, dim = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
     torch = _torch_module
@@ -956,7 +957,9 @@ def aq_kv_evict(weights, lengths, page_table, new_table, k_codes, k_scales, k_bi
     """Every sequence back to at most `keep` tokens: its first `sinks`, its last `recent` and those
     between with the largest weights (fp32 [B, tokens]), in their order, copied to the pages of
     new_table (int32 [B, pages], other pages than page_table's) -> (kept int32 [B, keep]: the
-    positions they had, -1 behind the last; new lengths int32 [B]; their weights fp32 [B, keep])."""
+    positions they had, -1 behind the last; new lengths int32 [B]; their weights fp32 [B, keep]).
+    Windows, slopes and first of later calls count the new places, not the positions they had;
+    the weights go on in rows with room for the tokens to come."""
     lib = load_library()
     cache, _, _ = _kv_cache(k_codes, k_scales, k_biases, v_codes, v_scales, v_biases, group_size, bits)
     torch = _torch_module

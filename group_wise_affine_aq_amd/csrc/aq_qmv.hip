@@ -866,8 +866,8 @@ template <> struct stream_shape<8> { static constexpr int R = 4, D = 2; };
 // wave, W waves per workgroup, SL staging loads of scales (and of biases) per
 // lane and row, and at most WPC workgroups per CU (0: as many as fit).
 // Measured on the MI355X (4-bit, cold weights; µs): at K = 4096 fewer waves
-// than fit run faster -- 14336 rows: 4-wave workgroups, 3 per CU (3072
-// waves) 7.88 .. 8.07, against 8.31 .. 8.42 with 6144 waves (8-wave
+// than fit run faster -- 14336 rows: 4-wave workgroups, 3 per CU (12 waves
+// a CU) 7.88 .. 8.07, against 8.31 .. 8.42 with 6144 waves (8-wave
 // workgroups, all that fit) and 8.05 .. 8.21 with 4096; 4096 rows: one
 // 16-wave workgroup per CU, a row per wave, 4.08 .. 4.12, against
 // 4.38 .. 4.51 with 2 rows in flight per wave on 8-wave workgroups;

@@ -16,7 +16,10 @@
 // go to the cache's quantizer (aq_kv.hpp) through LDS, neighbouring tokens of one head
 // together, which mostly lie in one run of the cache.
 //
-// Bound: HBM at prompt size, launch latency at decode size.
+// Bound: HBM at prompt size, launch latency at decode size.  8191 tokens of 32 + 8
+// heads of 128: rows alone 168 MB in 33 us (5.1 TB/s), written at 4 bits 178 MB in
+// 39 us (4.6 TB/s).  64 tokens: rows alone 2.9 us; written at 8 bits 6.9, where the
+// quantizer, two rounds of 32 of the 256 threads, waits for the angles.
 #include "aq_kv.hpp"
 
 namespace aq {

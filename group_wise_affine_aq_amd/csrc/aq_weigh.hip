@@ -14,7 +14,11 @@
 // Tokens are cut evenly over the chip in chunks, as in the attention, by the
 // lengths on the device.
 //
-// Bound: HBM, the keys' codes, scales and biases read once.
+// Bound: neither HBM nor vector instructions are full, the waves of a CU (two a
+// SIMD) wait in turn.  131072 tokens of 8 key heads of 128 at 4 bits, 32 rows
+// each: 30 us, 12 of bytes at 6.2 TB/s and 16 of vector instructions at 2.4 GHz;
+// 16 sequences of up to 4096 tokens at 8 bits, 4 rows: 17 us, 6 of bytes and 4 of
+// instructions, the rest first loads that wait for each other.
 #include "aq_attn.hpp"
 
 namespace aq {
@@ -169,8 +173,8 @@ __global__ __launch_bounds__(64 * WV, 2) void weigh_kernel(Params p, float *weig
             };
             auto weight = [&](int nt, int j) { return exp2_fast(t[nt][j] - lse[nt]); };
             // (one tile of columns mostly has idle ones, and a branch costs it more than the choices: 16
-            // sequences of up to 4096 tokens 17.9 us against 17.0; two tiles without idle ones 32.6 against
-            // 33.9, 131072 tokens; both with the copy of the weights)
+            // sequences of up to 4096 tokens 17.9 us against 17.0; two tiles without idle ones 32.9 against
+            // 33.9, 131072 tokens; both with a copy of the weights)
             if (NT == 1 || edge || some_idle)
               gather([&](int nt, int j) { return idle[nt] || t[nt][j] == kNegInf ? 0.f : weight(nt, j); });
             else

@@ -491,7 +491,8 @@ int64_t aq_paged_attention_workspace(int64_t B, int L, int q_heads, int kv_heads
  *
  * What a row does not see has no part in it, whatever it holds (infinite and
  * NaN values too).  A row that sees no token is zero.  lse, where it is given,
- * gets log(sum_t exp(s_t)) of each row, -inf for a row that sees no token.
+ * gets log(sum_t exp(s_t)) of each row, -inf for a row that sees no token.  A
+ * row that sees a score of +inf or NaN is NaN, and so is its lse.
  *
  * softcap: 0, or from 1e-30 to 1e30.  window >= 0.  slopes: device float
  * [q_heads].  All pointers are device memory, 16-byte aligned. */
@@ -640,7 +641,8 @@ aq_status aq_rope_frequencies(int rotary, double base, aq_rope_stretch kind, dou
  * queries, and is required; a row whose lse is -inf adds nothing.  weights:
  * device float, sequence b's at weights + b * weights_stride, weights_stride a
  * multiple of 4.  Only the keys of the cache are read.  The sums are binary32,
- * in an order that does not depend on timing. */
+ * in an order that does not depend on timing.  AQ_ERR_UNSUPPORTED for B *
+ * max_pages * page_size / 128 >= 2^31, beside what aq_paged_attention refuses. */
 aq_status aq_kv_weigh(const void *q, aq_dtype x_dtype, int64_t B, int L, int q_heads,
                       int64_t q_stride, const aq_kv_cache *cache, const int32_t *page_table,
                       int64_t max_pages, const int32_t *lengths, float scale,
@@ -656,6 +658,15 @@ aq_status aq_kv_weigh(const void *q, aq_dtype x_dtype, int64_t B, int L, int q_h
  * are copied there as they are.  Outputs: kept int32 [B, keep], the positions
  * they had, -1 behind the last; new_weights float [B, keep], their weights, 0
  * behind the last; new_lengths int32 [B].
+ *
+ * A kept token is from then on the token of its new place: `first`, windows and
+ * slopes of aq_paged_attention_masked and aq_kv_weigh count places, so distances
+ * shrink by what was evicted between, and a caller's `first` has to be moved by
+ * `kept`.  Rotary positions are in the keys and stay.  A model whose slopes or
+ * windows are to mean the conversation's distances is not served by eviction.
+ * new_weights has rows of `keep`; aq_kv_weigh goes on in rows that have room for
+ * the tokens to come (weights past a row's end are not gathered, and tokens past
+ * it are not kept by the next eviction).
  *
  * The pages of new_table are to be other pages than those of page_table, since
  * a page may be shared by sequences and tokens move at once; the caller frees
